@@ -1,0 +1,295 @@
+"""Python binding of the layer's operators (include/block.h in libroute.so):
+layer norm, the gated feed-forward product and the linear product with bias,
+activation and residual, each forward and backward. Argument marshalling only.
+
+Like the route's binding: every function checks types, shapes and placement,
+then calls the C entry point of the same operator; a non-zero status raises
+RouteError and there is no fallback. Matrices of rows may have any row stride
+(`t.stride(0)`), weights are contiguous [K][N].
+"""
+from __future__ import annotations
+
+import ctypes
+
+import torch
+
+from .route import LIB, OK, RouteError, _stream
+
+ABI_VERSION = 1
+MAX_ROWS = 1 << 20
+MAX_SIZE = 1 << 17
+MAX_STRIDE = 1 << 20
+
+DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+SYMBOLS = tuple(f"block_{op}{call}" for op in ("norm", "gated", "linear")
+                for call in ("_prepare", "_workspace_bytes", "", "_backward", "_destroy"))
+
+
+class NormConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("device", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("width", ctypes.c_int32), ("dtype", ctypes.c_int32), ("param_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class GatedConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("device", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("inputs", ctypes.c_int32), ("inner", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("training", ctypes.c_int32)]
+
+
+class LinearConfig(ctypes.Structure):
+    _fields_ = [("abi_version", ctypes.c_uint32), ("device", ctypes.c_int32), ("rows", ctypes.c_int32),
+                ("inputs", ctypes.c_int32), ("outputs", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("activation", ctypes.c_int32), ("training", ctypes.c_int32)]
+
+
+def _declare() -> None:
+    p, i32, i64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
+    mat = [p, i64]  # a matrix of rows and its stride
+    args = {
+        "block_norm": [p, *mat, p, p, *mat, p, p, i32, p],
+        "block_norm_backward": [p, *mat, *mat, p, p, p, *mat, p, p, p, i32, p],
+        "block_gated": [p, *mat, p, p, *mat, p, p, p, i32, p],
+        "block_gated_backward": [p, *mat, *mat, p, p, p, p, *mat, p, p, p, i32, p],
+        "block_linear": [p, *mat, p, p, *mat, *mat, p, p, i32, p],
+        "block_linear_backward": [p, *mat, *mat, p, p, *mat, p, p, p, i32, p],
+    }
+    for name, types in args.items():
+        fn = getattr(LIB, name)
+        fn.argtypes, fn.restype = types, ctypes.c_int
+    for op, config in (("norm", NormConfig), ("gated", GatedConfig), ("linear", LinearConfig)):
+        fn = getattr(LIB, f"block_{op}_prepare")
+        fn.argtypes, fn.restype = [ctypes.POINTER(config), ctypes.POINTER(ctypes.c_void_p)], ctypes.c_int
+        fn = getattr(LIB, f"block_{op}_workspace_bytes")
+        fn.argtypes, fn.restype = [p], ctypes.c_size_t
+        fn = getattr(LIB, f"block_{op}_destroy")
+        fn.argtypes, fn.restype = [p], None
+
+
+_declare()
+
+
+def prepare_raw(op: str, cfg) -> tuple[int, int]:
+    """Call block_<op>_prepare; returns (status, plan handle or 0). cfg may be None."""
+    out = ctypes.c_void_p(0)
+    st = getattr(LIB, f"block_{op}_prepare")(ctypes.byref(cfg) if cfg is not None else None,
+                                             ctypes.byref(out))
+    return st, (out.value or 0)
+
+
+def _code(table, key, what: str) -> int:
+    if key not in table:
+        raise ValueError(f"{what}: expected one of {list(table)}, got {key!r}")
+    return table[key]
+
+
+class _Plan:
+    """A prepared plan (owns the C plan; freed on close/GC)."""
+
+    OP = ""
+
+    def _prepare(self, cfg) -> None:
+        st, handle = prepare_raw(self.OP, cfg)
+        if st != OK:
+            raise RouteError(st, f"block_{self.OP}_prepare")
+        self.handle = handle
+        self.rows = cfg.rows
+        self.device = cfg.device
+        self.workspace_bytes = int(getattr(LIB, f"block_{self.OP}_workspace_bytes")(handle))
+
+    def new_workspace(self) -> torch.Tensor:
+        """A zero-filled workspace tensor of the size this plan needs."""
+        return torch.zeros(max(self.workspace_bytes, 256), dtype=torch.uint8, device=f"cuda:{self.device}")
+
+    def close(self) -> None:
+        if getattr(self, "handle", 0):
+            getattr(LIB, f"block_{self.OP}_destroy")(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _device(device) -> int:
+    return torch.cuda.current_device() if device is None else int(device)
+
+
+class NormPlan(_Plan):
+    """Layer norm of up to `rows` rows of `width` values."""
+
+    OP = "norm"
+
+    def __init__(self, rows: int, width: int, dtype=torch.bfloat16, param_dtype=torch.float32,
+                 eps: float = 1e-5, device: int | None = None):
+        self.width, self.dtype, self.param_dtype = width, dtype, param_dtype
+        self._prepare(NormConfig(ABI_VERSION, _device(device), rows, width, _code(DTYPES, dtype, "dtype"),
+                                 _code(DTYPES, param_dtype, "param_dtype"), eps))
+
+
+class GatedPlan(_Plan):
+    """h = act(x w_gate) * (x w_up) of up to `rows` rows; `training` sizes the
+    workspace for the backward call as well."""
+
+    OP = "gated"
+
+    def __init__(self, rows: int, inputs: int, inner: int, activation: str = "silu", dtype=torch.bfloat16,
+                 training: bool = False, device: int | None = None):
+        self.inputs, self.inner, self.dtype, self.activation = inputs, inner, dtype, activation
+        self.training = bool(training)
+        self._prepare(GatedConfig(ABI_VERSION, _device(device), rows, inputs, inner,
+                                  _code(DTYPES, dtype, "dtype"), _code(ACTIVATIONS, activation, "activation"),
+                                  int(self.training)))
+
+
+class LinearPlan(_Plan):
+    """y = act(x w + bias) + residual of up to `rows` rows; `training` sizes
+    the workspace for the backward call as well."""
+
+    OP = "linear"
+
+    def __init__(self, rows: int, inputs: int, outputs: int, activation: str = "none", dtype=torch.bfloat16,
+                 training: bool = False, device: int | None = None):
+        self.inputs, self.outputs, self.dtype, self.activation = inputs, outputs, dtype, activation
+        self.training = bool(training)
+        self._prepare(LinearConfig(ABI_VERSION, _device(device), rows, inputs, outputs,
+                                   _code(DTYPES, dtype, "dtype"),
+                                   _code(ACTIVATIONS, activation, "activation"), int(self.training)))
+
+
+def _check(t: torch.Tensor, dtype, plan: _Plan, name: str) -> None:
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a device tensor")
+    if t.device.index != plan.device:
+        raise ValueError(f"{name}: on cuda:{t.device.index}, the plan is for cuda:{plan.device}")
+
+
+def _rows_of(t, dtype, plan: _Plan, rows: int, width: int, name: str) -> tuple[int | None, int]:
+    """Pointer and row stride of a matrix of rows; None gives (NULL, width)."""
+    if t is None:
+        return None, width
+    _check(t, dtype, plan, name)
+    if t.dim() != 2 or t.shape[1] != width:
+        raise ValueError(f"{name}: expected [rows][{width}], got {tuple(t.shape)}")
+    if t.shape[0] < rows:
+        raise ValueError(f"{name}: needs at least {rows} rows, has {t.shape[0]}")
+    if width > 1 and rows > 0 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the values of a row must be adjacent")
+    # the stride of a single row is never used
+    if rows > 1 and t.stride(0) < width:
+        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)}, width {width})")
+    return t.data_ptr() or None, (t.stride(0) if rows > 1 else width)
+
+
+def _dense(t, dtype, plan: _Plan, shape, name: str) -> int | None:
+    """Pointer of a contiguous tensor; its first dimension may be longer when
+    the shape has two (spare rows)."""
+    if t is None:
+        return None
+    _check(t, dtype, plan, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t.data_ptr() or None
+
+
+def _per_row(t, dtype, plan: _Plan, shape, name: str) -> int | None:
+    """Like _dense for outputs kept per row: spare rows at the end are allowed."""
+    if t is not None and t.dim() == len(shape) and t.shape[0] > shape[0]:
+        t = t[:shape[0]]
+    return _dense(t, dtype, plan, shape, name)
+
+
+def _workspace(plan: _Plan, workspace) -> int:
+    _check(workspace, torch.uint8, plan, "workspace")
+    if not workspace.is_contiguous() or workspace.numel() < max(plan.workspace_bytes, 256):
+        raise ValueError(f"workspace: needs {max(plan.workspace_bytes, 256)} contiguous bytes")
+    return workspace.data_ptr()
+
+
+def _run(name: str, plan: _Plan, *args) -> None:
+    st = getattr(LIB, name)(plan.handle, *args)
+    if st != OK:
+        raise RouteError(st, name)
+
+
+def layer_norm(plan: NormPlan, x, weight, bias, y, mean=None, rstd=None, rows: int | None = None,
+               stream=None) -> None:
+    """y = (x - mean) * rstd * weight + bias; weight and bias may be None; mean
+    and rstd (FP32, one per row) are kept for layer_norm_backward if given."""
+    rows = x.shape[0] if rows is None else rows
+    dt, pdt, w = plan.dtype, plan.param_dtype, plan.width
+    _run("block_norm", plan, *_rows_of(x, dt, plan, rows, w, "x"),
+         _dense(weight, pdt, plan, (w,), "weight"), _dense(bias, pdt, plan, (w,), "bias"),
+         *_rows_of(y, dt, plan, rows, w, "y"), _per_row(mean, torch.float32, plan, (rows,), "mean"),
+         _per_row(rstd, torch.float32, plan, (rows,), "rstd"), rows, _stream(stream))
+
+
+def layer_norm_backward(plan: NormPlan, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace,
+                        rows: int | None = None, stream=None) -> None:
+    """Gradients of layer_norm; dx, dweight or dbias None is not computed."""
+    rows = dy.shape[0] if rows is None else rows
+    dt, pdt, w = plan.dtype, plan.param_dtype, plan.width
+    _run("block_norm_backward", plan, *_rows_of(dy, dt, plan, rows, w, "dy"),
+         *_rows_of(x, dt, plan, rows, w, "x"), _dense(weight, pdt, plan, (w,), "weight"),
+         _per_row(mean, torch.float32, plan, (rows,), "mean"),
+         _per_row(rstd, torch.float32, plan, (rows,), "rstd"), *_rows_of(dx, dt, plan, rows, w, "dx"),
+         _dense(dweight, pdt, plan, (w,), "dweight"), _dense(dbias, pdt, plan, (w,), "dbias"),
+         _workspace(plan, workspace), rows, _stream(stream))
+
+
+def gated(plan: GatedPlan, x, w_gate, w_up, h, workspace, d_gate=None, d_up=None, rows: int | None = None,
+          stream=None) -> None:
+    """h = act(x w_gate) * (x w_up). For training, d_gate and d_up receive the
+    derivatives of h by the two products, for gated_backward."""
+    rows = x.shape[0] if rows is None else rows
+    dt, k, n = plan.dtype, plan.inputs, plan.inner
+    _run("block_gated", plan, *_rows_of(x, dt, plan, rows, k, "x"),
+         _dense(w_gate, dt, plan, (k, n), "w_gate"), _dense(w_up, dt, plan, (k, n), "w_up"),
+         *_rows_of(h, dt, plan, rows, n, "h"), _per_row(d_gate, dt, plan, (rows, n), "d_gate"),
+         _per_row(d_up, dt, plan, (rows, n), "d_up"), _workspace(plan, workspace), rows, _stream(stream))
+
+
+def gated_backward(plan: GatedPlan, dh, x, w_gate, w_up, d_gate, d_up, dx, dw_gate, dw_up, workspace,
+                   rows: int | None = None, stream=None) -> None:
+    """Gradients of gated; dx None, or dw_gate and dw_up None, is not computed."""
+    rows = dh.shape[0] if rows is None else rows
+    dt, k, n = plan.dtype, plan.inputs, plan.inner
+    _run("block_gated_backward", plan, *_rows_of(dh, dt, plan, rows, n, "dh"),
+         *_rows_of(x, dt, plan, rows, k, "x"), _dense(w_gate, dt, plan, (k, n), "w_gate"),
+         _dense(w_up, dt, plan, (k, n), "w_up"), _per_row(d_gate, dt, plan, (rows, n), "d_gate"),
+         _per_row(d_up, dt, plan, (rows, n), "d_up"), *_rows_of(dx, dt, plan, rows, k, "dx"),
+         _dense(dw_gate, dt, plan, (k, n), "dw_gate"), _dense(dw_up, dt, plan, (k, n), "dw_up"),
+         _workspace(plan, workspace), rows, _stream(stream))
+
+
+def linear(plan: LinearPlan, x, w, y, workspace, bias=None, residual=None, slope=None,
+           rows: int | None = None, stream=None) -> None:
+    """y = act(x w + bias) + residual; `residual` may be `y` itself. For
+    training with an activation, `slope` receives act' for linear_backward."""
+    rows = x.shape[0] if rows is None else rows
+    dt, k, n = plan.dtype, plan.inputs, plan.outputs
+    _run("block_linear", plan, *_rows_of(x, dt, plan, rows, k, "x"), _dense(w, dt, plan, (k, n), "w"),
+         _dense(bias, dt, plan, (n,), "bias"), *_rows_of(residual, dt, plan, rows, n, "residual"),
+         *_rows_of(y, dt, plan, rows, n, "y"), _per_row(slope, dt, plan, (rows, n), "slope"),
+         _workspace(plan, workspace), rows, _stream(stream))
+
+
+def linear_backward(plan: LinearPlan, dy, x, w, slope, dx, dw, dbias, workspace, rows: int | None = None,
+                    stream=None) -> None:
+    """Gradients of linear (the residual's is dy itself); dx, dw or dbias None
+    is not computed. `slope` is None when the plan has no activation."""
+    rows = dy.shape[0] if rows is None else rows
+    dt, k, n = plan.dtype, plan.inputs, plan.outputs
+    _run("block_linear_backward", plan, *_rows_of(dy, dt, plan, rows, n, "dy"),
+         *_rows_of(x, dt, plan, rows, k, "x"), _dense(w, dt, plan, (k, n), "w"),
+         _per_row(slope, dt, plan, (rows, n), "slope"), *_rows_of(dx, dt, plan, rows, k, "dx"),
+         _dense(dw, dt, plan, (k, n), "dw"), _dense(dbias, dt, plan, (n,), "dbias"),
+         _workspace(plan, workspace), rows, _stream(stream))

@@ -19,8 +19,9 @@ LIB_PATH = os.path.join(HERE, "libroute.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hip", "prefill_gemm.hip"]
-HEADERS = ["route_device.h", "route_launch.h"]
+SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hip", "prefill_gemm.hip",
+           "block_api.cpp", "norm.hip", "block_gemm.hip"]
+HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",

@@ -1,0 +1,397 @@
+// C ABI of the layer's operators (block.h): plan preparation, argument checks
+// and launches. Every check runs before any launch; nothing allocates device
+// memory or synchronises.
+#include "block.h"
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstring>
+#include <new>
+
+#include "block_launch.h"
+
+struct block_norm_plan {
+  block_norm_config cfg;
+  size_t ws_bytes;
+};
+
+// Workspace of the matrix operators: [0, off_dz) the products' counters and
+// partial sums; then dz (linear) or dg and du (gated) with their rows padded
+// to a multiple of 8 elements, and the partial column sums of dbias.
+struct block_gated_plan {
+  block_gated_config cfg;
+  size_t off_dz, off_du, ws_bytes;
+};
+
+struct block_linear_plan {
+  block_linear_config cfg;
+  size_t off_dz, off_sum, ws_bytes;
+};
+
+namespace {
+
+using block::GemmArgs;
+
+bool misaligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
+size_t round256(size_t n) { return (n + 255) & ~size_t(255); }
+size_t dtype_size(int dtype) { return dtype == BLOCK_F32 ? 4 : 2; }
+int64_t padded(int n) { return (n + 7) & ~int64_t(7); }
+bool bad_size(int32_t n) { return n < 1 || n > BLOCK_MAX_SIZE; }
+bool bad_rows(int32_t n) { return n < 1 || n > BLOCK_MAX_ROWS; }
+bool bad_stride(int64_t s, int64_t width) { return s < width || s > BLOCK_MAX_STRIDE; }
+int status_of(hipError_t e) { return e == hipSuccess ? ROUTE_OK : ROUTE_E_HIP; }
+
+int find_device(int32_t device) {
+  int count = 0;
+  if (device < 0 || hipGetDeviceCount(&count) != hipSuccess || device >= count) return ROUTE_E_DEVICE;
+  hipDeviceProp_t prop;
+  if (hipGetDeviceProperties(&prop, device) != hipSuccess) return ROUTE_E_DEVICE;
+  return std::strncmp(prop.gcnArchName, "gfx950", 6) == 0 ? ROUTE_OK : ROUTE_E_DEVICE;
+}
+
+int check_current(int32_t device) {
+  int cur = -1;
+  return hipGetDevice(&cur) == hipSuccess && cur == device ? ROUTE_OK : ROUTE_E_DEVICE;
+}
+
+template <typename Plan, typename Config>
+Plan* new_plan(const Config& cfg) {
+  Plan* p = new (std::nothrow) Plan();
+  if (p != nullptr) p->cfg = cfg;
+  return p;
+}
+
+}  // namespace
+
+extern "C" {
+
+// ------------------------------------------------------------------- norm --
+
+int block_norm_prepare(const block_norm_config* cfg, block_norm_plan** out) {
+  if (out == nullptr) return ROUTE_E_ARG;
+  *out = nullptr;
+  if (cfg == nullptr || cfg->abi_version != BLOCK_ABI_VERSION) return ROUTE_E_ARG;
+  if (cfg->dtype < BLOCK_BF16 || cfg->dtype > BLOCK_F32 || cfg->param_dtype < BLOCK_BF16 ||
+      cfg->param_dtype > BLOCK_F32 || !std::isfinite(cfg->eps) || !(cfg->eps > 0.f))
+    return ROUTE_E_ARG;
+  if (bad_size(cfg->width)) return ROUTE_E_SHAPE;
+  if (bad_rows(cfg->rows)) return ROUTE_E_ROWS;
+  if (int st = find_device(cfg->device)) return st;
+  block_norm_plan* p = new_plan<block_norm_plan>(*cfg);
+  if (p == nullptr) return ROUTE_E_ARG;
+  p->ws_bytes = round256(block::norm_backward_bytes(cfg->rows, cfg->width));
+  *out = p;
+  return ROUTE_OK;
+}
+
+size_t block_norm_workspace_bytes(const block_norm_plan* plan) { return plan ? plan->ws_bytes : 0; }
+
+int block_norm(const block_norm_plan* plan, const void* x, int64_t x_stride, const void* weight,
+               const void* bias, void* y, int64_t y_stride, float* mean, float* rstd, int32_t rows,
+               void* stream) {
+  if (!plan || (mean == nullptr) != (rstd == nullptr)) return ROUTE_E_ARG;
+  if (rows != 0 && (!x || !y)) return ROUTE_E_ARG;
+  const block_norm_config& c = plan->cfg;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(x_stride, c.width) || bad_stride(y_stride, c.width)) return ROUTE_E_SHAPE;
+  const size_t e = dtype_size(c.dtype), pe = dtype_size(c.param_dtype);
+  if (misaligned(x, e) || misaligned(y, e) || misaligned(weight, pe) || misaligned(bias, pe) ||
+      misaligned(mean, 4) || misaligned(rstd, 4))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  if (rows == 0) return ROUTE_OK;
+  block::NormArgs a{};
+  a.x = x;
+  a.ldx = x_stride;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.ldy = y_stride;
+  a.mean = mean;
+  a.rstd = rstd;
+  a.rows = rows;
+  a.width = c.width;
+  a.param_dtype = c.param_dtype;
+  a.eps = c.eps;
+  return status_of(block::launch_norm(c.dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+int block_norm_backward(const block_norm_plan* plan, const void* dy, int64_t dy_stride, const void* x,
+                        int64_t x_stride, const void* weight, const float* mean, const float* rstd,
+                        void* dx, int64_t dx_stride, void* dweight, void* dbias, void* workspace,
+                        int32_t rows, void* stream) {
+  if (!plan || !workspace || (!dx && !dweight && !dbias)) return ROUTE_E_ARG;
+  if (rows != 0 && (!dy || !x || !mean || !rstd)) return ROUTE_E_ARG;
+  const block_norm_config& c = plan->cfg;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(dy_stride, c.width) || bad_stride(x_stride, c.width) ||
+      (dx != nullptr && bad_stride(dx_stride, c.width)))
+    return ROUTE_E_SHAPE;
+  const size_t e = dtype_size(c.dtype), pe = dtype_size(c.param_dtype);
+  if (misaligned(dy, e) || misaligned(x, e) || misaligned(dx, e) || misaligned(weight, pe) ||
+      misaligned(dweight, pe) || misaligned(dbias, pe) || misaligned(mean, 4) || misaligned(rstd, 4) ||
+      misaligned(workspace, 256))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  if (rows == 0 && !dweight && !dbias) return ROUTE_OK;
+  block::NormArgs a{};
+  a.x = x;
+  a.ldx = x_stride;
+  a.dy = dy;
+  a.lddy = dy_stride;
+  a.weight = weight;
+  a.dx = dx;
+  a.lddx = dx_stride;
+  a.dweight = dweight;
+  a.dbias = dbias;
+  a.mean = const_cast<float*>(mean);
+  a.rstd = const_cast<float*>(rstd);
+  a.partial = static_cast<float*>(workspace);
+  a.rows = rows;
+  a.width = c.width;
+  a.param_dtype = c.param_dtype;
+  return status_of(block::launch_norm_backward(c.dtype, a, static_cast<hipStream_t>(stream)));
+}
+
+void block_norm_destroy(block_norm_plan* plan) { delete plan; }
+
+// ------------------------------------------------------------------ gated --
+
+int block_gated_prepare(const block_gated_config* cfg, block_gated_plan** out) {
+  if (out == nullptr) return ROUTE_E_ARG;
+  *out = nullptr;
+  if (cfg == nullptr || cfg->abi_version != BLOCK_ABI_VERSION) return ROUTE_E_ARG;
+  if ((cfg->dtype != BLOCK_BF16 && cfg->dtype != BLOCK_F16) || cfg->activation <= BLOCK_ACT_NONE ||
+      cfg->activation > BLOCK_ACT_GELU_TANH)
+    return ROUTE_E_ARG;
+  if (bad_size(cfg->inputs) || bad_size(cfg->inner)) return ROUTE_E_SHAPE;
+  if (bad_rows(cfg->rows)) return ROUTE_E_ROWS;
+  if (int st = find_device(cfg->device)) return st;
+  block_gated_plan* p = new_plan<block_gated_plan>(*cfg);
+  if (p == nullptr) return ROUTE_E_ARG;
+  const size_t dz = cfg->training ? round256((size_t)cfg->rows * padded(cfg->inner) * 2) : 0;
+  p->off_dz = 0;
+  p->off_du = p->off_dz + dz;
+  p->ws_bytes = p->off_du + dz;
+  *out = p;
+  return ROUTE_OK;
+}
+
+size_t block_gated_workspace_bytes(const block_gated_plan* plan) { return plan ? plan->ws_bytes : 0; }
+
+int block_gated(const block_gated_plan* plan, const void* x, int64_t x_stride, const void* w_gate,
+                const void* w_up, void* h, int64_t h_stride, void* d_gate, void* d_up, void* workspace,
+                int32_t rows, void* stream) {
+  if (!plan || !w_gate || !w_up || !workspace) return ROUTE_E_ARG;
+  if (rows != 0 && (!x || !h || (d_gate == nullptr) != (d_up == nullptr))) return ROUTE_E_ARG;
+  const block_gated_config& c = plan->cfg;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(x_stride, c.inputs) || bad_stride(h_stride, c.inner)) return ROUTE_E_SHAPE;
+  if (misaligned(x, 2) || misaligned(w_gate, 2) || misaligned(w_up, 2) || misaligned(h, 2) ||
+      misaligned(d_gate, 2) || misaligned(d_up, 2) || misaligned(workspace, 256))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  if (rows == 0) return ROUTE_OK;
+  GemmArgs a{};
+  a.a[0] = x;
+  a.lda = x_stride;
+  a.b[0] = w_gate;
+  a.b[1] = w_up;
+  a.ldb = c.inner;
+  a.c[0] = h;
+  a.ldc = h_stride;
+  a.saved[0] = d_gate;
+  a.saved[1] = d_up;
+  a.m = rows;
+  a.n = c.inner;
+  a.red = c.inputs;
+  a.segments = a.outputs = 1;
+  a.act = c.activation;
+  return status_of(block::launch_gemm(c.dtype, block::kGated, a, static_cast<hipStream_t>(stream)));
+}
+
+int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t dh_stride, const void* x,
+                         int64_t x_stride, const void* w_gate, const void* w_up, const void* d_gate,
+                         const void* d_up, void* dx, int64_t dx_stride, void* dw_gate, void* dw_up,
+                         void* workspace, int32_t rows, void* stream) {
+  if (!plan || !w_gate || !w_up || !workspace || !plan->cfg.training) return ROUTE_E_ARG;
+  if ((dw_gate == nullptr) != (dw_up == nullptr)) return ROUTE_E_ARG;
+  if (rows != 0 && (!dh || !x || !d_gate || !d_up || (!dx && !dw_gate))) return ROUTE_E_ARG;
+  const block_gated_config& c = plan->cfg;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(dh_stride, c.inner) || bad_stride(x_stride, c.inputs) ||
+      (dx != nullptr && bad_stride(dx_stride, c.inputs)))
+    return ROUTE_E_SHAPE;
+  if (misaligned(dh, 2) || misaligned(x, 2) || misaligned(w_gate, 2) || misaligned(w_up, 2) ||
+      misaligned(d_gate, 2) || misaligned(d_up, 2) || misaligned(dx, 2) || misaligned(dw_gate, 2) ||
+      misaligned(dw_up, 2) || misaligned(workspace, 256))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  void* dz[2] = {ws + plan->off_dz, ws + plan->off_du};
+  const void* slopes[2] = {d_gate, d_up};
+  int st = status_of(block::launch_scale(c.dtype, dh, dh_stride, slopes, 2, dz, padded(c.inner), rows, c.inner, s));
+  if (st != ROUTE_OK) return st;
+  if (dx != nullptr && rows != 0) {
+    GemmArgs a{};
+    a.a[0] = dz[0];
+    a.a[1] = dz[1];
+    a.lda = padded(c.inner);
+    a.b[0] = w_gate;
+    a.b[1] = w_up;
+    a.ldb = c.inner;
+    a.c[0] = dx;
+    a.ldc = dx_stride;
+    a.m = rows;
+    a.n = c.inputs;
+    a.red = c.inner;
+    a.segments = 2;
+    a.outputs = 1;
+    st = status_of(block::launch_gemm(c.dtype, block::kDx, a, s));
+    if (st != ROUTE_OK) return st;
+  }
+  if (dw_gate == nullptr) return ROUTE_OK;
+  GemmArgs a{};
+  a.a[0] = x;
+  a.lda = x_stride;
+  a.b[0] = dz[0];
+  a.b[1] = dz[1];
+  a.ldb = padded(c.inner);
+  a.c[0] = dw_gate;
+  a.c[1] = dw_up;
+  a.ldc = c.inner;
+  a.m = c.inputs;
+  a.n = c.inner;
+  a.red = rows;
+  a.segments = 1;
+  a.outputs = 2;
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, s));
+}
+
+void block_gated_destroy(block_gated_plan* plan) { delete plan; }
+
+// ----------------------------------------------------------------- linear --
+
+int block_linear_prepare(const block_linear_config* cfg, block_linear_plan** out) {
+  if (out == nullptr) return ROUTE_E_ARG;
+  *out = nullptr;
+  if (cfg == nullptr || cfg->abi_version != BLOCK_ABI_VERSION) return ROUTE_E_ARG;
+  if ((cfg->dtype != BLOCK_BF16 && cfg->dtype != BLOCK_F16) || cfg->activation < BLOCK_ACT_NONE ||
+      cfg->activation > BLOCK_ACT_GELU_TANH)
+    return ROUTE_E_ARG;
+  if (bad_size(cfg->inputs) || bad_size(cfg->outputs)) return ROUTE_E_SHAPE;
+  if (bad_rows(cfg->rows)) return ROUTE_E_ROWS;
+  if (int st = find_device(cfg->device)) return st;
+  block_linear_plan* p = new_plan<block_linear_plan>(*cfg);
+  if (p == nullptr) return ROUTE_E_ARG;
+  const bool dz = cfg->training && cfg->activation != BLOCK_ACT_NONE;
+  p->off_dz = 0;
+  p->off_sum = p->off_dz + (dz ? round256((size_t)cfg->rows * padded(cfg->outputs) * 2) : 0);
+  p->ws_bytes = p->off_sum + (cfg->training ? round256(block::column_sum_bytes(cfg->rows, cfg->outputs)) : 0);
+  *out = p;
+  return ROUTE_OK;
+}
+
+size_t block_linear_workspace_bytes(const block_linear_plan* plan) { return plan ? plan->ws_bytes : 0; }
+
+int block_linear(const block_linear_plan* plan, const void* x, int64_t x_stride, const void* w,
+                 const void* bias, const void* residual, int64_t residual_stride, void* y,
+                 int64_t y_stride, void* slope, void* workspace, int32_t rows, void* stream) {
+  if (!plan || !w || !workspace) return ROUTE_E_ARG;
+  if (rows != 0 && (!x || !y)) return ROUTE_E_ARG;
+  const block_linear_config& c = plan->cfg;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(x_stride, c.inputs) || bad_stride(y_stride, c.outputs) ||
+      (residual != nullptr && bad_stride(residual_stride, c.outputs)))
+    return ROUTE_E_SHAPE;
+  if (misaligned(x, 2) || misaligned(w, 2) || misaligned(bias, 2) || misaligned(residual, 2) ||
+      misaligned(y, 2) || misaligned(slope, 2) || misaligned(workspace, 256))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  if (rows == 0) return ROUTE_OK;
+  GemmArgs a{};
+  a.a[0] = x;
+  a.lda = x_stride;
+  a.b[0] = w;
+  a.ldb = c.outputs;
+  a.c[0] = y;
+  a.ldc = y_stride;
+  a.saved[0] = slope;
+  a.bias = bias;
+  a.residual = residual;
+  a.ldr = residual_stride;
+  a.m = rows;
+  a.n = c.outputs;
+  a.red = c.inputs;
+  a.segments = a.outputs = 1;
+  a.act = c.activation;
+  return status_of(block::launch_gemm(c.dtype, block::kLinear, a, static_cast<hipStream_t>(stream)));
+}
+
+int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t dy_stride, const void* x,
+                          int64_t x_stride, const void* w, const void* slope, void* dx, int64_t dx_stride,
+                          void* dw, void* dbias, void* workspace, int32_t rows, void* stream) {
+  if (!plan || !w || !workspace || !plan->cfg.training) return ROUTE_E_ARG;
+  const block_linear_config& c = plan->cfg;
+  const bool scaled = c.activation != BLOCK_ACT_NONE;
+  if (rows != 0 && (!dy || !x || (scaled && !slope) || (!dx && !dw && !dbias))) return ROUTE_E_ARG;
+  if (rows < 0 || rows > c.rows) return ROUTE_E_ROWS;
+  if (bad_stride(dy_stride, c.outputs) || bad_stride(x_stride, c.inputs) ||
+      (dx != nullptr && bad_stride(dx_stride, c.inputs)))
+    return ROUTE_E_SHAPE;
+  if (misaligned(dy, 2) || misaligned(x, 2) || misaligned(w, 2) || misaligned(slope, 2) || misaligned(dx, 2) ||
+      misaligned(dw, 2) || misaligned(dbias, 2) || misaligned(workspace, 256))
+    return ROUTE_E_ALIGN;
+  if (int st = check_current(c.device)) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  char* ws = static_cast<char*>(workspace);
+  const void* dz = dy;
+  int64_t ldz = dy_stride;
+  if (scaled) {
+    void* out = ws + plan->off_dz;
+    const int st = status_of(block::launch_scale(c.dtype, dy, dy_stride, &slope, 1, &out, padded(c.outputs), rows,
+                                                 c.outputs, s));
+    if (st != ROUTE_OK) return st;
+    dz = out;
+    ldz = padded(c.outputs);
+  }
+  if (dbias != nullptr) {
+    const int st = status_of(block::launch_column_sum(c.dtype, dz, ldz, rows, c.outputs, dbias,
+                                                      reinterpret_cast<float*>(ws + plan->off_sum), s));
+    if (st != ROUTE_OK) return st;
+  }
+  if (dx != nullptr && rows != 0) {
+    GemmArgs a{};
+    a.a[0] = dz;
+    a.lda = ldz;
+    a.b[0] = w;
+    a.ldb = c.outputs;
+    a.c[0] = dx;
+    a.ldc = dx_stride;
+    a.m = rows;
+    a.n = c.inputs;
+    a.red = c.outputs;
+    a.segments = a.outputs = 1;
+    const int st = status_of(block::launch_gemm(c.dtype, block::kDx, a, s));
+    if (st != ROUTE_OK) return st;
+  }
+  if (dw == nullptr) return ROUTE_OK;
+  GemmArgs a{};
+  a.a[0] = x;
+  a.lda = x_stride;
+  a.b[0] = dz;
+  a.ldb = ldz;
+  a.c[0] = dw;
+  a.ldc = c.outputs;
+  a.m = c.inputs;
+  a.n = c.outputs;
+  a.red = rows;
+  a.segments = a.outputs = 1;
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, s));
+}
+
+void block_linear_destroy(block_linear_plan* plan) { delete plan; }
+
+}  // extern "C"

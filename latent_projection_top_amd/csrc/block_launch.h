@@ -1,0 +1,75 @@
+// Host-side launchers of the layer's operators (called by the C ABI in
+// block_api.cpp).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "block.h"
+#include "route_launch.h"
+
+namespace block {
+
+using route::launch_kernel;
+
+// The four products. Every one is C[m][n] = sum over r of A(m, r) * B(r, n),
+// with r running over `segments` pairs of operands of length `red` each:
+//   kLinear  A = x (r contiguous),  B = W       (n contiguous), 1 segment
+//   kGated   the same with two B matrices, whose sums meet in the epilogue
+//   kDx      A = dz (r contiguous), B = W^T     (r contiguous), 1 or 2 segments
+//   kDw      A = x^T (m contiguous), B = dz     (n contiguous), `outputs`
+//            pairs of B and C
+enum Mode { kLinear = 0, kGated = 1, kDx = 2, kDw = 3 };
+
+struct GemmArgs {
+  const void* a[2];
+  const void* b[2];
+  void* c[2];
+  void* saved[2];        // kGated: d_gate, d_up; kLinear: slope; row stride n
+  const void* bias;
+  const void* residual;
+  int64_t lda, ldb, ldc, ldr;
+  int64_t m;
+  int n;
+  int64_t red;
+  int segments;
+  int outputs;
+  int act;
+};
+
+hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, hipStream_t stream);
+
+// Elementwise first half of the backward passes, and the column sums.
+// out[i] [rows][ld] = dy * s[i]; n columns.
+hipError_t launch_scale(int dtype, const void* dy, int64_t dy_stride, const void* const* s, int count,
+                        void* const* out, int64_t ld, int64_t rows, int n, hipStream_t stream);
+// dst[n] (dtype) = sum over rows of src.
+hipError_t launch_column_sum(int dtype, const void* src, int64_t ld, int64_t rows, int n, void* dst,
+                             float* partial, hipStream_t stream);
+size_t column_sum_bytes(int64_t rows, int n);
+
+struct NormArgs {
+  const void* x;
+  const void* dy;
+  const void* weight;
+  const void* bias;
+  void* y;
+  void* dx;
+  void* dweight;
+  void* dbias;
+  float* mean;
+  float* rstd;
+  float* partial;
+  int64_t ldx, lddy, ldy, lddx;
+  int64_t rows;
+  int width;
+  int param_dtype;
+  float eps;
+};
+
+hipError_t launch_norm(int dtype, const NormArgs& args, hipStream_t stream);
+hipError_t launch_norm_backward(int dtype, const NormArgs& args, hipStream_t stream);
+size_t norm_backward_bytes(int64_t rows, int width);
+
+}  // namespace block
