@@ -20,7 +20,7 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hip", "prefill_gemm.hip",
-           "block_api.cpp", "norm.hip", "block_gemm.hip"]
+           "block_api.cpp", "norm.hip", "block_gemm.hip", "block_tile.hip"]
 HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h"]
 
 COMMON_FLAGS = [
@@ -38,7 +38,8 @@ COMMON_FLAGS = [
 # its stage loads over its MFMAs, and the latent GEMMs ran 4-10 % faster
 # (same bits).
 EXTRA_FLAGS = {"prefill_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form",
-                                    "-mllvm", "-amdgpu-sched-strategy=iterative-ilp"]}
+                                    "-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
+               "block_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

@@ -5,6 +5,7 @@
 
 #include <hip/hip_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <new>
@@ -21,12 +22,12 @@ struct block_norm_plan {
 // to a multiple of 8 elements, and the partial column sums of dbias.
 struct block_gated_plan {
   block_gated_config cfg;
-  size_t off_dz, off_du, ws_bytes;
+  size_t partial_bytes, off_dz, off_du, ws_bytes;
 };
 
 struct block_linear_plan {
   block_linear_config cfg;
-  size_t off_dz, off_sum, ws_bytes;
+  size_t partial_bytes, off_dz, off_sum, ws_bytes;
 };
 
 namespace {
@@ -53,6 +54,17 @@ int find_device(int32_t device) {
 int check_current(int32_t device) {
   int cur = -1;
   return hipGetDevice(&cur) == hipSuccess && cur == device ? ROUTE_OK : ROUTE_E_DEVICE;
+}
+
+// The most any of an operator's products can use for split sums: its forward
+// product and, for training, dx [rows][k] and dw `outputs` x [k][n].
+size_t partial_area(block::Mode mode, int64_t rows, int k, int n, int outputs, bool training) {
+  size_t b = block::gemm_partial_bytes(mode, rows, n, 1);
+  if (training) {
+    b = std::max(b, block::gemm_partial_bytes(block::kDx, rows, k, 1));
+    b = std::max(b, block::gemm_partial_bytes(block::kDw, k, n, outputs));
+  }
+  return round256(b);
 }
 
 template <typename Plan, typename Config>
@@ -170,8 +182,9 @@ int block_gated_prepare(const block_gated_config* cfg, block_gated_plan** out) {
   if (int st = find_device(cfg->device)) return st;
   block_gated_plan* p = new_plan<block_gated_plan>(*cfg);
   if (p == nullptr) return ROUTE_E_ARG;
+  p->partial_bytes = partial_area(block::kGated, cfg->rows, cfg->inputs, cfg->inner, 2, cfg->training != 0);
   const size_t dz = cfg->training ? round256((size_t)cfg->rows * padded(cfg->inner) * 2) : 0;
-  p->off_dz = 0;
+  p->off_dz = p->partial_bytes;
   p->off_du = p->off_dz + dz;
   p->ws_bytes = p->off_du + dz;
   *out = p;
@@ -208,7 +221,8 @@ int block_gated(const block_gated_plan* plan, const void* x, int64_t x_stride, c
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
-  return status_of(block::launch_gemm(c.dtype, block::kGated, a, static_cast<hipStream_t>(stream)));
+  return status_of(block::launch_gemm(c.dtype, block::kGated, a, static_cast<float*>(workspace),
+                                      plan->partial_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t dh_stride, const void* x,
@@ -249,7 +263,7 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
     a.red = c.inner;
     a.segments = 2;
     a.outputs = 1;
-    st = status_of(block::launch_gemm(c.dtype, block::kDx, a, s));
+    st = status_of(block::launch_gemm(c.dtype, block::kDx, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
     if (st != ROUTE_OK) return st;
   }
   if (dw_gate == nullptr) return ROUTE_OK;
@@ -267,7 +281,7 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   a.red = rows;
   a.segments = 1;
   a.outputs = 2;
-  return status_of(block::launch_gemm(c.dtype, block::kDw, a, s));
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
 }
 
 void block_gated_destroy(block_gated_plan* plan) { delete plan; }
@@ -287,7 +301,8 @@ int block_linear_prepare(const block_linear_config* cfg, block_linear_plan** out
   block_linear_plan* p = new_plan<block_linear_plan>(*cfg);
   if (p == nullptr) return ROUTE_E_ARG;
   const bool dz = cfg->training && cfg->activation != BLOCK_ACT_NONE;
-  p->off_dz = 0;
+  p->partial_bytes = partial_area(block::kLinear, cfg->rows, cfg->inputs, cfg->outputs, 1, cfg->training != 0);
+  p->off_dz = p->partial_bytes;
   p->off_sum = p->off_dz + (dz ? round256((size_t)cfg->rows * padded(cfg->outputs) * 2) : 0);
   p->ws_bytes = p->off_sum + (cfg->training ? round256(block::column_sum_bytes(cfg->rows, cfg->outputs)) : 0);
   *out = p;
@@ -327,7 +342,8 @@ int block_linear(const block_linear_plan* plan, const void* x, int64_t x_stride,
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
-  return status_of(block::launch_gemm(c.dtype, block::kLinear, a, static_cast<hipStream_t>(stream)));
+  return status_of(block::launch_gemm(c.dtype, block::kLinear, a, static_cast<float*>(workspace),
+                                      plan->partial_bytes, static_cast<hipStream_t>(stream)));
 }
 
 int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t dy_stride, const void* x,
@@ -374,7 +390,7 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
     a.n = c.inputs;
     a.red = c.outputs;
     a.segments = a.outputs = 1;
-    const int st = status_of(block::launch_gemm(c.dtype, block::kDx, a, s));
+    const int st = status_of(block::launch_gemm(c.dtype, block::kDx, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
     if (st != ROUTE_OK) return st;
   }
   if (dw == nullptr) return ROUTE_OK;
@@ -389,7 +405,7 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   a.n = c.outputs;
   a.red = rows;
   a.segments = a.outputs = 1;
-  return status_of(block::launch_gemm(c.dtype, block::kDw, a, s));
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
 }
 
 void block_linear_destroy(block_linear_plan* plan) { delete plan; }

@@ -98,7 +98,27 @@ static hipError_t launch_any(Mode mode, const GemmArgs& p, hipStream_t stream) {
   }
 }
 
-hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, hipStream_t stream) {
+// 16-byte loads of the tile kernel: every row of every operand starts on a
+// 16-byte boundary and its contiguous length is a multiple of 8.
+static bool aligned16(Mode mode, const GemmArgs& p) {
+  uintptr_t bits = 0;
+  for (int i = 0; i < 2; ++i)
+    bits |= reinterpret_cast<uintptr_t>(p.a[i]) | reinterpret_cast<uintptr_t>(p.b[i]);
+  const int64_t a_len = mode == kDw ? p.m : p.red, b_len = mode == kDx ? p.red : p.n;
+  return (bits & 15) == 0 && ((p.lda | p.ldb | a_len | b_len) & 7) == 0;
+}
+
+size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
+  const size_t plane = (size_t)m * n * 4 * (mode == kGated ? 2 : outputs);
+  // the tile plans split into at most 16, and only products of few tiles
+  const size_t most = (size_t)64 << 20;
+  return plane * 16 < most ? plane * 16 : most;
+}
+
+hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, float* partial, size_t partial_bytes,
+                       hipStream_t stream) {
+  if (aligned16(mode, p))
+    return launch_gemm_tile(dtype, mode, p, plan_tiles(mode, p, partial_bytes), partial, stream);
   return dtype == BLOCK_BF16 ? launch_any<BF16>(mode, p, stream) : launch_any<F16>(mode, p, stream);
 }
 

@@ -1,0 +1,395 @@
+// Matrix products of the layer's operators, large tiles: the kernel behind
+// every product whose operands are 16-byte aligned and whose row count makes
+// the matrix cores, not the weights' bandwidth, the bound.
+#include "block_device.h"
+
+namespace block {
+
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr int kStep = 32;    // reduction per stage: one MFMA deep
+constexpr int kStages = 5;   // LDS buffers
+
+template <int BMr, int BNr, int WMr, int WNr>
+struct TileShape {
+  static constexpr int BM = BMr, BN = BNr, WM = WMr, WN = WNr;
+  static constexpr int NW = WM * WN;
+  static constexpr int MT = BM / WM / 16, NT = BN / WN / 16;  // 16 x 16 tiles of a wave
+  static constexpr int A_BYTES = BM * kStep * 2, B_BYTES = BN * kStep * 2;
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int A_PER = BM / 16 / NW, B_PER = BN / 16 / NW;  // 1 KB loads of a wave per stage
+  static constexpr int PER = A_PER + B_PER;
+  static_assert(A_PER >= 1 && B_PER >= 1 && NT % 2 == 0 && MT % 2 == 0, "");
+  static_assert(kStages * STAGE <= 160 * 1024, "LDS");
+};
+
+// 16 bytes that lanes outside the reduction's range load.
+__device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
+
+// Global -> LDS, 16 bytes per lane: lane l's bytes land at lds + 16 l. Inline
+// assembly, so that the compiler does not wait for every load in flight
+// before each LDS read (it cannot tell the stages apart); the kernel's own
+// vmcnt waits order them, and the volatile barriers below keep the LDS reads
+// on their side.
+__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
+}
+__device__ __forceinline__ void dma16(const char* addr, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(addr), "{m0}"(lds));
+}
+
+__device__ __forceinline__ u32x4 lds_b128(uint32_t addr) {
+  return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)addr;
+}
+__device__ __forceinline__ u32x2 lds_tr16(uint32_t addr) {
+  return __builtin_bit_cast(
+      u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(uintptr_t)addr));
+}
+
+// Wait until at most Vm of this wave's loads are in flight and at most Lgkm
+// LDS reads are outstanding, then meet the block.
+template <int Vm, int Lgkm>
+__device__ __forceinline__ void wait_barrier() {
+  static_assert(Vm >= 0 && Vm < 64 && Lgkm >= 0 && Lgkm < 16, "counter range");
+  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)\n\ts_barrier" : : "n"(Vm), "n"(Lgkm) : "memory");
+}
+
+// An operand's tile of `Rows` rows (or columns) by 32 of the reduction, and
+// how it lies in a stage.
+//   RContig (the reduction is contiguous in memory): 64-byte rows; the
+//     16-byte piece c of row r sits at position c ^ ((r >> 2) & 3), so that
+//     the 16 rows that the lanes of one group read take 16 different bank
+//     groups. Read with ds_read_b128.
+//   otherwise (rows contiguous): blocks of [32 r][32 rows], 64-byte lines,
+//     whose two halves are swapped where bit 3 of r is set. The MFMA wants 8
+//     consecutive r of one row per lane, which ds_read_tr16_b64 delivers.
+template <bool RContig>
+struct Operand {
+  // this lane's source of load `c` (1 KB): row within the tile and r within
+  // the stage of its first element
+  static __device__ __forceinline__ int row(int c, int lane) {
+    if constexpr (RContig) return 16 * c + (lane >> 2);
+    return 32 * (c >> 1) + 8 * ((lane & 3) ^ ((lane >> 5) << 1));
+  }
+  static __device__ __forceinline__ int red(int c, int lane) {
+    if constexpr (RContig) return 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+    return 16 * (c & 1) + (lane >> 2);
+  }
+  // addresses of this lane's part of a 16-row fragment: rows 16 t, t even
+  // (h = 0) or odd (h = 1), relative to the even tile
+  static __device__ __forceinline__ uint32_t base(int lane, int h) {
+    const int g = lane >> 4, m = lane & 15;
+    if constexpr (RContig) return (uint32_t)((16 * h + m) * 64 + ((g ^ ((m >> 2) & 3)) * 16));
+    return (uint32_t)((8 * g + (m >> 2)) * 64 + (2 * (h ^ (g & 1)) + ((m & 3) >> 1)) * 16 + (m & 1) * 8);
+  }
+  static constexpr int kReads = RContig ? 1 : 2;  // LDS reads per fragment
+  static __device__ __forceinline__ u32x4 read(uint32_t addr) {
+    if constexpr (RContig) return lds_b128(addr);
+    const u32x2 lo = lds_tr16(addr), hi = lds_tr16(addr + 4 * 64);
+    return u32x4{lo[0], lo[1], hi[0], hi[1]};
+  }
+  // bytes from one pair of 16-row fragments to the next: the same in both
+  static constexpr int kPair = 2048;
+};
+
+template <typename T, int Mode, typename S>
+__global__ __launch_bounds__(64 * S::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* partial) {
+  typedef Operand<Mode != kDw> A;
+  typedef Operand<Mode == kDx> B;
+  constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;  // output columns of a tile
+  __shared__ __attribute__((aligned(1024))) char smem[kStages * S::STAGE];
+
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  const int g = lane >> 4, m = lane & 15;
+  const int wm = wave / S::WN, wn = wave % S::WN;
+
+  // Blocks are dealt round-robin over the 8 XCDs: renumber them so that each
+  // XCD has a contiguous range of tiles, and walk the range in groups of 8
+  // row tiles, column by column, so that one XCD's L2 holds few A and B tiles
+  // at a time.
+  const int total = mtiles * ntiles * p.outputs;
+  const int split = blockIdx.x / total;
+  int lin = blockIdx.x - split * total;
+  if ((total & 7) == 0) lin = (lin & 7) * (total >> 3) + (lin >> 3);
+  const int cols_all = ntiles * p.outputs;
+  const int group = lin / (8 * cols_all);
+  const int gm = min(mtiles - 8 * group, 8);
+  const int loc = lin - group * 8 * cols_all;
+  const int64_t row0 = (int64_t)(8 * group + loc % gm) * S::BM;
+  const int ct = loc / gm;
+  const int which = ct / ntiles;
+  const int col0 = (ct - which * ntiles) * kCols;
+
+  const int per_seg = (int)((p.red + kStep - 1) / kStep);
+  const int all = per_seg * p.segments;
+  const int s0 = (int)((int64_t)all * split / splits);
+  const int s1 = (int)((int64_t)all * (split + 1) / splits);
+  const bool ragged = (p.red & (kStep - 1)) != 0;
+
+  // ---- global -> LDS -------------------------------------------------------
+  // Rows past the matrix's end repeat its last one and columns its last eight
+  // (their sums are not stored); past the reduction's end lanes load zeros.
+  uint32_t off[S::PER];
+  int red_of[S::PER];
+#pragma unroll
+  for (int i = 0; i < S::PER; ++i) {
+    const bool is_a = i < S::A_PER;
+    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+    if (is_a) {
+      const int r = A::row(c, lane), k = A::red(c, lane);
+      red_of[i] = k;
+      if (Mode != kDw)
+        off[i] = (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + k) * 2u;
+      else
+        off[i] = (uint32_t)(k * p.lda + min(row0 + r, p.m - 8)) * 2u;
+    } else {
+      int r = B::row(c, lane);
+      const int k = B::red(c, lane);
+      red_of[i] = k;
+      // gated: 32-column blocks alternate between the two matrices
+      if (Mode == kGated) r = 32 * (r >> 6) + (r & 31);
+      if (Mode == kDx)
+        off[i] = (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + k) * 2u;
+      else
+        off[i] = (uint32_t)(k * p.ldb + min(col0 + r, p.n - 8)) * 2u;
+    }
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)smem;
+
+  auto issue_one = [&](int s, uint32_t buf, int i) {
+    const bool is_a = i < S::A_PER;
+    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+    const int seg = s >= per_seg ? 1 : 0;
+    const int ks = s - seg * per_seg;
+    const char* base;
+    if (is_a) {
+      base = static_cast<const char*>(p.a[seg]) +
+             (Mode != kDw ? row0 * p.lda * 2 + (int64_t)ks * (kStep * 2) : (int64_t)ks * (kStep * 2) * p.lda);
+    } else {
+      const int mat = Mode == kGated ? ((c >> 1) & 1) : (Mode == kDx ? seg : which);
+      base = static_cast<const char*>(p.b[mat]) +
+             (Mode == kDx ? (int64_t)col0 * p.ldb * 2 + (int64_t)ks * (kStep * 2)
+                          : (int64_t)ks * (kStep * 2) * p.ldb);
+    }
+    const uint32_t dst = buf + (is_a ? 0 : S::A_BYTES) + c * 1024;
+    if (ragged && ks == per_seg - 1) {
+      const bool in = (int64_t)ks * kStep + red_of[i] < p.red;
+      dma16(in ? base + off[i] : reinterpret_cast<const char*>(kZeros), dst);
+    } else {
+      dma16(base, off[i], dst);
+    }
+  };
+
+  // ---- LDS -> registers ----------------------------------------------------
+  uint32_t a_rd[2], b_rd[2];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    a_rd[h] = A::base(lane, h) + wm * (S::MT / 2) * A::kPair;
+    b_rd[h] = B::base(lane, h) + S::A_BYTES + wn * (S::NT / 2) * B::kPair;
+  }
+  auto read_a = [&](uint32_t buf, int i) { return A::read(buf + a_rd[i & 1] + (i >> 1) * A::kPair); };
+  auto read_b = [&](uint32_t buf, int j) { return B::read(buf + b_rd[j & 1] + (j >> 1) * B::kPair); };
+  constexpr int kReads = S::MT * A::kReads + S::NT * B::kReads;  // per stage and wave
+
+  f32x4 acc[S::MT][S::NT] = {};
+  u32x4 a[S::MT], b0[S::NT], b1[S::NT];
+
+  // Stage s's MFMAs. Meanwhile the operands of stage s + 1 are read (a[i] as
+  // soon as its last MFMA is issued, B into the other register set) and this
+  // wave's loads of stage s + 4 go out, into the buffer of stage s - 1, which
+  // the barrier before this step has freed.
+  auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], uint32_t next, int load, uint32_t load_buf, bool issue) {
+    constexpr int kEvery = S::MT * S::NT / S::PER;
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i) {
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) {
+        const int n = i * S::NT + j;
+        if (issue && n % kEvery == kEvery / 2) issue_one(load, load_buf, n / kEvery);
+        acc[i][j] = T::mfma(b[j], a[i], acc[i][j]);
+      }
+      if (i < S::NT) bn[i] = read_b(next, i);
+      if (S::MT < S::NT && i == S::MT - 1)
+#pragma unroll
+        for (int j = S::MT; j < S::NT; ++j) bn[j] = read_b(next, j);
+      a[i] = read_a(next, i);
+    }
+  };
+  // At the end of stage s: stage s + 2 has to be in LDS (at most the loads of
+  // the stages after it still in flight), and every read of stage s's buffer
+  // has to have returned (at most the reads of stage s + 1 outstanding).
+  constexpr int kLgkm = kReads < 15 ? kReads : 15;
+
+  const int count = s1 - s0;
+  if (count > 0) {
+#pragma unroll 1
+    for (int s = 0; s < min(count, 4); ++s)
+#pragma unroll
+      for (int i = 0; i < S::PER; ++i) issue_one(s0 + s, lds0 + s * S::STAGE, i);
+    if (count >= 4)
+      wait_barrier<2 * S::PER, 0>();
+    else
+      wait_barrier<0, 0>();
+#pragma unroll
+    for (int i = 0; i < S::MT; ++i) a[i] = read_a(lds0, i);
+#pragma unroll
+    for (int j = 0; j < S::NT; ++j) b0[j] = read_b(lds0, j);
+
+    constexpr uint32_t kEnd = kStages * S::STAGE;
+    uint32_t next = S::STAGE, fill = 4 * S::STAGE;  // buffers of stages s + 1 and s + 4
+    auto advance = [&] {
+      next = next + S::STAGE == kEnd ? 0 : next + S::STAGE;
+      fill = fill + S::STAGE == kEnd ? 0 : fill + S::STAGE;
+    };
+    int s = 0;
+    // steady state: two stages a turn (the two B register sets)
+#pragma unroll 1
+    for (; s + 5 < count; s += 2) {
+      step(b0, b1, lds0 + next, s0 + s + 4, lds0 + fill, true);
+      wait_barrier<2 * S::PER, kLgkm>();
+      advance();
+      step(b1, b0, lds0 + next, s0 + s + 5, lds0 + fill, true);
+      wait_barrier<2 * S::PER, kLgkm>();
+      advance();
+    }
+    // the last stages; one more load if an odd number is left
+#pragma unroll 1
+    for (; s < count; ++s) {
+      const bool issue = s + 4 < count;
+      step(b0, b1, lds0 + next, s0 + s + 4, lds0 + fill, issue);
+      if (s + 2 < count) {
+        if (s + 4 < count)
+          wait_barrier<2 * S::PER, kLgkm>();
+        else if (s + 3 < count)
+          wait_barrier<S::PER, kLgkm>();
+        else
+          wait_barrier<0, kLgkm>();
+      }
+      advance();
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j) b0[j] = b1[j];
+    }
+  }
+
+  // lane (g, m) of tile (i, j) holds row 16 i + m, columns 16 j + 4 g .. + 3
+#pragma unroll
+  for (int i = 0; i < S::MT; ++i) {
+    const int64_t row = row0 + 16 * (S::MT * wm + i) + m;
+    constexpr int kJ = Mode == kGated ? S::NT / 2 : S::NT;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+      const int col = col0 + 16 * (kJ * wn + j) + 4 * g;
+      const f32x4 v = acc[i][j], u = acc[i][Mode == kGated ? S::NT / 2 + j : j];
+      if (splits > 1) {
+        if (row < p.m && col < p.n) {
+          const int planes = Mode == kGated ? 2 : p.outputs;
+          float* d = partial + (((int64_t)split * planes + which) * p.m + row) * p.n + col;
+          *reinterpret_cast<f32x4*>(d) = v;
+          if (Mode == kGated) *reinterpret_cast<f32x4*>(d + p.m * p.n) = u;
+        }
+      } else {
+        epilogue<T, Mode>(p, which, row, col, v, u);
+      }
+    }
+  }
+}
+
+// Joins the splits' FP32 sums in split order and ends the product.
+template <typename T, int Mode>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits, const float* partial) {
+  const int64_t quads = (p.n + 3) / 4;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int planes = Mode == kGated ? 2 : p.outputs;
+  const int64_t plane = p.m * p.n;
+  if (id >= quads * p.m * (Mode == kGated ? 1 : planes)) return;
+  const int which = (int)(id / (quads * p.m));
+  const int64_t q = id - which * quads * p.m;
+  const int64_t row = q / quads;
+  const int col = (int)(q - row * quads) * 4;
+  const float* d = partial + which * plane + row * p.n + col;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
+  for (int s = 0; s < splits; ++s) {
+    v += *reinterpret_cast<const f32x4*>(d);
+    if (Mode == kGated) u += *reinterpret_cast<const f32x4*>(d + plane);
+    d += planes * plane;
+  }
+  epilogue<T, Mode>(p, which, row, col, v, u);
+}
+
+template <typename T, int Mode, typename S>
+static hipError_t launch_shape(const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
+  constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;
+  const int mt = (int)((p.m + S::BM - 1) / S::BM), nt = (p.n + kCols - 1) / kCols;
+  const int64_t blocks = (int64_t)mt * nt * p.outputs * splits;
+  const hipError_t e = launch_kernel(gemm_tile_kernel<T, Mode, S>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
+                                     p, mt, nt, splits, partial);
+  if (e != hipSuccess || splits == 1) return e;
+  const int64_t items = (int64_t)((p.n + 3) / 4) * p.m * (Mode == kGated ? 1 : p.outputs);
+  return launch_kernel(gemm_join_kernel<T, Mode>, dim3((unsigned)((items + 255) / 256)), dim3(256), stream, p,
+                       splits, static_cast<const float*>(partial));
+}
+
+typedef TileShape<256, 256, 2, 4> Large;
+typedef TileShape<128, 256, 2, 4> Wide;
+typedef TileShape<128, 128, 2, 2> Small;
+
+template <typename T, int Mode>
+static hipError_t launch_mode(const GemmArgs& p, const TilePlan& t, float* partial, hipStream_t stream) {
+  switch (t.shape) {
+    case 0: return launch_shape<T, Mode, Large>(p, t.splits, partial, stream);
+    case 1: return launch_shape<T, Mode, Wide>(p, t.splits, partial, stream);
+    default: return launch_shape<T, Mode, Small>(p, t.splits, partial, stream);
+  }
+}
+
+template <typename T>
+static hipError_t launch_typed(Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
+                               hipStream_t stream) {
+  switch (mode) {
+    case kLinear: return launch_mode<T, kLinear>(p, t, partial, stream);
+    case kGated: return launch_mode<T, kGated>(p, t, partial, stream);
+    case kDx: return launch_mode<T, kDx>(p, t, partial, stream);
+    default: return launch_mode<T, kDw>(p, t, partial, stream);
+  }
+}
+
+hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
+                            hipStream_t stream) {
+  return dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, t, partial, stream)
+                             : launch_typed<F16>(mode, p, t, partial, stream);
+}
+
+// Tile shape and K split of a product: the one whose time a simple model puts
+// lowest.
+TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
+  struct { int bm, bn; double rate; int per_cu; } const shapes[3] = {
+      {256, 256, 1.0, 1}, {128, 256, 0.75, 1}, {128, 128, 0.6, 2}};
+  const double steps = (double)((p.red + kStep - 1) / kStep) * p.segments;
+  const int planes = mode == kGated ? 2 : p.outputs;
+  TilePlan best{0, 1};
+  double best_t = 0;
+  for (int k = 0; k < 3; ++k) {
+    const int bn = mode == kGated ? shapes[k].bn / 2 : shapes[k].bn;
+    const double tiles = (double)((p.m + shapes[k].bm - 1) / shapes[k].bm) * ((p.n + bn - 1) / bn) * p.outputs;
+    // microseconds of one stage of a block that has its CU to itself
+    const double stage = 0.6 * shapes[k].bm * shapes[k].bn / 65536.0 / shapes[k].rate;
+    for (int s = 1; s <= 16; ++s) {
+      const double bytes = 4.0 * p.m * p.n * planes * s;
+      if (s > 1 && (bytes > (double)partial_bytes || steps / s < 8 || (p.n & 3) != 0)) break;
+      const double slots = 256.0 * shapes[k].per_cu;
+      const double blocks = tiles * s;
+      const double rounds = blocks <= 256 ? 1.0 : (double)(int64_t)((blocks + slots - 1) / slots) * shapes[k].per_cu;
+      double t = rounds * (steps / s + 6) * stage;
+      if (s > 1) t += 4.0 + 2.0 * bytes / 4e6;
+      if (best_t == 0 || t < best_t) {
+        best = TilePlan{k, s};
+        best_t = t;
+      }
+    }
+  }
+  return best;
+}
+
+}  // namespace block
