@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "block_launch.h"
 
 namespace block {
@@ -77,109 +79,142 @@ struct ValueSlope {
   float d;  // act'(z)
 };
 
-// `act` is uniform over a launch, so the switch is one scalar branch. The
-// arguments of terms that vanish for large |z| are clamped where the term is
-// already 0 in FP32, so that they stay 0 and not infinity times 0.
-__device__ __forceinline__ ValueSlope activate(int act, float z) {
+// The arguments of terms that vanish for large |z| are clamped where the term
+// is already 0 in FP32, so that they stay 0 and not infinity times 0.
+template <int Act>
+__device__ __forceinline__ ValueSlope activate(float z) {
+  if constexpr (Act == BLOCK_ACT_RELU) {
+    return {z < 0.f ? 0.f : z, z > 0.f ? 1.f : (z == z ? 0.f : z)};
+  } else if constexpr (Act == BLOCK_ACT_SILU) {
+    const float s = 1.f / (1.f + __expf(-z));
+    return {z * s, s * (1.f + z * (1.f - s))};
+  } else if constexpr (Act == BLOCK_ACT_GELU) {
+    const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
+    const float zc = fminf(fmaxf(z, -20.f), 20.f);  // exp(-200) is 0 in FP32
+    return {z * cdf, cdf + zc * (__expf(-0.5f * zc * zc) * 0.39894228040143268f)};
+  } else {
+    const float c = 0.79788456080286536f;
+    const float zc = fminf(fmaxf(z, -10.f), 10.f);  // tanh of +-43 is +-1 in FP32
+    const float q = zc * zc;
+    const float t = 1.f - 2.f / (1.f + __expf(2.f * c * zc * (1.f + 0.044715f * q)));
+    const float half = 0.5f * (1.f + t);
+    return {z * half, half + 0.5f * zc * (1.f - t * t) * c * (1.f + 3.f * 0.044715f * q)};
+  }
+}
+
+// Calls f(activation constant): `act` is uniform over a launch, so this is one
+// scalar branch around each whole use.
+template <typename F>
+__device__ __forceinline__ void with_activation(int act, F f) {
   switch (act) {
-    case BLOCK_ACT_RELU:
-      return {z < 0.f ? 0.f : z, z > 0.f ? 1.f : (z == z ? 0.f : z)};
-    case BLOCK_ACT_SILU: {
-      const float s = 1.f / (1.f + __expf(-z));
-      return {z * s, s * (1.f + z * (1.f - s))};
-    }
-    case BLOCK_ACT_GELU: {
-      const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
-      const float zc = fminf(fmaxf(z, -20.f), 20.f);  // exp(-200) is 0 in FP32
-      return {z * cdf, cdf + zc * (__expf(-0.5f * zc * zc) * 0.39894228040143268f)};
-    }
-    case BLOCK_ACT_GELU_TANH: {
-      const float c = 0.79788456080286536f;
-      const float zc = fminf(fmaxf(z, -10.f), 10.f);  // tanh of +-43 is +-1 in FP32
-      const float q = zc * zc;
-      const float t = 1.f - 2.f / (1.f + __expf(2.f * c * zc * (1.f + 0.044715f * q)));
-      const float half = 0.5f * (1.f + t);
-      return {z * half, half + 0.5f * zc * (1.f - t * t) * c * (1.f + 3.f * 0.044715f * q)};
-    }
-    default:
-      return {z, 1.f};
+    case BLOCK_ACT_RELU: f(std::integral_constant<int, BLOCK_ACT_RELU>{}); break;
+    case BLOCK_ACT_SILU: f(std::integral_constant<int, BLOCK_ACT_SILU>{}); break;
+    case BLOCK_ACT_GELU: f(std::integral_constant<int, BLOCK_ACT_GELU>{}); break;
+    default: f(std::integral_constant<int, BLOCK_ACT_GELU_TANH>{}); break;
   }
 }
 
 // --------------------------------------------------------------- epilogue --
 
-// Store up to four consecutive columns of a row (`count` of them, 4 unless
-// the matrix ends inside).
-template <typename T>
-__device__ __forceinline__ void store4(typename T::raw* p, f32x4 v, int count) {
-  if (count == 4) {
-    const u32x2 w = {(uint32_t)T::store(v[0]) | (uint32_t)T::store(v[1]) << 16,
-                     (uint32_t)T::store(v[2]) | (uint32_t)T::store(v[3]) << 16};
-    reinterpret_cast<Any8*>(p)->v = w;
+// Up to C (4 or 8) consecutive columns of a row, `count` of them inside the
+// matrix.
+template <typename T, int C>
+__device__ __forceinline__ void store_cols(typename T::raw* p, const float (&v)[C], int count) {
+  uint32_t w[C / 2];
+#pragma unroll
+  for (int t = 0; t < C / 2; ++t)
+    w[t] = (uint32_t)T::store(v[2 * t]) | (uint32_t)T::store(v[2 * t + 1]) << 16;
+  if (count >= C) {
+    if constexpr (C == 8)
+      reinterpret_cast<Any16*>(p)->v = u32x4{w[0], w[1], w[2], w[3]};
+    else
+      reinterpret_cast<Any8*>(p)->v = u32x2{w[0], w[1]};
     return;
   }
 #pragma unroll
-  for (int t = 0; t < 3; ++t)
-    if (t < count) p[t] = T::store(v[t]);
+  for (int t = 0; t < C - 1; ++t)
+    if (t < count) p[t] = (uint16_t)(w[t >> 1] >> (16 * (t & 1)));
 }
 
-template <typename T>
-__device__ __forceinline__ f32x4 load4(const typename T::raw* p, int count) {
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
-  if (count == 4) {
-    const u32x2 w = reinterpret_cast<const Any8*>(p)->v;
+template <typename T, int C>
+__device__ __forceinline__ void load_cols(const typename T::raw* p, float (&v)[C], int count) {
+  uint32_t w[C / 2] = {};
+  if (count >= C) {
+    if constexpr (C == 8) {
+      const u32x4 x = reinterpret_cast<const Any16*>(p)->v;
+      w[0] = x[0]; w[1] = x[1]; w[2] = x[2]; w[3] = x[3];
+    } else {
+      const u32x2 x = reinterpret_cast<const Any8*>(p)->v;
+      w[0] = x[0]; w[1] = x[1];
+    }
+  } else {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) v[t] = T::load((uint16_t)(w[t >> 1] >> (16 * (t & 1))));
-    return v;
+    for (int t = 0; t < C - 1; ++t)
+      if (t < count) w[t >> 1] |= (uint32_t)p[t] << (16 * (t & 1));
   }
 #pragma unroll
-  for (int t = 0; t < 3; ++t)
-    if (t < count) v[t] = T::load(p[t]);
-  return v;
+  for (int t = 0; t < C; ++t) v[t] = T::load((uint16_t)(w[t >> 1] >> (16 * (t & 1))));
 }
 
 // The end of a product: `v` (and for the gated product `u`) are the FP32 sums
-// of columns col .. col + 3 of output row `row`; `which` selects the output
-// matrix of a product with two. Everything happens in FP32 and each output is
-// rounded once.
-template <typename T, int Mode>
-__device__ __forceinline__ void epilogue(const GemmArgs& p, int which, int64_t row, int col, f32x4 v,
-                                         f32x4 u) {
+// of columns col .. col + C - 1 of output row `row`; `which` selects the
+// output matrix of a product with two. Everything happens in FP32 and each
+// output is rounded once. The derivatives kept for the backward pass are
+// rounded to the activations' type like everything else a training step
+// keeps: FP32 would double the bytes of what is, per layer, the largest
+// thing kept. It costs one rounding of three in the gradients (an RMS of 1.7
+// instead of 1.4 roundings).
+template <typename T, int Mode, int C>
+__device__ __forceinline__ void epilogue(const GemmArgs& p, int which, int64_t row, int col, float (&v)[C],
+                                         float (&u)[C]) {
   typedef typename T::raw raw;
-  const int count = min(4, p.n - col);
+  const int count = p.n - col;
   if (row >= p.m || count <= 0) return;
   raw* c = static_cast<raw*>(p.c[which]) + row * p.ldc + col;
   if constexpr (Mode == kGated) {
-    f32x4 h, dg, du;
+    float dg[C], du[C];
+    with_activation(p.act, [&](auto act) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const ValueSlope s = activate(p.act, v[t]);
-      h[t] = s.a * u[t];
-      dg[t] = s.d * u[t];
-      du[t] = s.a;
-    }
-    store4<T>(c, h, count);
+      for (int t = 0; t < C; ++t) {
+        const ValueSlope s = activate<decltype(act)::value>(v[t]);
+        v[t] = s.a * u[t];
+        dg[t] = s.d * u[t];
+        du[t] = s.a;
+      }
+    });
+    store_cols<T, C>(c, v, count);
     if (p.saved[0] != nullptr) {
-      store4<T>(static_cast<raw*>(p.saved[0]) + row * p.n + col, dg, count);
-      store4<T>(static_cast<raw*>(p.saved[1]) + row * p.n + col, du, count);
+      store_cols<T, C>(static_cast<raw*>(p.saved[0]) + row * p.n + col, dg, count);
+      store_cols<T, C>(static_cast<raw*>(p.saved[1]) + row * p.n + col, du, count);
     }
   } else if constexpr (Mode == kLinear) {
-    if (p.bias != nullptr) v += load4<T>(static_cast<const raw*>(p.bias) + col, count);
-    if (p.act != BLOCK_ACT_NONE) {
-      f32x4 d;
+    if (p.bias != nullptr) {
+      float b[C];
+      load_cols<T, C>(static_cast<const raw*>(p.bias) + col, b, count);
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        const ValueSlope s = activate(p.act, v[t]);
-        v[t] = s.a;
-        d[t] = s.d;
-      }
-      if (p.saved[0] != nullptr) store4<T>(static_cast<raw*>(p.saved[0]) + row * p.n + col, d, count);
+      for (int t = 0; t < C; ++t) v[t] += b[t];
     }
-    if (p.residual != nullptr)
-      v += load4<T>(static_cast<const raw*>(p.residual) + row * p.ldr + col, count);
-    store4<T>(c, v, count);
+    if (p.act != BLOCK_ACT_NONE) {
+      float d[C];
+      with_activation(p.act, [&](auto act) {
+#pragma unroll
+        for (int t = 0; t < C; ++t) {
+          const ValueSlope s = activate<decltype(act)::value>(v[t]);
+          v[t] = s.a;
+          d[t] = s.d;
+        }
+      });
+      if (p.saved[0] != nullptr) store_cols<T, C>(static_cast<raw*>(p.saved[0]) + row * p.n + col, d, count);
+    }
+    if (p.residual != nullptr) {
+      float r[C];
+      load_cols<T, C>(static_cast<const raw*>(p.residual) + row * p.ldr + col, r, count);
+#pragma unroll
+      for (int t = 0; t < C; ++t) v[t] += r[t];
+    }
+    store_cols<T, C>(c, v, count);
   } else {
-    store4<T>(c, v, count);
+    store_cols<T, C>(c, v, count);
   }
 }
 

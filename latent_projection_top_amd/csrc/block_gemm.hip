@@ -3,9 +3,10 @@
 
 namespace block {
 
-// One kernel for every product, layout, size and alignment: 64 x 64 output
-// tiles, four waves of 32 x 32 each, reduction steps of 32 staged through LDS
-// with r contiguous.
+// Products with an operand of fewer than 8 contiguous elements, which no
+// 16-byte load fits: 64 x 64 output tiles, four waves of 32 x 32 each,
+// reduction steps of 32 staged element by element through LDS with r
+// contiguous.
 constexpr int kTile = 64;
 constexpr int kStep = 32;
 constexpr int kPitch = kStep + 8;  // 16-byte aligned, spreads rows over banks
@@ -42,7 +43,7 @@ __device__ __forceinline__ void stage(uint16_t* lds, const uint16_t* src, int64_
 }
 
 template <typename T, int Mode>
-__global__ __launch_bounds__(256) void gemm_any_kernel(GemmArgs p) {
+__global__ __launch_bounds__(256) void gemm_narrow_kernel(GemmArgs p) {
   constexpr bool kAContig = Mode != kDw, kBContig = Mode == kDx;
   constexpr int kB = Mode == kGated ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint16_t sa[kTile * kPitch];
@@ -82,24 +83,30 @@ __global__ __launch_bounds__(256) void gemm_any_kernel(GemmArgs p) {
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      epilogue<T, Mode>(p, which, row0 + wr + 16 * i + m, col0 + wc + 16 * j + 4 * g, acc[0][i][j],
-                        acc[kB - 1][i][j]);
+    for (int j = 0; j < 2; ++j) {
+      float v[4], u[4];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        v[t] = acc[0][i][j][t];
+        u[t] = acc[kB - 1][i][j][t];
+      }
+      epilogue<T, Mode, 4>(p, which, row0 + wr + 16 * i + m, col0 + wc + 16 * j + 4 * g, v, u);
+    }
 }
 
 template <typename T>
-static hipError_t launch_any(Mode mode, const GemmArgs& p, hipStream_t stream) {
+static hipError_t launch_narrow(Mode mode, const GemmArgs& p, hipStream_t stream) {
   const dim3 grid((p.n + kTile - 1) / kTile, (unsigned)((p.m + kTile - 1) / kTile), mode == kDw ? p.outputs : 1);
   switch (mode) {
-    case kLinear: return launch_kernel(gemm_any_kernel<T, kLinear>, grid, dim3(256), stream, p);
-    case kGated: return launch_kernel(gemm_any_kernel<T, kGated>, grid, dim3(256), stream, p);
-    case kDx: return launch_kernel(gemm_any_kernel<T, kDx>, grid, dim3(256), stream, p);
-    default: return launch_kernel(gemm_any_kernel<T, kDw>, grid, dim3(256), stream, p);
+    case kLinear: return launch_kernel(gemm_narrow_kernel<T, kLinear>, grid, dim3(256), stream, p);
+    case kGated: return launch_kernel(gemm_narrow_kernel<T, kGated>, grid, dim3(256), stream, p);
+    case kDx: return launch_kernel(gemm_narrow_kernel<T, kDx>, grid, dim3(256), stream, p);
+    default: return launch_kernel(gemm_narrow_kernel<T, kDw>, grid, dim3(256), stream, p);
   }
 }
 
-// 16-byte loads of the tile kernel: every row of every operand starts on a
-// 16-byte boundary and its contiguous length is a multiple of 8.
+// Asynchronous 16-byte loads: every row of every operand starts on a 16-byte
+// boundary and its contiguous length is a multiple of 8.
 static bool aligned16(Mode mode, const GemmArgs& p) {
   uintptr_t bits = 0;
   for (int i = 0; i < 2; ++i)
@@ -108,8 +115,12 @@ static bool aligned16(Mode mode, const GemmArgs& p) {
   return (bits & 15) == 0 && ((p.lda | p.ldb | a_len | b_len) & 7) == 0;
 }
 
+static bool narrow(Mode mode, const GemmArgs& p) {
+  return (mode == kDw ? p.m : p.red) < 8 || (mode == kDx ? p.red : p.n) < 8;
+}
+
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
-  const size_t plane = (size_t)m * n * 4 * (mode == kGated ? 2 : outputs);
+  const size_t plane = (size_t)m * ((n + 3) & ~3) * 4 * (mode == kGated ? 2 : outputs);
   // the tile plans split into at most 16, and only products of few tiles
   const size_t most = (size_t)64 << 20;
   return plane * 16 < most ? plane * 16 : most;
@@ -117,9 +128,10 @@ size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, float* partial, size_t partial_bytes,
                        hipStream_t stream) {
-  if (aligned16(mode, p))
-    return launch_gemm_tile(dtype, mode, p, plan_tiles(mode, p, partial_bytes), partial, stream);
-  return dtype == BLOCK_BF16 ? launch_any<BF16>(mode, p, stream) : launch_any<F16>(mode, p, stream);
+  if (!narrow(mode, p))
+    return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, partial_bytes), partial,
+                            stream);
+  return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream) : launch_narrow<F16>(mode, p, stream);
 }
 
 // ------------------------------------------------------------- elementwise --

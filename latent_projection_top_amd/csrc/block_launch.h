@@ -44,14 +44,14 @@ hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, float* partia
 // The area that products of up to `rows` rows can use.
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs);
 
-// Large tiles (aligned operands): shape 0..2 and K split.
+// Tile kernel: shape 0..2 and K split; `aligned`: 16-byte loads fit.
 struct TilePlan {
   int shape;
   int splits;
 };
 TilePlan plan_tiles(Mode mode, const GemmArgs& args, size_t partial_bytes);
-hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, const TilePlan& plan, float* partial,
-                            hipStream_t stream);
+hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, bool aligned, const TilePlan& plan,
+                            float* partial, hipStream_t stream);
 
 // Elementwise first half of the backward passes, and the column sums.
 // out[i] [rows][ld] = dy * s[i]; n columns.

@@ -1,6 +1,5 @@
-// Matrix products of the layer's operators, large tiles: the kernel behind
-// every product whose operands are 16-byte aligned and whose row count makes
-// the matrix cores, not the weights' bandwidth, the bound.
+// Matrix products of the layer's operators: the tile kernel, for row counts
+// that make the matrix cores, not the weights' bandwidth, the bound.
 #include "block_device.h"
 
 namespace block {
@@ -92,7 +91,20 @@ struct Operand {
   static constexpr int kPair = 2048;
 };
 
-template <typename T, int Mode, typename S>
+// `v` moved down by d elements of 16 bits, zeros from above (d >= 8: all).
+__device__ __forceinline__ u32x4 shift_down(u32x4 v, int d) {
+  if (d & 4) v = u32x4{v[2], v[3], 0, 0};
+  if (d & 2) v = u32x4{v[1], v[2], v[3], 0};
+  if (d & 1)
+    v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
+  return d >= 8 ? u32x4{0, 0, 0, 0} : v;
+}
+
+// Direct: operands go from global memory straight to LDS. Otherwise (rows
+// that start at any element, contiguous lengths of any size from 8) they pass
+// through registers: a 16-byte load that would run past a row's end starts
+// earlier and is shifted into place before it is stored to LDS.
+template <typename T, int Mode, typename S, bool Direct>
 __global__ __launch_bounds__(64 * S::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* partial) {
   typedef Operand<Mode != kDw> A;
@@ -127,6 +139,8 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   const int s0 = (int)((int64_t)all * split / splits);
   const int s1 = (int)((int64_t)all * (split + 1) / splits);
   const bool ragged = (p.red & (kStep - 1)) != 0;
+  // the tile reaches past an operand's rows or columns
+  const bool edge = row0 + S::BM > p.m || col0 + kCols > p.n;
 
   // ---- global -> LDS -------------------------------------------------------
   // Rows past the matrix's end repeat its last one and columns its last eight
@@ -141,7 +155,7 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
       const int r = A::row(c, lane), k = A::red(c, lane);
       red_of[i] = k;
       if (Mode != kDw)
-        off[i] = (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + k) * 2u;
+        off[i] = (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + (Direct ? k : 0)) * 2u;
       else
         off[i] = (uint32_t)(k * p.lda + min(row0 + r, p.m - 8)) * 2u;
     } else {
@@ -151,7 +165,7 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
       // gated: 32-column blocks alternate between the two matrices
       if (Mode == kGated) r = 32 * (r >> 6) + (r & 31);
       if (Mode == kDx)
-        off[i] = (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + k) * 2u;
+        off[i] = (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + (Direct ? k : 0)) * 2u;
       else
         off[i] = (uint32_t)(k * p.ldb + min(col0 + r, p.n - 8)) * 2u;
     }
@@ -182,6 +196,49 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     }
   };
 
+  // Through registers: load i of stage s, and its store to LDS. The r of an
+  // r-contiguous piece, the r row of the others, and their first column are
+  // clamped to the matrix; `shift` says by how much on the way to LDS.
+  u32x4 held[2][Direct ? 1 : S::PER];
+  auto fetch = [&](int s, int i) -> u32x4 {
+    const bool is_a = i < S::A_PER;
+    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+    const int seg = s >= per_seg ? 1 : 0;
+    const int ks = s - seg * per_seg;
+    const int64_t k = (int64_t)ks * kStep + red_of[i];
+    const char* base;
+    uint32_t o = off[i];
+    if (is_a ? Mode != kDw : Mode == kDx) {
+      base = is_a ? static_cast<const char*>(p.a[seg]) + row0 * p.lda * 2
+                  : static_cast<const char*>(p.b[seg]) + (int64_t)col0 * p.ldb * 2;
+      o += (uint32_t)min(k, p.red - 8) * 2u;
+    } else {
+      const int64_t ld = is_a ? p.lda : p.ldb;
+      const int mat = Mode == kGated ? ((c >> 1) & 1) : which;
+      base = static_cast<const char*>(is_a ? p.a[0] : p.b[mat]) + (int64_t)ks * (kStep * 2) * ld;
+      o -= (uint32_t)(max(k - (p.red - 1), (int64_t)0) * ld) * 2u;
+    }
+    return reinterpret_cast<const Any16*>(base + o)->v;
+  };
+  auto put = [&](int s, uint32_t buf, int i, u32x4 v) {
+    const bool is_a = i < S::A_PER;
+    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+    const int ks = s >= per_seg ? s - per_seg : s;
+    if (edge || ks == per_seg - 1) {
+      const int64_t k = (int64_t)ks * kStep + red_of[i];
+      if (is_a ? Mode != kDw : Mode == kDx) {
+        v = shift_down(v, (int)min(max(k - (p.red - 8), (int64_t)0), (int64_t)8));
+      } else {
+        int r = is_a ? A::row(c, lane) : B::row(c, lane);
+        if (!is_a && Mode == kGated) r = 32 * (r >> 6) + (r & 31);
+        const int64_t over = is_a ? row0 + r - (p.m - 8) : (int64_t)col0 + r - (p.n - 8);
+        v = shift_down(v, k >= p.red ? 8 : (int)min(max(over, (int64_t)0), (int64_t)8));
+      }
+    }
+    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(buf + (is_a ? 0 : S::A_BYTES) + c * 1024 + lane * 16) =
+        v;
+  };
+
   // ---- LDS -> registers ----------------------------------------------------
   uint32_t a_rd[2], b_rd[2];
 #pragma unroll
@@ -198,132 +255,211 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
 
   // Stage s's MFMAs. Meanwhile the operands of stage s + 1 are read (a[i] as
   // soon as its last MFMA is issued, B into the other register set) and this
-  // wave's loads of stage s + 4 go out, into the buffer of stage s - 1, which
-  // the barrier before this step has freed.
-  auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], uint32_t next, int load, uint32_t load_buf, bool issue) {
+  // wave's loads of stage s + 4 go out. Direct: into the buffer of stage
+  // s - 1, which the barrier before this step has freed. Through registers:
+  // into one of two sets, while the other set, stage s + 3, goes to LDS (into
+  // the buffer of stage s - 2), so that a load has two steps to arrive.
+  auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], u32x4(&in)[Direct ? 1 : S::PER],
+                  u32x4(&out)[Direct ? 1 : S::PER], uint32_t next, int s, uint32_t fill, bool issue, bool write) {
     constexpr int kEvery = S::MT * S::NT / S::PER;
+    if constexpr (!Direct) {
+      if (issue)
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) in[i] = fetch(s + 4, i);
+    }
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) {
         const int n = i * S::NT + j;
-        if (issue && n % kEvery == kEvery / 2) issue_one(load, load_buf, n / kEvery);
+        if (n % kEvery == kEvery / 2) {
+          if constexpr (Direct) {
+            if (issue) issue_one(s + 4, lds0 + fill, n / kEvery);
+          } else {
+            if (write) put(s + 3, lds0 + fill, n / kEvery, out[n / kEvery]);
+          }
+        }
         acc[i][j] = T::mfma(b[j], a[i], acc[i][j]);
       }
       if (i < S::NT) bn[i] = read_b(next, i);
-      if (S::MT < S::NT && i == S::MT - 1)
-#pragma unroll
-        for (int j = S::MT; j < S::NT; ++j) bn[j] = read_b(next, j);
       a[i] = read_a(next, i);
     }
   };
-  // At the end of stage s: stage s + 2 has to be in LDS (at most the loads of
-  // the stages after it still in flight), and every read of stage s's buffer
-  // has to have returned (at most the reads of stage s + 1 outstanding).
+  static_assert(S::MT >= S::NT, "every B operand is read");
+  // At the end of stage s: stage s + 2 has to be in LDS (Direct: at most the
+  // loads of the stages after it still in flight; through registers: it was
+  // stored a step ago), and every read of stage s's buffer has to have
+  // returned (at most the reads of stage s + 1 outstanding).
   constexpr int kLgkm = kReads < 15 ? kReads : 15;
+  // (through registers the compiler waits for its own loads)
+  constexpr int kVm1 = Direct ? S::PER : 63, kVm2 = Direct ? 2 * S::PER : 63, kVm0 = Direct ? 0 : 63;
 
   const int count = s1 - s0;
   if (count > 0) {
+    // the first four stages; through registers: three, and the fourth held
+    if constexpr (Direct) {
 #pragma unroll 1
-    for (int s = 0; s < min(count, 4); ++s)
+      for (int s = 0; s < min(count, 4); ++s)
 #pragma unroll
-      for (int i = 0; i < S::PER; ++i) issue_one(s0 + s, lds0 + s * S::STAGE, i);
+        for (int i = 0; i < S::PER; ++i) issue_one(s0 + s, lds0 + s * S::STAGE, i);
+    } else {
+#pragma unroll 1
+      for (int s = 0; s < min(count, 3); ++s) {
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) held[0][i] = fetch(s0 + s, i);
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) put(s0 + s, lds0 + s * S::STAGE, i, held[0][i]);
+      }
+      if (count > 3)
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) held[1][i] = fetch(s0 + 3, i);
+    }
     if (count >= 4)
-      wait_barrier<2 * S::PER, 0>();
+      wait_barrier<kVm2, 0>();
     else
-      wait_barrier<0, 0>();
+      wait_barrier<kVm0, 0>();
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) a[i] = read_a(lds0, i);
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) b0[j] = read_b(lds0, j);
 
     constexpr uint32_t kEnd = kStages * S::STAGE;
-    uint32_t next = S::STAGE, fill = 4 * S::STAGE;  // buffers of stages s + 1 and s + 4
+    // buffers of stage s + 1, and of stage s + 4 (through registers s + 3)
+    uint32_t next = lds0 + S::STAGE, fill = (Direct ? 4 : 3) * S::STAGE;
     auto advance = [&] {
-      next = next + S::STAGE == kEnd ? 0 : next + S::STAGE;
+      next = next + S::STAGE == lds0 + kEnd ? lds0 : next + S::STAGE;
       fill = fill + S::STAGE == kEnd ? 0 : fill + S::STAGE;
     };
     int s = 0;
     // steady state: two stages a turn (the two B register sets)
 #pragma unroll 1
     for (; s + 5 < count; s += 2) {
-      step(b0, b1, lds0 + next, s0 + s + 4, lds0 + fill, true);
-      wait_barrier<2 * S::PER, kLgkm>();
+      step(b0, b1, held[0], held[1], next, s0 + s, fill, true, true);
+      wait_barrier<kVm2, kLgkm>();
       advance();
-      step(b1, b0, lds0 + next, s0 + s + 5, lds0 + fill, true);
-      wait_barrier<2 * S::PER, kLgkm>();
+      step(b1, b0, held[1], held[0], next, s0 + s + 1, fill, true, true);
+      wait_barrier<kVm2, kLgkm>();
       advance();
     }
-    // the last stages; one more load if an odd number is left
+    // the last stages
 #pragma unroll 1
     for (; s < count; ++s) {
-      const bool issue = s + 4 < count;
-      step(b0, b1, lds0 + next, s0 + s + 4, lds0 + fill, issue);
+      step(b0, b1, held[0], held[1], next, s0 + s, fill, s + 4 < count, s + 3 < count);
       if (s + 2 < count) {
         if (s + 4 < count)
-          wait_barrier<2 * S::PER, kLgkm>();
+          wait_barrier<kVm2, kLgkm>();
         else if (s + 3 < count)
-          wait_barrier<S::PER, kLgkm>();
+          wait_barrier<kVm1, kLgkm>();
         else
-          wait_barrier<0, kLgkm>();
+          wait_barrier<kVm0, kLgkm>();
       }
       advance();
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) b0[j] = b1[j];
+      if constexpr (!Direct) {
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) held[1][i] = held[0][i];
+      }
     }
   }
 
   // lane (g, m) of tile (i, j) holds row 16 i + m, columns 16 j + 4 g .. + 3
+  const int64_t pn = (p.n + 3) & ~3;
+  if (splits > 1) {
+    const int planes = Mode == kGated ? 2 : p.outputs;
 #pragma unroll
-  for (int i = 0; i < S::MT; ++i) {
-    const int64_t row = row0 + 16 * (S::MT * wm + i) + m;
-    constexpr int kJ = Mode == kGated ? S::NT / 2 : S::NT;
+    for (int i = 0; i < S::MT; ++i) {
+      const int64_t row = row0 + 16 * (S::MT * wm + i) + m;
+      constexpr int kJ = Mode == kGated ? S::NT / 2 : S::NT;
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-      const int col = col0 + 16 * (kJ * wn + j) + 4 * g;
-      const f32x4 v = acc[i][j], u = acc[i][Mode == kGated ? S::NT / 2 + j : j];
-      if (splits > 1) {
+      for (int j = 0; j < kJ; ++j) {
+        const int col = col0 + 16 * (kJ * wn + j) + 4 * g;
         if (row < p.m && col < p.n) {
-          const int planes = Mode == kGated ? 2 : p.outputs;
-          float* d = partial + (((int64_t)split * planes + which) * p.m + row) * p.n + col;
-          *reinterpret_cast<f32x4*>(d) = v;
-          if (Mode == kGated) *reinterpret_cast<f32x4*>(d + p.m * p.n) = u;
+          float* d = partial + (((int64_t)split * planes + which) * p.m + row) * pn + col;
+          *reinterpret_cast<f32x4*>(d) = acc[i][j];
+          if (Mode == kGated) *reinterpret_cast<f32x4*>(d + p.m * pn) = acc[i][S::NT / 2 + j];
         }
-      } else {
-        epilogue<T, Mode>(p, which, row, col, v, u);
       }
     }
+    return;
+  }
+  // Each wave turns its sums around in LDS (its own part, so only the first
+  // use waits for the block), 16 * kRows rows at a time, so that a lane ends
+  // eight columns of a row at once: 16-byte accesses to every matrix, whole
+  // lines per row, and the activation's code is there once per turn instead
+  // of once per MFMA tile (32 copies cost the 256 x 256 kernel a fifth of
+  // its time in instruction fetches).
+  constexpr int kPitch = 16 * S::NT + 4;
+  constexpr int kRows = S::NW * 64 * kPitch * 4 <= kStages * S::STAGE ? 4 : 2;
+  static_assert(S::NW * 16 * kRows * kPitch * 4 <= kStages * S::STAGE && S::MT % kRows == 0, "LDS");
+  constexpr int kWide = Mode == kGated ? 8 * S::NT : 16 * S::NT;  // output columns of a wave
+  constexpr int kLanes = kWide / 8;                               // lanes of a row
+  float* turn = reinterpret_cast<float*>(smem) + wave * 16 * kRows * kPitch;
+  const int64_t wrow = row0 + 16 * S::MT * wm + lane / kLanes;
+  const int wcol = 8 * (lane % kLanes);
+  __syncthreads();
+#pragma unroll
+  for (int c = 0; c < S::MT / kRows; ++c) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+#pragma unroll
+      for (int j = 0; j < S::NT; ++j)
+        *reinterpret_cast<f32x4*>(turn + (16 * i + m) * kPitch + 16 * j + 4 * g) = acc[kRows * c + i][j];
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll 2
+    for (int r = 0; r < 16 * kRows; r += 64 / kLanes) {
+      const float* t = turn + (r + lane / kLanes) * kPitch + wcol;
+      float v[8], u[8];
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(t + 4 * q);
+        const f32x4 y = *reinterpret_cast<const f32x4*>(t + 4 * q + (Mode == kGated ? 8 * S::NT : 0));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[4 * q + e] = x[e];
+          u[4 * q + e] = y[e];
+        }
+      }
+      epilogue<T, Mode, 8>(p, which, wrow + 16 * kRows * c + r, col0 + kWide * wn + wcol, v, u);
+    }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 
 // Joins the splits' FP32 sums in split order and ends the product.
 template <typename T, int Mode>
 __global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits, const float* partial) {
-  const int64_t quads = (p.n + 3) / 4;
+  const int64_t pn = (p.n + 3) & ~3, quads = pn / 4;
   const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
   const int planes = Mode == kGated ? 2 : p.outputs;
-  const int64_t plane = p.m * p.n;
+  const int64_t plane = p.m * pn;
   if (id >= quads * p.m * (Mode == kGated ? 1 : planes)) return;
   const int which = (int)(id / (quads * p.m));
   const int64_t q = id - which * quads * p.m;
   const int64_t row = q / quads;
   const int col = (int)(q - row * quads) * 4;
-  const float* d = partial + which * plane + row * p.n + col;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f}, u = v;
+  const float* d = partial + which * plane + row * pn + col;
+  f32x4 vs = {0.f, 0.f, 0.f, 0.f}, us = vs;
   for (int s = 0; s < splits; ++s) {
-    v += *reinterpret_cast<const f32x4*>(d);
-    if (Mode == kGated) u += *reinterpret_cast<const f32x4*>(d + plane);
+    vs += *reinterpret_cast<const f32x4*>(d);
+    if (Mode == kGated) us += *reinterpret_cast<const f32x4*>(d + plane);
     d += planes * plane;
   }
-  epilogue<T, Mode>(p, which, row, col, v, u);
+  float v[4], u[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    v[t] = vs[t];
+    u[t] = us[t];
+  }
+  epilogue<T, Mode, 4>(p, which, row, col, v, u);
 }
 
 template <typename T, int Mode, typename S>
-static hipError_t launch_shape(const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
+static hipError_t launch_shape(const GemmArgs& p, bool aligned, int splits, float* partial, hipStream_t stream) {
   constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;
   const int mt = (int)((p.m + S::BM - 1) / S::BM), nt = (p.n + kCols - 1) / kCols;
   const int64_t blocks = (int64_t)mt * nt * p.outputs * splits;
-  const hipError_t e = launch_kernel(gemm_tile_kernel<T, Mode, S>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
+  const hipError_t e = launch_kernel(aligned ? gemm_tile_kernel<T, Mode, S, true> : gemm_tile_kernel<T, Mode, S, false>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
                                      p, mt, nt, splits, partial);
   if (e != hipSuccess || splits == 1) return e;
   const int64_t items = (int64_t)((p.n + 3) / 4) * p.m * (Mode == kGated ? 1 : p.outputs);
@@ -336,29 +472,29 @@ typedef TileShape<128, 256, 2, 4> Wide;
 typedef TileShape<128, 128, 2, 2> Small;
 
 template <typename T, int Mode>
-static hipError_t launch_mode(const GemmArgs& p, const TilePlan& t, float* partial, hipStream_t stream) {
+static hipError_t launch_mode(const GemmArgs& p, bool aligned, const TilePlan& t, float* partial, hipStream_t stream) {
   switch (t.shape) {
-    case 0: return launch_shape<T, Mode, Large>(p, t.splits, partial, stream);
-    case 1: return launch_shape<T, Mode, Wide>(p, t.splits, partial, stream);
-    default: return launch_shape<T, Mode, Small>(p, t.splits, partial, stream);
+    case 0: return launch_shape<T, Mode, Large>(p, aligned, t.splits, partial, stream);
+    case 1: return launch_shape<T, Mode, Wide>(p, aligned, t.splits, partial, stream);
+    default: return launch_shape<T, Mode, Small>(p, aligned, t.splits, partial, stream);
   }
 }
 
 template <typename T>
-static hipError_t launch_typed(Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
+static hipError_t launch_typed(Mode mode, const GemmArgs& p, bool aligned, const TilePlan& t, float* partial,
                                hipStream_t stream) {
   switch (mode) {
-    case kLinear: return launch_mode<T, kLinear>(p, t, partial, stream);
-    case kGated: return launch_mode<T, kGated>(p, t, partial, stream);
-    case kDx: return launch_mode<T, kDx>(p, t, partial, stream);
-    default: return launch_mode<T, kDw>(p, t, partial, stream);
+    case kLinear: return launch_mode<T, kLinear>(p, aligned, t, partial, stream);
+    case kGated: return launch_mode<T, kGated>(p, aligned, t, partial, stream);
+    case kDx: return launch_mode<T, kDx>(p, aligned, t, partial, stream);
+    default: return launch_mode<T, kDw>(p, aligned, t, partial, stream);
   }
 }
 
-hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
+hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, bool aligned, const TilePlan& t, float* partial,
                             hipStream_t stream) {
-  return dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, t, partial, stream)
-                             : launch_typed<F16>(mode, p, t, partial, stream);
+  return dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, aligned, t, partial, stream)
+                             : launch_typed<F16>(mode, p, aligned, t, partial, stream);
 }
 
 // Tile shape and K split of a product: the one whose time a simple model puts
@@ -376,7 +512,7 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
     // microseconds of one stage of a block that has its CU to itself
     const double stage = 0.6 * shapes[k].bm * shapes[k].bn / 65536.0 / shapes[k].rate;
     for (int s = 1; s <= 16; ++s) {
-      const double bytes = 4.0 * p.m * p.n * planes * s;
+      const double bytes = 4.0 * p.m * ((p.n + 3) & ~3) * planes * s;
       if (s > 1 && (bytes > (double)partial_bytes || steps / s < 8 || (p.n & 3) != 0)) break;
       const double slots = 256.0 * shapes[k].per_cu;
       const double blocks = tiles * s;
