@@ -13,7 +13,7 @@ import ctypes
 
 import torch
 
-from .route import LIB, OK, RouteError, _stream
+from .route import LIB, OK, RouteError
 
 ABI_VERSION = 1
 MAX_ROWS = 1 << 20
@@ -97,11 +97,11 @@ class _Plan:
         self.handle = handle
         self.rows = cfg.rows
         self.device = cfg.device
-        self.workspace_bytes = int(getattr(LIB, f"block_{self.OP}_workspace_bytes")(handle))
+        self.workspace_bytes = max(int(getattr(LIB, f"block_{self.OP}_workspace_bytes")(handle)), 256)
 
     def new_workspace(self) -> torch.Tensor:
         """A zero-filled workspace tensor of the size this plan needs."""
-        return torch.zeros(max(self.workspace_bytes, 256), dtype=torch.uint8, device=f"cuda:{self.device}")
+        return torch.zeros(self.workspace_bytes, dtype=torch.uint8, device=f"cuda:{self.device}")
 
     def close(self) -> None:
         if getattr(self, "handle", 0):
@@ -161,61 +161,77 @@ class LinearPlan(_Plan):
                                    _code(ACTIVATIONS, activation, "activation"), int(self.training)))
 
 
+# The checks run on every call, in front of kernels of a few microseconds, so
+# they read each property of a tensor once.
+
+
 def _check(t: torch.Tensor, dtype, plan: _Plan, name: str) -> None:
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: expected {dtype}, got {t.dtype}")
-    if not t.is_cuda:
-        raise ValueError(f"{name}: must be a device tensor")
-    if t.device.index != plan.device:
-        raise ValueError(f"{name}: on cuda:{t.device.index}, the plan is for cuda:{plan.device}")
+    if t.get_device() != plan.device:
+        raise ValueError(f"{name}: on {t.device}, the plan is for cuda:{plan.device}")
 
 
 def _rows_of(t, dtype, plan: _Plan, rows: int, width: int, name: str) -> tuple[int | None, int]:
     """Pointer and row stride of a matrix of rows; None gives (NULL, width)."""
     if t is None:
         return None, width
-    _check(t, dtype, plan, name)
-    if t.dim() != 2 or t.shape[1] != width:
-        raise ValueError(f"{name}: expected [rows][{width}], got {tuple(t.shape)}")
-    if t.shape[0] < rows:
-        raise ValueError(f"{name}: needs at least {rows} rows, has {t.shape[0]}")
-    if width > 1 and rows > 0 and t.stride(1) != 1:
+    if t.dtype is not dtype or t.get_device() != plan.device:
+        _check(t, dtype, plan, name)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or shape[1] != width:
+        raise ValueError(f"{name}: expected [rows][{width}], got {tuple(shape)}")
+    if shape[0] < rows:
+        raise ValueError(f"{name}: needs at least {rows} rows, has {shape[0]}")
+    if strides[1] != 1 and width > 1 and rows > 0:
         raise ValueError(f"{name}: the values of a row must be adjacent")
-    # the stride of a single row is never used
-    if rows > 1 and t.stride(0) < width:
-        raise ValueError(f"{name}: rows overlap (row stride {t.stride(0)}, width {width})")
-    return t.data_ptr() or None, (t.stride(0) if rows > 1 else width)
+    if rows <= 1:  # the stride of a single row is never used
+        return t.data_ptr(), width
+    if strides[0] < width:
+        raise ValueError(f"{name}: rows overlap (row stride {strides[0]}, width {width})")
+    return t.data_ptr(), strides[0]
 
 
 def _dense(t, dtype, plan: _Plan, shape, name: str) -> int | None:
-    """Pointer of a contiguous tensor; its first dimension may be longer when
-    the shape has two (spare rows)."""
+    """Pointer of a contiguous tensor of exactly this shape."""
     if t is None:
         return None
-    _check(t, dtype, plan, name)
+    if t.dtype is not dtype or t.get_device() != plan.device:
+        _check(t, dtype, plan, name)
+    if t.shape != shape:
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    return t.data_ptr() or None
+    return t.data_ptr()
 
 
 def _per_row(t, dtype, plan: _Plan, shape, name: str) -> int | None:
-    """Like _dense for outputs kept per row: spare rows at the end are allowed."""
+    """Like _dense for what is kept per row: spare rows at the end are allowed."""
     if t is not None and t.dim() == len(shape) and t.shape[0] > shape[0]:
         t = t[:shape[0]]
     return _dense(t, dtype, plan, shape, name)
 
 
 def _workspace(plan: _Plan, workspace) -> int:
-    _check(workspace, torch.uint8, plan, "workspace")
-    if not workspace.is_contiguous() or workspace.numel() < max(plan.workspace_bytes, 256):
-        raise ValueError(f"workspace: needs {max(plan.workspace_bytes, 256)} contiguous bytes")
+    if workspace.dtype is not torch.uint8 or workspace.get_device() != plan.device:
+        _check(workspace, torch.uint8, plan, "workspace")
+    if workspace.numel() < plan.workspace_bytes or not workspace.is_contiguous():
+        raise ValueError(f"workspace: needs {plan.workspace_bytes} contiguous bytes")
     return workspace.data_ptr()
 
 
-def _run(name: str, plan: _Plan, *args) -> None:
-    st = getattr(LIB, name)(plan.handle, *args)
+def _stream(plan: _Plan, stream) -> int | None:
+    if stream is not None:
+        return stream.cuda_stream or None
+    return _current_stream(plan.device) or None
+
+
+# the current stream's handle alone (torch.cuda.current_stream builds an object)
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _run(fn, name: str, plan: _Plan, *args) -> None:
+    st = fn(plan.handle, *args)
     if st != OK:
         raise RouteError(st, name)
 
@@ -226,10 +242,10 @@ def layer_norm(plan: NormPlan, x, weight, bias, y, mean=None, rstd=None, rows: i
     and rstd (FP32, one per row) are kept for layer_norm_backward if given."""
     rows = x.shape[0] if rows is None else rows
     dt, pdt, w = plan.dtype, plan.param_dtype, plan.width
-    _run("block_norm", plan, *_rows_of(x, dt, plan, rows, w, "x"),
+    _run(LIB.block_norm, "block_norm", plan, *_rows_of(x, dt, plan, rows, w, "x"),
          _dense(weight, pdt, plan, (w,), "weight"), _dense(bias, pdt, plan, (w,), "bias"),
          *_rows_of(y, dt, plan, rows, w, "y"), _per_row(mean, torch.float32, plan, (rows,), "mean"),
-         _per_row(rstd, torch.float32, plan, (rows,), "rstd"), rows, _stream(stream))
+         _per_row(rstd, torch.float32, plan, (rows,), "rstd"), rows, _stream(plan, stream))
 
 
 def layer_norm_backward(plan: NormPlan, dy, x, weight, mean, rstd, dx, dweight, dbias, workspace,
@@ -237,12 +253,12 @@ def layer_norm_backward(plan: NormPlan, dy, x, weight, mean, rstd, dx, dweight, 
     """Gradients of layer_norm; dx, dweight or dbias None is not computed."""
     rows = dy.shape[0] if rows is None else rows
     dt, pdt, w = plan.dtype, plan.param_dtype, plan.width
-    _run("block_norm_backward", plan, *_rows_of(dy, dt, plan, rows, w, "dy"),
+    _run(LIB.block_norm_backward, "block_norm_backward", plan, *_rows_of(dy, dt, plan, rows, w, "dy"),
          *_rows_of(x, dt, plan, rows, w, "x"), _dense(weight, pdt, plan, (w,), "weight"),
          _per_row(mean, torch.float32, plan, (rows,), "mean"),
          _per_row(rstd, torch.float32, plan, (rows,), "rstd"), *_rows_of(dx, dt, plan, rows, w, "dx"),
          _dense(dweight, pdt, plan, (w,), "dweight"), _dense(dbias, pdt, plan, (w,), "dbias"),
-         _workspace(plan, workspace), rows, _stream(stream))
+         _workspace(plan, workspace), rows, _stream(plan, stream))
 
 
 def gated(plan: GatedPlan, x, w_gate, w_up, h, workspace, d_gate=None, d_up=None, rows: int | None = None,
@@ -251,10 +267,10 @@ def gated(plan: GatedPlan, x, w_gate, w_up, h, workspace, d_gate=None, d_up=None
     derivatives of h by the two products, for gated_backward."""
     rows = x.shape[0] if rows is None else rows
     dt, k, n = plan.dtype, plan.inputs, plan.inner
-    _run("block_gated", plan, *_rows_of(x, dt, plan, rows, k, "x"),
+    _run(LIB.block_gated, "block_gated", plan, *_rows_of(x, dt, plan, rows, k, "x"),
          _dense(w_gate, dt, plan, (k, n), "w_gate"), _dense(w_up, dt, plan, (k, n), "w_up"),
          *_rows_of(h, dt, plan, rows, n, "h"), _per_row(d_gate, dt, plan, (rows, n), "d_gate"),
-         _per_row(d_up, dt, plan, (rows, n), "d_up"), _workspace(plan, workspace), rows, _stream(stream))
+         _per_row(d_up, dt, plan, (rows, n), "d_up"), _workspace(plan, workspace), rows, _stream(plan, stream))
 
 
 def gated_backward(plan: GatedPlan, dh, x, w_gate, w_up, d_gate, d_up, dx, dw_gate, dw_up, workspace,
@@ -262,12 +278,12 @@ def gated_backward(plan: GatedPlan, dh, x, w_gate, w_up, d_gate, d_up, dx, dw_ga
     """Gradients of gated; dx None, or dw_gate and dw_up None, is not computed."""
     rows = dh.shape[0] if rows is None else rows
     dt, k, n = plan.dtype, plan.inputs, plan.inner
-    _run("block_gated_backward", plan, *_rows_of(dh, dt, plan, rows, n, "dh"),
+    _run(LIB.block_gated_backward, "block_gated_backward", plan, *_rows_of(dh, dt, plan, rows, n, "dh"),
          *_rows_of(x, dt, plan, rows, k, "x"), _dense(w_gate, dt, plan, (k, n), "w_gate"),
          _dense(w_up, dt, plan, (k, n), "w_up"), _per_row(d_gate, dt, plan, (rows, n), "d_gate"),
          _per_row(d_up, dt, plan, (rows, n), "d_up"), *_rows_of(dx, dt, plan, rows, k, "dx"),
          _dense(dw_gate, dt, plan, (k, n), "dw_gate"), _dense(dw_up, dt, plan, (k, n), "dw_up"),
-         _workspace(plan, workspace), rows, _stream(stream))
+         _workspace(plan, workspace), rows, _stream(plan, stream))
 
 
 def linear(plan: LinearPlan, x, w, y, workspace, bias=None, residual=None, slope=None,
@@ -276,10 +292,10 @@ def linear(plan: LinearPlan, x, w, y, workspace, bias=None, residual=None, slope
     training with an activation, `slope` receives act' for linear_backward."""
     rows = x.shape[0] if rows is None else rows
     dt, k, n = plan.dtype, plan.inputs, plan.outputs
-    _run("block_linear", plan, *_rows_of(x, dt, plan, rows, k, "x"), _dense(w, dt, plan, (k, n), "w"),
+    _run(LIB.block_linear, "block_linear", plan, *_rows_of(x, dt, plan, rows, k, "x"), _dense(w, dt, plan, (k, n), "w"),
          _dense(bias, dt, plan, (n,), "bias"), *_rows_of(residual, dt, plan, rows, n, "residual"),
          *_rows_of(y, dt, plan, rows, n, "y"), _per_row(slope, dt, plan, (rows, n), "slope"),
-         _workspace(plan, workspace), rows, _stream(stream))
+         _workspace(plan, workspace), rows, _stream(plan, stream))
 
 
 def linear_backward(plan: LinearPlan, dy, x, w, slope, dx, dw, dbias, workspace, rows: int | None = None,
@@ -288,8 +304,8 @@ def linear_backward(plan: LinearPlan, dy, x, w, slope, dx, dw, dbias, workspace,
     is not computed. `slope` is None when the plan has no activation."""
     rows = dy.shape[0] if rows is None else rows
     dt, k, n = plan.dtype, plan.inputs, plan.outputs
-    _run("block_linear_backward", plan, *_rows_of(dy, dt, plan, rows, n, "dy"),
+    _run(LIB.block_linear_backward, "block_linear_backward", plan, *_rows_of(dy, dt, plan, rows, n, "dy"),
          *_rows_of(x, dt, plan, rows, k, "x"), _dense(w, dt, plan, (k, n), "w"),
          _per_row(slope, dt, plan, (rows, n), "slope"), *_rows_of(dx, dt, plan, rows, k, "dx"),
          _dense(dw, dt, plan, (k, n), "dw"), _dense(dbias, dt, plan, (n,), "dbias"),
-         _workspace(plan, workspace), rows, _stream(stream))
+         _workspace(plan, workspace), rows, _stream(plan, stream))

@@ -92,7 +92,7 @@ int block_norm_prepare(const block_norm_config* cfg, block_norm_plan** out) {
   if (int st = find_device(cfg->device)) return st;
   block_norm_plan* p = new_plan<block_norm_plan>(*cfg);
   if (p == nullptr) return ROUTE_E_ARG;
-  p->ws_bytes = round256(block::norm_backward_bytes(cfg->rows, cfg->width));
+  p->ws_bytes = round256(block::norm_backward_bytes(cfg->dtype, cfg->rows, cfg->width));
   *out = p;
   return ROUTE_OK;
 }

@@ -105,6 +105,53 @@ static hipError_t launch_narrow(Mode mode, const GemmArgs& p, hipStream_t stream
   }
 }
 
+// Joins the splits' FP32 sums in split order and ends the product.
+template <typename T, int Mode>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits, const float* partial) {
+  const int64_t pn = (p.n + 3) & ~3, quads = pn / 4;
+  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int planes = Mode == kGated ? 2 : p.outputs;
+  const int64_t plane = p.m * pn;
+  if (id >= quads * p.m * (Mode == kGated ? 1 : planes)) return;
+  const int which = (int)(id / (quads * p.m));
+  const int64_t q = id - which * quads * p.m;
+  const int64_t row = q / quads;
+  const int col = (int)(q - row * quads) * 4;
+  const float* d = partial + which * plane + row * pn + col;
+  f32x4 vs = {0.f, 0.f, 0.f, 0.f}, us = vs;
+  #pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    vs += *reinterpret_cast<const f32x4*>(d);
+    if (Mode == kGated) us += *reinterpret_cast<const f32x4*>(d + plane);
+    d += planes * plane;
+  }
+  float v[4], u[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    v[t] = vs[t];
+    u[t] = us[t];
+  }
+  epilogue<T, Mode, 4>(p, which, row, col, v, u);
+}
+
+template <typename T>
+static hipError_t join_typed(Mode mode, const GemmArgs& p, int splits, const float* partial, hipStream_t stream) {
+  const int64_t items = (int64_t)((p.n + 3) / 4) * p.m * (mode == kGated ? 1 : p.outputs);
+  const dim3 grid((unsigned)((items + 255) / 256));
+  switch (mode) {
+    case kLinear: return launch_kernel(gemm_join_kernel<T, kLinear>, grid, dim3(256), stream, p, splits, partial);
+    case kGated: return launch_kernel(gemm_join_kernel<T, kGated>, grid, dim3(256), stream, p, splits, partial);
+    case kDx: return launch_kernel(gemm_join_kernel<T, kDx>, grid, dim3(256), stream, p, splits, partial);
+    default: return launch_kernel(gemm_join_kernel<T, kDw>, grid, dim3(256), stream, p, splits, partial);
+  }
+}
+
+hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& p, int splits, const float* partial,
+                            hipStream_t stream) {
+  return dtype == BLOCK_BF16 ? join_typed<BF16>(mode, p, splits, partial, stream)
+                             : join_typed<F16>(mode, p, splits, partial, stream);
+}
+
 // Asynchronous 16-byte loads: every row of every operand starts on a 16-byte
 // boundary and its contiguous length is a multiple of 8.
 static bool aligned16(Mode mode, const GemmArgs& p) {
@@ -121,17 +168,19 @@ static bool narrow(Mode mode, const GemmArgs& p) {
 
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
   const size_t plane = (size_t)m * ((n + 3) & ~3) * 4 * (mode == kGated ? 2 : outputs);
-  // the tile plans split into at most 16, and only products of few tiles
+  // at most 64 splits, and only products of few tiles are split
   const size_t most = (size_t)64 << 20;
-  return plane * 16 < most ? plane * 16 : most;
+  return plane * 64 < most ? plane * 64 : most;
 }
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, float* partial, size_t partial_bytes,
                        hipStream_t stream) {
-  if (!narrow(mode, p))
-    return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, partial_bytes), partial,
+  if (narrow(mode, p)) return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream)
+                                                  : launch_narrow<F16>(mode, p, stream);
+  if (mode != kDw && p.m <= kStreamRows)
+    return launch_gemm_stream(dtype, mode, p, partial, partial_bytes, stream);
+  return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, partial_bytes), partial,
                             stream);
-  return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream) : launch_narrow<F16>(mode, p, stream);
 }
 
 // ------------------------------------------------------------- elementwise --

@@ -53,6 +53,16 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& args, size_t partial_bytes);
 hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, bool aligned, const TilePlan& plan,
                             float* partial, hipStream_t stream);
 
+// Adds the splits' sums [splits][planes][m][n rounded up to 4] in split order
+// and ends the product (planes: 2 for kGated, else `outputs`).
+hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& args, int splits, const float* partial,
+                            hipStream_t stream);
+
+// At most kStreamRows rows; not kDw.
+constexpr int kStreamRows = 32;
+hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& args, float* partial, size_t partial_bytes,
+                              hipStream_t stream);
+
 // Elementwise first half of the backward passes, and the column sums.
 // out[i] [rows][ld] = dy * s[i]; n columns.
 hipError_t launch_scale(int dtype, const void* dy, int64_t dy_stride, const void* const* s, int count,
@@ -83,6 +93,6 @@ struct NormArgs {
 
 hipError_t launch_norm(int dtype, const NormArgs& args, hipStream_t stream);
 hipError_t launch_norm_backward(int dtype, const NormArgs& args, hipStream_t stream);
-size_t norm_backward_bytes(int64_t rows, int width);
+size_t norm_backward_bytes(int dtype, int64_t rows, int width);
 
 }  // namespace block

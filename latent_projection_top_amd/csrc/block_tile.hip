@@ -426,34 +426,6 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   }
 }
 
-// Joins the splits' FP32 sums in split order and ends the product.
-template <typename T, int Mode>
-__global__ __launch_bounds__(256) void gemm_join_kernel(GemmArgs p, int splits, const float* partial) {
-  const int64_t pn = (p.n + 3) & ~3, quads = pn / 4;
-  const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int planes = Mode == kGated ? 2 : p.outputs;
-  const int64_t plane = p.m * pn;
-  if (id >= quads * p.m * (Mode == kGated ? 1 : planes)) return;
-  const int which = (int)(id / (quads * p.m));
-  const int64_t q = id - which * quads * p.m;
-  const int64_t row = q / quads;
-  const int col = (int)(q - row * quads) * 4;
-  const float* d = partial + which * plane + row * pn + col;
-  f32x4 vs = {0.f, 0.f, 0.f, 0.f}, us = vs;
-  for (int s = 0; s < splits; ++s) {
-    vs += *reinterpret_cast<const f32x4*>(d);
-    if (Mode == kGated) us += *reinterpret_cast<const f32x4*>(d + plane);
-    d += planes * plane;
-  }
-  float v[4], u[4];
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    v[t] = vs[t];
-    u[t] = us[t];
-  }
-  epilogue<T, Mode, 4>(p, which, row, col, v, u);
-}
-
 template <typename T, int Mode, typename S>
 static hipError_t launch_shape(const GemmArgs& p, bool aligned, int splits, float* partial, hipStream_t stream) {
   constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;
@@ -462,9 +434,7 @@ static hipError_t launch_shape(const GemmArgs& p, bool aligned, int splits, floa
   const hipError_t e = launch_kernel(aligned ? gemm_tile_kernel<T, Mode, S, true> : gemm_tile_kernel<T, Mode, S, false>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
                                      p, mt, nt, splits, partial);
   if (e != hipSuccess || splits == 1) return e;
-  const int64_t items = (int64_t)((p.n + 3) / 4) * p.m * (Mode == kGated ? 1 : p.outputs);
-  return launch_kernel(gemm_join_kernel<T, Mode>, dim3((unsigned)((items + 255) / 256)), dim3(256), stream, p,
-                       splits, static_cast<const float*>(partial));
+  return launch_gemm_join(T::code, (enum Mode)Mode, p, splits, partial, stream);
 }
 
 typedef TileShape<256, 256, 2, 4> Large;
