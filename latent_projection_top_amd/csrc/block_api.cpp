@@ -17,8 +17,8 @@ struct block_norm_plan {
   size_t ws_bytes;
 };
 
-// Workspace of the matrix operators: [0, off_dz) the products' counters and
-// partial sums; then dz (linear) or dg and du (gated) with their rows padded
+// Workspace of the matrix operators: the products' counters, their split sums
+// (up to off_dz), then dz (linear) or dg and du (gated) with their rows padded
 // to a multiple of 8 elements, and the partial column sums of dbias.
 struct block_gated_plan {
   block_gated_config cfg;
@@ -65,6 +65,13 @@ size_t partial_area(block::Mode mode, int64_t rows, int k, int n, int outputs, b
     b = std::max(b, block::gemm_partial_bytes(block::kDw, k, n, outputs));
   }
   return round256(b);
+}
+
+template <typename Plan>
+block::Workspace products(const Plan* plan, void* workspace) {
+  char* base = static_cast<char*>(workspace);
+  return block::Workspace{reinterpret_cast<uint32_t*>(base), reinterpret_cast<float*>(base + block::kCounterBytes),
+                          plan->partial_bytes};
 }
 
 template <typename Plan, typename Config>
@@ -184,7 +191,7 @@ int block_gated_prepare(const block_gated_config* cfg, block_gated_plan** out) {
   if (p == nullptr) return ROUTE_E_ARG;
   p->partial_bytes = partial_area(block::kGated, cfg->rows, cfg->inputs, cfg->inner, 2, cfg->training != 0);
   const size_t dz = cfg->training ? round256((size_t)cfg->rows * padded(cfg->inner) * 2) : 0;
-  p->off_dz = p->partial_bytes;
+  p->off_dz = block::kCounterBytes + p->partial_bytes;
   p->off_du = p->off_dz + dz;
   p->ws_bytes = p->off_du + dz;
   *out = p;
@@ -221,8 +228,8 @@ int block_gated(const block_gated_plan* plan, const void* x, int64_t x_stride, c
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
-  return status_of(block::launch_gemm(c.dtype, block::kGated, a, static_cast<float*>(workspace),
-                                      plan->partial_bytes, static_cast<hipStream_t>(stream)));
+  return status_of(block::launch_gemm(c.dtype, block::kGated, a, products(plan, workspace),
+                                      static_cast<hipStream_t>(stream)));
 }
 
 int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t dh_stride, const void* x,
@@ -263,7 +270,7 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
     a.red = c.inner;
     a.segments = 2;
     a.outputs = 1;
-    st = status_of(block::launch_gemm(c.dtype, block::kDx, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
+    st = status_of(block::launch_gemm(c.dtype, block::kDx, a, products(plan, workspace), s));
     if (st != ROUTE_OK) return st;
   }
   if (dw_gate == nullptr) return ROUTE_OK;
@@ -281,7 +288,7 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   a.red = rows;
   a.segments = 1;
   a.outputs = 2;
-  return status_of(block::launch_gemm(c.dtype, block::kDw, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, products(plan, workspace), s));
 }
 
 void block_gated_destroy(block_gated_plan* plan) { delete plan; }
@@ -302,7 +309,7 @@ int block_linear_prepare(const block_linear_config* cfg, block_linear_plan** out
   if (p == nullptr) return ROUTE_E_ARG;
   const bool dz = cfg->training && cfg->activation != BLOCK_ACT_NONE;
   p->partial_bytes = partial_area(block::kLinear, cfg->rows, cfg->inputs, cfg->outputs, 1, cfg->training != 0);
-  p->off_dz = p->partial_bytes;
+  p->off_dz = block::kCounterBytes + p->partial_bytes;
   p->off_sum = p->off_dz + (dz ? round256((size_t)cfg->rows * padded(cfg->outputs) * 2) : 0);
   p->ws_bytes = p->off_sum + (cfg->training ? round256(block::column_sum_bytes(cfg->rows, cfg->outputs)) : 0);
   *out = p;
@@ -342,8 +349,8 @@ int block_linear(const block_linear_plan* plan, const void* x, int64_t x_stride,
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
-  return status_of(block::launch_gemm(c.dtype, block::kLinear, a, static_cast<float*>(workspace),
-                                      plan->partial_bytes, static_cast<hipStream_t>(stream)));
+  return status_of(block::launch_gemm(c.dtype, block::kLinear, a, products(plan, workspace),
+                                      static_cast<hipStream_t>(stream)));
 }
 
 int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t dy_stride, const void* x,
@@ -390,7 +397,7 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
     a.n = c.inputs;
     a.red = c.outputs;
     a.segments = a.outputs = 1;
-    const int st = status_of(block::launch_gemm(c.dtype, block::kDx, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
+    const int st = status_of(block::launch_gemm(c.dtype, block::kDx, a, products(plan, workspace), s));
     if (st != ROUTE_OK) return st;
   }
   if (dw == nullptr) return ROUTE_OK;
@@ -405,7 +412,7 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   a.n = c.outputs;
   a.red = rows;
   a.segments = a.outputs = 1;
-  return status_of(block::launch_gemm(c.dtype, block::kDw, a, reinterpret_cast<float*>(ws), plan->partial_bytes, s));
+  return status_of(block::launch_gemm(c.dtype, block::kDw, a, products(plan, workspace), s));
 }
 
 void block_linear_destroy(block_linear_plan* plan) { delete plan; }

@@ -168,19 +168,18 @@ static bool narrow(Mode mode, const GemmArgs& p) {
 
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
   const size_t plane = (size_t)m * ((n + 3) & ~3) * 4 * (mode == kGated ? 2 : outputs);
-  // at most 64 splits, and only products of few tiles are split
+  // only products of few tiles are split
   const size_t most = (size_t)64 << 20;
-  return plane * 64 < most ? plane * 64 : most;
+  return plane * kMaxSplits < most ? plane * kMaxSplits : most;
 }
 
-hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, float* partial, size_t partial_bytes,
-                       hipStream_t stream) {
+hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, const Workspace& ws, hipStream_t stream) {
   if (narrow(mode, p)) return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream)
                                                   : launch_narrow<F16>(mode, p, stream);
   if (mode != kDw && p.m <= kStreamRows)
-    return launch_gemm_stream(dtype, mode, p, partial, partial_bytes, stream);
-  return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, partial_bytes), partial,
-                            stream);
+    return launch_gemm_stream(dtype, mode, p, ws, stream);
+  return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, ws.partial_bytes), ws.partial,
+                          stream);
 }
 
 // ------------------------------------------------------------- elementwise --

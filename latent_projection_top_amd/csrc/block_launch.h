@@ -38,10 +38,18 @@ struct GemmArgs {
   int act;
 };
 
-// partial: the workspace's area for split sums (partial_bytes of it).
-hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, float* partial, size_t partial_bytes,
-                       hipStream_t stream);
-// The area that products of up to `rows` rows can use.
+// What a product uses of its operator's workspace: a counter per column tile,
+// 64 bytes apart, zero between calls, and an area for split sums.
+struct Workspace {
+  uint32_t* counters;
+  float* partial;
+  size_t partial_bytes;
+};
+constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 128) * 64;
+constexpr int kMaxSplits = 64;
+
+hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
+// The area that products of up to m rows can use for split sums.
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs);
 
 // Tile kernel: shape 0..2 and K split; `aligned`: 16-byte loads fit.
@@ -60,8 +68,7 @@ hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& args, int spli
 
 // At most kStreamRows rows; not kDw.
 constexpr int kStreamRows = 32;
-hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& args, float* partial, size_t partial_bytes,
-                              hipStream_t stream);
+hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
 
 // Elementwise first half of the backward passes, and the column sums.
 // out[i] [rows][ld] = dy * s[i]; n columns.

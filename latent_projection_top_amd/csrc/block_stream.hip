@@ -6,8 +6,10 @@
 // registers (8 loads of 16 bytes per lane, the next step's under way while
 // this one is multiplied), and multiplies on the matrix cores with the rows
 // padded to 16. The eight waves of a block take its steps in turn and their
-// sums meet in LDS; with few column tiles the reduction is also split over
-// blocks and joined by a second kernel.
+// sums meet in LDS. With few column tiles the reduction is also split over
+// blocks: their FP32 sums go through the workspace and are added in split
+// order, by the last block of a tile to arrive where they are few (Join), by
+// a second kernel where they are many.
 //
 // Weights with contiguous columns ([K][N], forward): lane (g, m) loads rows
 // 8 g .. 8 g + 7 of columns 8 m .. 8 m + 7 (256-byte segments) and transposes
@@ -15,6 +17,8 @@
 // Weights with a contiguous reduction (backward, W^T): lane (g, m) loads
 // 8 values of columns 8 m + c, c = 0..7, which are the fragments as they are.
 #include "block_device.h"
+
+#include <algorithm>
 
 namespace block {
 
@@ -34,8 +38,25 @@ __device__ __forceinline__ u32x4 drop_low(u32x4 v, int d) {
 
 __device__ __forceinline__ u32x4 load16(const uint16_t* p) { return reinterpret_cast<const Any16*>(p)->v; }
 
-template <typename T, int Mode, int RT>
-__global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, int splits, float* partial) {
+// Partial sums between blocks of one launch: relaxed device-scope atomics,
+// which go past the XCDs' L2s both ways, so that no fence has to write a
+// whole L2 back. A block waits for its stores before it counts itself in.
+__device__ __forceinline__ void put4(float* p, float a, float b, float c, float d) {
+  auto pair = [](float lo, float hi) { return (uint64_t)__float_as_uint(hi) << 32 | __float_as_uint(lo); };
+  uint64_t* q = reinterpret_cast<uint64_t*>(p);
+  __hip_atomic_store(q, pair(a, b), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(q + 1, pair(c, d), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void get2(const float* p, float& a, float& b) {
+  const uint64_t v = __hip_atomic_load(reinterpret_cast<uint64_t*>(const_cast<float*>(p)), __ATOMIC_RELAXED,
+                                       __HIP_MEMORY_SCOPE_AGENT);
+  a = __uint_as_float((uint32_t)v);
+  b = __uint_as_float((uint32_t)(v >> 32));
+}
+
+template <typename T, int Mode, int RT, bool Join>
+__global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, int splits, float* partial,
+                                                                  uint32_t* counters) {
   constexpr bool kTurn = Mode != kDx;                  // weights need the transpose
   constexpr int kTeam = Mode == kGated ? kWaves / 2 : kWaves;  // waves of one matrix
   __shared__ __attribute__((aligned(16))) float part[kWaves][16 * RT][kPart];
@@ -177,48 +198,136 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
         if (col + 4 * q >= p.n) break;
-        *reinterpret_cast<f32x4*>(d + 4 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
-        if (Mode == kGated)
-          *reinterpret_cast<f32x4*>(d + p.m * pn + 4 * q) =
-              f32x4{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]};
+        if constexpr (Join) {
+          put4(d + 4 * q, v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]);
+          if (Mode == kGated) put4(d + p.m * pn + 4 * q, u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]);
+        } else {
+          *reinterpret_cast<f32x4*>(d + 4 * q) = f32x4{v[4 * q], v[4 * q + 1], v[4 * q + 2], v[4 * q + 3]};
+          if (Mode == kGated)
+            *reinterpret_cast<f32x4*>(d + p.m * pn + 4 * q) =
+                f32x4{u[4 * q], u[4 * q + 1], u[4 * q + 2], u[4 * q + 3]};
+        }
       }
     } else {
       epilogue<T, Mode, 8>(p, 0, row, col, v, u);
     }
   }
-}
-
-template <typename T, int Mode>
-static hipError_t launch_rows(const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
-  const dim3 grid((p.n + kCols - 1) / kCols, splits), block(64 * kWaves);
-  if (p.m <= 16) return launch_kernel(gemm_stream_kernel<T, Mode, 1>, grid, block, stream, p, splits, partial);
-  return launch_kernel(gemm_stream_kernel<T, Mode, 2>, grid, block, stream, p, splits, partial);
-}
-
-template <typename T>
-static hipError_t launch_typed(Mode mode, const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
-  switch (mode) {
-    case kLinear: return launch_rows<T, kLinear>(p, splits, partial, stream);
-    case kGated: return launch_rows<T, kGated>(p, splits, partial, stream);
-    default: return launch_rows<T, kDx>(p, splits, partial, stream);
+  if constexpr (Join) {
+    // The tile's last block adds the splits' sums. Its counter goes back to
+    // zero for the next call.
+    __shared__ uint32_t arrived;
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's sums are out
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      uint32_t* c = counters + 16 * tile;
+      arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (arrived == (uint32_t)splits - 1) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (arrived != (uint32_t)splits - 1) return;
+    constexpr int kPlanes = Mode == kGated ? 2 : 1;
+    for (int id = threadIdx.x; id < (int)p.m * (kCols / 4); id += 64 * kWaves) {
+      const int row = id / (kCols / 4), col = col0 + 4 * (id % (kCols / 4));
+      if (col >= p.n) continue;
+      const float* d = partial + (int64_t)row * pn + col;
+      float v[4] = {}, u[4] = {};
+      // eight splits' loads in flight at a time
+#pragma unroll 1
+      for (int s = 0; s < splits; s += 8) {
+        float x[8][4], y[8][4];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float* e = d + (int64_t)min(s + q, splits - 1) * kPlanes * p.m * pn;
+          get2(e, x[q][0], x[q][1]);
+          get2(e + 2, x[q][2], x[q][3]);
+          if (Mode == kGated) {
+            get2(e + p.m * pn, y[q][0], y[q][1]);
+            get2(e + p.m * pn + 2, y[q][2], y[q][3]);
+          }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          if (s + q < splits)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              v[c] += x[q][c];
+              if (Mode == kGated) u[c] += y[q][c];
+            }
+      }
+      epilogue<T, Mode, 4>(p, 0, row, col, v, u);
+    }
   }
 }
 
-hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& p, float* partial, size_t partial_bytes,
+template <typename T, int Mode>
+static hipError_t launch_rows(const GemmArgs& p, int splits, bool join, float* partial, uint32_t* counters,
                               hipStream_t stream) {
+  const dim3 grid((p.n + kCols - 1) / kCols, splits), block(64 * kWaves);
+  const bool one = p.m <= 16;
+  if (join)
+    return launch_kernel(one ? gemm_stream_kernel<T, Mode, 1, true> : gemm_stream_kernel<T, Mode, 2, true>, grid,
+                         block, stream, p, splits, partial, counters);
+  return launch_kernel(one ? gemm_stream_kernel<T, Mode, 1, false> : gemm_stream_kernel<T, Mode, 2, false>, grid,
+                       block, stream, p, splits, partial, counters);
+}
+
+template <typename T>
+static hipError_t launch_typed(Mode mode, const GemmArgs& p, int splits, bool join, float* partial,
+                               uint32_t* counters, hipStream_t stream) {
+  switch (mode) {
+    case kLinear: return launch_rows<T, kLinear>(p, splits, join, partial, counters, stream);
+    case kGated: return launch_rows<T, kGated>(p, splits, join, partial, counters, stream);
+    default: return launch_rows<T, kDx>(p, splits, join, partial, counters, stream);
+  }
+}
+
+struct StreamPlan {
+  int splits;
+  bool join;  // by the last block of each tile
+};
+
+// At most a block per CU: a second round costs another start and end (16 rows
+// of 3584 x 7168: 4 splits, 224 blocks, 15.3 us; 5 splits, 280 blocks, 20.4;
+// 9 splits, 504 blocks, 17.2). Within that, the split whose modelled time is
+// least: the weights at 5.2 TB/s, or 0.12 us for each step of a block if that
+// is more; 0.6 us for each of a wave's steps in turn; 3.3 us for a join by the
+// last block, or 5.3 for one by a second kernel and the sums twice at 4 TB/s
+// (1000 x 776, 1 row: 6.6 us unsplit, 5.6 with 8 splits; 512 x 512: 4.0
+// unsplit, 4.8 with 8).
+// The last block joins up to 8 rows of sums (8 rows of 2048 x 7168, 4 splits:
+// 10.7 us against 11.4; 1 row of gated 3584 x 2048, 16 splits: 10.4 against
+// 12.3); beyond, its one CU takes longer than a second kernel on all of them
+// (16 rows of 3584 x 7168, 4 splits: 16.3 against 15.3).
+static StreamPlan plan_stream(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   const int64_t tiles = (p.n + kCols - 1) / kCols;
   const int64_t steps = (p.red + kRed - 1) / kRed * p.segments;
-  const int team = mode == kGated ? kWaves / 2 : kWaves;
-  const int64_t plane = (int64_t)p.m * ((p.n + 3) & ~3) * 4 * (mode == kGated ? 2 : 1);
-  // a block per CU, but a step at least for every wave
-  int64_t splits = tiles >= 256 ? 1 : (p.m <= 16 ? (256 + tiles - 1) / tiles : 256 / tiles);
-  splits = splits < steps / team ? splits : steps / team;
-  splits = splits < (int64_t)partial_bytes / plane ? splits : (int64_t)partial_bytes / plane;
-  splits = splits < 1 ? 1 : (splits > 64 ? 64 : splits);
-  const hipError_t e = dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, (int)splits, partial, stream)
-                                           : launch_typed<F16>(mode, p, (int)splits, partial, stream);
-  if (e != hipSuccess || splits == 1) return e;
-  return launch_gemm_join(dtype, mode, p, (int)splits, partial, stream);
+  const int planes = mode == kGated ? 2 : 1, team = kWaves / planes;
+  const double plane = (double)p.m * ((p.n + 3) & ~3) * 4 * planes;
+  const double bytes = (double)tiles * steps * planes * (kCols * kRed * 2);
+  const bool join = p.m * planes <= 8;
+  StreamPlan best{1, false};
+  double best_t = 0;
+  for (int s = 1; s <= kMaxSplits; ++s) {
+    if (s > 1 && (plane * s > (double)partial_bytes || tiles * s > 256 || s > steps)) break;
+    const int64_t block_steps = (steps + s - 1) / s;
+    const double t = std::max(bytes / 5.2e6, 0.12 * (double)(block_steps * planes)) +
+                     0.6 * (double)((block_steps + team - 1) / team) + (s == 1 ? 0.0 : join ? 3.3 : 5.3 + 2.0 * s * plane / 4e6);
+    if (s == 1 || t <= best_t) {
+      best = StreamPlan{s, join && s > 1};
+      best_t = t;
+    }
+  }
+  return best;
+}
+
+hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& p, const Workspace& ws, hipStream_t stream) {
+  const StreamPlan t = plan_stream(mode, p, ws.partial_bytes);
+  const hipError_t e = dtype == BLOCK_BF16
+                           ? launch_typed<BF16>(mode, p, t.splits, t.join, ws.partial, ws.counters, stream)
+                           : launch_typed<F16>(mode, p, t.splits, t.join, ws.partial, ws.counters, stream);
+  if (e != hipSuccess || t.splits == 1 || t.join) return e;
+  return launch_gemm_join(dtype, mode, p, t.splits, ws.partial, stream);
 }
 
 }  // namespace block
