@@ -178,7 +178,8 @@ hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, const Workspace&
                                                   : launch_narrow<F16>(mode, p, stream);
   if (mode != kDw && p.m <= kStreamRows)
     return launch_gemm_stream(dtype, mode, p, ws, stream);
-  return launch_gemm_tile(dtype, mode, p, aligned16(mode, p), plan_tiles(mode, p, ws.partial_bytes), ws.partial,
+  const bool aligned = aligned16(mode, p);
+  return launch_gemm_tile(dtype, mode, p, aligned, plan_tiles(mode, p, aligned, ws.partial_bytes), ws.partial,
                           stream);
 }
 

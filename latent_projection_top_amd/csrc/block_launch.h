@@ -57,7 +57,7 @@ struct TilePlan {
   int shape;
   int splits;
 };
-TilePlan plan_tiles(Mode mode, const GemmArgs& args, size_t partial_bytes);
+TilePlan plan_tiles(Mode mode, const GemmArgs& args, bool aligned, size_t partial_bytes);
 hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, bool aligned, const TilePlan& plan,
                             float* partial, hipStream_t stream);
 

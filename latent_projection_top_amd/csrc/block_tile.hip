@@ -2,6 +2,8 @@
 // that make the matrix cores, not the weights' bandwidth, the bound.
 #include "block_device.h"
 
+#include <algorithm>
+
 namespace block {
 
 typedef __attribute__((address_space(3))) void lds_void;
@@ -100,6 +102,11 @@ __device__ __forceinline__ u32x4 shift_down(u32x4 v, int d) {
   return d >= 8 ? u32x4{0, 0, 0, 0} : v;
 }
 
+// (the address space is said where a pointer is made from an integer: a flat
+// load would also wait for LDS)
+#define global_mem __attribute__((address_space(1)))
+struct __attribute__((packed, aligned(4))) Dwords4 { u32x4 v; };
+
 // Direct: operands go from global memory straight to LDS. Otherwise (rows
 // that start at any element, contiguous lengths of any size from 8) they pass
 // through registers: a 16-byte load that would run past a row's end starts
@@ -138,105 +145,135 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   const int all = per_seg * p.segments;
   const int s0 = (int)((int64_t)all * split / splits);
   const int s1 = (int)((int64_t)all * (split + 1) / splits);
-  const bool ragged = (p.red & (kStep - 1)) != 0;
+  const int red = (int)p.red;
+  const bool ragged = (red & (kStep - 1)) != 0;
   // the tile reaches past an operand's rows or columns
   const bool edge = row0 + S::BM > p.m || col0 + kCols > p.n;
 
   // ---- global -> LDS -------------------------------------------------------
   // Rows past the matrix's end repeat its last one and columns its last eight
   // (their sums are not stored); past the reduction's end lanes load zeros.
+  // off: this lane's byte offset of each of the wave's loads from the stage's
+  // first byte of its matrix (a wave's loads of B are all of one matrix).
+  // (through registers the offset of an r-contiguous piece leaves out r)
   uint32_t off[S::PER];
   int red_of[S::PER];
+  auto b_row = [&](int c) {
+    const int r = B::row(c, lane);
+    // gated: 32-column blocks alternate between the two matrices
+    return Mode == kGated ? 32 * (r >> 6) + (r & 31) : r;
+  };
 #pragma unroll
   for (int i = 0; i < S::PER; ++i) {
     const bool is_a = i < S::A_PER;
     const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
-    if (is_a) {
-      const int r = A::row(c, lane), k = A::red(c, lane);
-      red_of[i] = k;
-      if (Mode != kDw)
-        off[i] = (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + (Direct ? k : 0)) * 2u;
-      else
-        off[i] = (uint32_t)(k * p.lda + min(row0 + r, p.m - 8)) * 2u;
-    } else {
-      int r = B::row(c, lane);
-      const int k = B::red(c, lane);
-      red_of[i] = k;
-      // gated: 32-column blocks alternate between the two matrices
-      if (Mode == kGated) r = 32 * (r >> 6) + (r & 31);
-      if (Mode == kDx)
-        off[i] = (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + (Direct ? k : 0)) * 2u;
-      else
-        off[i] = (uint32_t)(k * p.ldb + min(col0 + r, p.n - 8)) * 2u;
-    }
+    const int r = is_a ? A::row(c, lane) : b_row(c);
+    const int k = is_a ? A::red(c, lane) : B::red(c, lane);
+    red_of[i] = k;
+    if (is_a)
+      off[i] = Mode != kDw ? (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + (Direct ? k : 0)) * 2u
+                           : (uint32_t)(k * p.lda + min(row0 + r, p.m - 8)) * 2u;
+    else
+      off[i] = Mode == kDx ? (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + (Direct ? k : 0)) * 2u
+                           : (uint32_t)(k * p.ldb + min(col0 + r, p.n - 8)) * 2u;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)smem;
-
-  auto issue_one = [&](int s, uint32_t buf, int i) {
+  // the matrices at stage 0 of each segment, and from one stage to the next
+  const int bm = Mode == kGated ? (wave >> 1) & 1 : Mode == kDx ? 0 : which;
+  const uintptr_t a_at = Mode != kDw ? row0 * p.lda * 2 : 0, b_at = Mode == kDx ? (int64_t)col0 * p.ldb * 2 : 0;
+  const uintptr_t a_seg[2] = {reinterpret_cast<uintptr_t>(p.a[0]) + a_at, reinterpret_cast<uintptr_t>(p.a[1]) + a_at};
+  const uintptr_t b_seg[2] = {reinterpret_cast<uintptr_t>(p.b[bm]) + b_at, reinterpret_cast<uintptr_t>(p.b[1]) + b_at};
+  const int64_t a_step = kStep * 2 * (Mode != kDw ? 1 : p.lda), b_step = kStep * 2 * (Mode == kDx ? 1 : p.ldb);
+  auto base_of = [&](bool is_a, int s) __attribute__((always_inline)) -> uintptr_t {
+    const bool second = s >= per_seg;
+    const int64_t ks = second ? s - per_seg : s;
+    return is_a ? (second ? a_seg[1] : a_seg[0]) + ks * a_step : (second ? b_seg[1] : b_seg[0]) + ks * b_step;
+  };
+  auto slot = [&](int i) __attribute__((always_inline)) -> uint32_t {  // of load i in a stage
     const bool is_a = i < S::A_PER;
-    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
-    const int seg = s >= per_seg ? 1 : 0;
-    const int ks = s - seg * per_seg;
-    const char* base;
-    if (is_a) {
-      base = static_cast<const char*>(p.a[seg]) +
-             (Mode != kDw ? row0 * p.lda * 2 + (int64_t)ks * (kStep * 2) : (int64_t)ks * (kStep * 2) * p.lda);
-    } else {
-      const int mat = Mode == kGated ? ((c >> 1) & 1) : (Mode == kDx ? seg : which);
-      base = static_cast<const char*>(p.b[mat]) +
-             (Mode == kDx ? (int64_t)col0 * p.ldb * 2 + (int64_t)ks * (kStep * 2)
-                          : (int64_t)ks * (kStep * 2) * p.ldb);
-    }
-    const uint32_t dst = buf + (is_a ? 0 : S::A_BYTES) + c * 1024;
-    if (ragged && ks == per_seg - 1) {
-      const bool in = (int64_t)ks * kStep + red_of[i] < p.red;
-      dma16(in ? base + off[i] : reinterpret_cast<const char*>(kZeros), dst);
-    } else {
-      dma16(base, off[i], dst);
-    }
+    return (is_a ? 0 : S::A_BYTES) + (wave + S::NW * (is_a ? i : i - S::A_PER)) * 1024;
   };
 
-  // Through registers: load i of stage s, and its store to LDS. The r of an
-  // r-contiguous piece, the r row of the others, and their first column are
-  // clamped to the matrix; `shift` says by how much on the way to LDS.
-  u32x4 held[2][Direct ? 1 : S::PER];
-  auto fetch = [&](int s, int i) -> u32x4 {
-    const bool is_a = i < S::A_PER;
-    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
-    const int seg = s >= per_seg ? 1 : 0;
-    const int ks = s - seg * per_seg;
-    const int64_t k = (int64_t)ks * kStep + red_of[i];
-    const char* base;
-    uint32_t o = off[i];
-    if (is_a ? Mode != kDw : Mode == kDx) {
-      base = is_a ? static_cast<const char*>(p.a[seg]) + row0 * p.lda * 2
-                  : static_cast<const char*>(p.b[seg]) + (int64_t)col0 * p.ldb * 2;
-      o += (uint32_t)min(k, p.red - 8) * 2u;
-    } else {
-      const int64_t ld = is_a ? p.lda : p.ldb;
-      const int mat = Mode == kGated ? ((c >> 1) & 1) : which;
-      base = static_cast<const char*>(is_a ? p.a[0] : p.b[mat]) + (int64_t)ks * (kStep * 2) * ld;
-      o -= (uint32_t)(max(k - (p.red - 1), (int64_t)0) * ld) * 2u;
-    }
-    return reinterpret_cast<const Any16*>(base + o)->v;
-  };
-  auto put = [&](int s, uint32_t buf, int i, u32x4 v) {
-    const bool is_a = i < S::A_PER;
-    const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+  // Direct. Any stage; the last of a segment may be short.
+  auto issue_any = [&](int s, uint32_t buf, int i) __attribute__((always_inline)) {
     const int ks = s >= per_seg ? s - per_seg : s;
-    if (edge || ks == per_seg - 1) {
-      const int64_t k = (int64_t)ks * kStep + red_of[i];
-      if (is_a ? Mode != kDw : Mode == kDx) {
-        v = shift_down(v, (int)min(max(k - (p.red - 8), (int64_t)0), (int64_t)8));
+    const char* base = reinterpret_cast<const char*>(base_of(i < S::A_PER, s));
+    if (ragged && ks == per_seg - 1) {
+      const bool in = ks * kStep + red_of[i] < red;
+      dma16(in ? base + off[i] : reinterpret_cast<const char*>(kZeros), buf + slot(i));
+    } else {
+      dma16(base, off[i], buf + slot(i));
+    }
+  };
+
+  // Through registers. The r of an r-contiguous piece, the r row of the
+  // others, and their first column are clamped to the matrix; `shift_down`
+  // says by how much on the way to LDS. Rows may start at odd elements: a
+  // piece is loaded as the four dwords from its first element's and the dword
+  // of its last, and v_alignbit_b32 moves it into place.
+  struct Held {
+    u32x4 v;
+    uint32_t last;
+  };
+  Held held[4][Direct ? 1 : S::PER];  // stage q in set q % 4
+  auto fetch_at = [&](uintptr_t base, uint32_t o) __attribute__((always_inline)) -> Held {
+    o += (uint32_t)(base & 2);
+    base &= ~(uintptr_t)3;
+    Held h;
+    h.v = reinterpret_cast<const global_mem Dwords4*>(base + (o & ~3u))->v;
+    h.last = *reinterpret_cast<const global_mem uint32_t*>(base + ((o + 14) & ~3u));
+    return h;
+  };
+  constexpr bool kAr = Mode != kDw, kBr = Mode == kDx;  // r-contiguous
+  // offset of load i of any stage: what the clamps make of it
+  auto off_any = [&](int s, int i) __attribute__((always_inline)) -> uint32_t {
+    const int ks = s >= per_seg ? s - per_seg : s;
+    const int k = ks * kStep + red_of[i];
+    if (i < S::A_PER ? kAr : kBr) return off[i] + (uint32_t)(min(k, red - 8) - ks * kStep) * 2u;
+    return off[i] - (uint32_t)max(k - (red - 1), 0) * (uint32_t)(i < S::A_PER ? p.lda : p.ldb) * 2u;
+  };
+  auto align = [&](Held& h, uint32_t o) __attribute__((always_inline)) {
+    const uint32_t by = (o & 2) * 8;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) h.v[q] = __builtin_amdgcn_alignbit(h.v[q + 1], h.v[q], by);
+    h.v[3] = __builtin_amdgcn_alignbit(h.last, h.v[3], by);
+  };
+  auto trim = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
+    const int ks = s >= per_seg ? s - per_seg : s;
+#pragma unroll
+    for (int i = 0; i < S::PER; ++i) {
+      const bool is_a = i < S::A_PER;
+      const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
+      const int k = ks * kStep + red_of[i];
+      if (is_a ? kAr : kBr) {
+        h[i].v = shift_down(h[i].v, min(max(k - (red - 8), 0), 8));
       } else {
-        int r = is_a ? A::row(c, lane) : B::row(c, lane);
-        if (!is_a && Mode == kGated) r = 32 * (r >> 6) + (r & 31);
-        const int64_t over = is_a ? row0 + r - (p.m - 8) : (int64_t)col0 + r - (p.n - 8);
-        v = shift_down(v, k >= p.red ? 8 : (int)min(max(over, (int64_t)0), (int64_t)8));
+        const int over = is_a ? (int)(row0 + A::row(c, lane) - (p.m - 8)) : col0 + b_row(c) - (p.n - 8);
+        h[i].v = shift_down(h[i].v, k >= red ? 8 : min(max(over, 0), 8));
       }
     }
-    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(buf + (is_a ? 0 : S::A_BYTES) + c * 1024 + lane * 16) =
-        v;
+  };
+  auto put = [&](uint32_t buf, int i, const Held& h) __attribute__((always_inline)) {
+    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(buf + slot(i) + lane * 16) = h.v;
+  };
+  auto fetch_any = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < S::PER; ++i) {
+      uintptr_t base = base_of(i < S::A_PER, s);
+      uint32_t o = off_any(s, i);
+      // a clamped r can lie before the stage's first: count from the row's
+      if (i < S::A_PER ? kAr : kBr) {
+        const uint32_t at = (uint32_t)(s >= per_seg ? s - per_seg : s) * (kStep * 2);
+        base -= at;
+        o += at;
+      }
+      h[i] = fetch_at(base, o);
+    }
+  };
+  auto arrange_any = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
+#pragma unroll
+    for (int i = 0; i < S::PER; ++i) align(h[i], off_any(s, i) + (uint32_t)(base_of(i < S::A_PER, s) & 2));
+    if (edge || (s >= per_seg ? s - per_seg : s) == per_seg - 1) trim(s, h);
   };
 
   // ---- LDS -> registers ----------------------------------------------------
@@ -255,30 +292,19 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
 
   // Stage s's MFMAs. Meanwhile the operands of stage s + 1 are read (a[i] as
   // soon as its last MFMA is issued, B into the other register set) and this
-  // wave's loads of stage s + 4 go out. Direct: into the buffer of stage
-  // s - 1, which the barrier before this step has freed. Through registers:
-  // into one of two sets, while the other set, stage s + 3, goes to LDS (into
-  // the buffer of stage s - 2), so that a load has two steps to arrive.
-  auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], u32x4(&in)[Direct ? 1 : S::PER],
-                  u32x4(&out)[Direct ? 1 : S::PER], uint32_t next, int s, uint32_t fill, bool issue, bool write) {
+  // wave's loads of a later stage go out. Direct: stage s + 4's, into the
+  // buffer of stage s - 1, which the barrier before this step has freed.
+  // Through registers: stage s + 6's, into one of four sets, while the set of
+  // stage s + 3 goes to LDS (into the buffer of stage s - 2), so that a load
+  // has three steps to arrive. load(n) does the n-th of PER shares of it.
+  auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], uint32_t next, auto load) __attribute__((always_inline)) {
     constexpr int kEvery = S::MT * S::NT / S::PER;
-    if constexpr (!Direct) {
-      if (issue)
-#pragma unroll
-        for (int i = 0; i < S::PER; ++i) in[i] = fetch(s + 4, i);
-    }
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) {
 #pragma unroll
       for (int j = 0; j < S::NT; ++j) {
         const int n = i * S::NT + j;
-        if (n % kEvery == kEvery / 2) {
-          if constexpr (Direct) {
-            if (issue) issue_one(s + 4, lds0 + fill, n / kEvery);
-          } else {
-            if (write) put(s + 3, lds0 + fill, n / kEvery, out[n / kEvery]);
-          }
-        }
+        if (n % kEvery == kEvery / 2) load(n / kEvery);
         acc[i][j] = T::mfma(b[j], a[i], acc[i][j]);
       }
       if (i < S::NT) bn[i] = read_b(next, i);
@@ -296,23 +322,24 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
 
   const int count = s1 - s0;
   if (count > 0) {
-    // the first four stages; through registers: three, and the fourth held
+    // the first four stages; through registers: three, and three held
     if constexpr (Direct) {
 #pragma unroll 1
       for (int s = 0; s < min(count, 4); ++s)
 #pragma unroll
-        for (int i = 0; i < S::PER; ++i) issue_one(s0 + s, lds0 + s * S::STAGE, i);
+        for (int i = 0; i < S::PER; ++i) issue_any(s0 + s, lds0 + s * S::STAGE, i);
     } else {
-#pragma unroll 1
-      for (int s = 0; s < min(count, 3); ++s) {
+      // (stages past the end repeat the last one: no branches here)
 #pragma unroll
-        for (int i = 0; i < S::PER; ++i) held[0][i] = fetch(s0 + s, i);
+      for (int s = 0; s < 4; ++s) fetch_any(min(s0 + s, s1 - 1), held[s]);
 #pragma unroll
-        for (int i = 0; i < S::PER; ++i) put(s0 + s, lds0 + s * S::STAGE, i, held[0][i]);
+      for (int s = 0; s < 3; ++s) {
+        arrange_any(min(s0 + s, s1 - 1), held[s]);
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) put(lds0 + s * S::STAGE, i, held[s][i]);
       }
-      if (count > 3)
 #pragma unroll
-        for (int i = 0; i < S::PER; ++i) held[1][i] = fetch(s0 + 3, i);
+      for (int s = 4; s < 6; ++s) fetch_any(min(s0 + s, s1 - 1), held[s & 3]);
     }
     if (count >= 4)
       wait_barrier<kVm2, 0>();
@@ -325,42 +352,112 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
 
     constexpr uint32_t kEnd = kStages * S::STAGE;
     // buffers of stage s + 1, and of stage s + 4 (through registers s + 3)
-    uint32_t next = lds0 + S::STAGE, fill = (Direct ? 4 : 3) * S::STAGE;
-    auto advance = [&] {
+    uint32_t next = lds0 + S::STAGE, fill = lds0 + (Direct ? 4 : 3) * S::STAGE;
+    auto advance = [&]() __attribute__((always_inline)) {
       next = next + S::STAGE == lds0 + kEnd ? lds0 : next + S::STAGE;
-      fill = fill + S::STAGE == kEnd ? 0 : fill + S::STAGE;
+      fill = fill + S::STAGE == lds0 + kEnd ? lds0 : fill + S::STAGE;
     };
+    // step s with s % kTurns == u: register sets by number
+    constexpr int kTurns = Direct ? 2 : 4, kAhead = Direct ? 4 : 6;
     int s = 0;
-    // steady state: two stages a turn (the two B register sets)
-#pragma unroll 1
-    for (; s + 5 < count; s += 2) {
-      step(b0, b1, held[0], held[1], next, s0 + s, fill, true, true);
+    // Steady state: the stages to load are whole and follow each other.
+    uintptr_t a_next = 0, b_next = 0;
+    auto steady = [&](auto u_) __attribute__((always_inline)) {
+      constexpr int u = decltype(u_)::value;
+      Held(&in)[Direct ? 1 : S::PER] = held[(u + 2) & 3];
+      Held(&out)[Direct ? 1 : S::PER] = held[(u + 3) & 3];
+      if constexpr (!Direct) {
+#pragma unroll
+        for (int i = 0; i < S::PER; ++i) {
+          const bool is_a = i < S::A_PER;
+          const uint32_t o = off[i] + ((is_a ? kAr : kBr) ? 2u * red_of[i] : 0u);
+          in[i] = fetch_at(is_a ? a_next : b_next, o);
+          align(out[i], o + (uint32_t)((is_a ? a_next : b_next) & 2));
+        }
+        if (edge) trim(s0 + s + u + 3, out);
+      }
+      auto load = [&](int n) __attribute__((always_inline)) {
+        if constexpr (Direct)
+          dma16(reinterpret_cast<const char*>(n < S::A_PER ? a_next : b_next), off[n], fill + slot(n));
+        else
+          put(fill, n, out[n]);
+      };
+      step((u & 1) ? b1 : b0, (u & 1) ? b0 : b1, next, load);
       wait_barrier<kVm2, kLgkm>();
       advance();
-      step(b1, b0, held[1], held[0], next, s0 + s + 1, fill, true, true);
-      wait_barrier<kVm2, kLgkm>();
-      advance();
-    }
-    // the last stages
-#pragma unroll 1
-    for (; s < count; ++s) {
-      step(b0, b1, held[0], held[1], next, s0 + s, fill, s + 4 < count, s + 3 < count);
-      if (s + 2 < count) {
-        if (s + 4 < count)
+      a_next += a_step;
+      b_next += b_step;
+    };
+    // Any step: the ends of the segments.
+    auto other = [&](auto u_) __attribute__((always_inline)) {
+      constexpr int u = decltype(u_)::value;
+      const int q = s + u;
+      if (q >= count) return;
+      const bool issue = q + kAhead < count, write = q + 3 < count;
+      Held(&in)[Direct ? 1 : S::PER] = held[(u + 2) & 3];
+      Held(&out)[Direct ? 1 : S::PER] = held[(u + 3) & 3];
+      if constexpr (!Direct) {
+        if (issue) fetch_any(s0 + q + kAhead, in);
+        if (write) arrange_any(s0 + q + 3, out);
+      }
+      auto load = [&](int n) __attribute__((always_inline)) {
+        if constexpr (Direct) {
+          if (issue) issue_any(s0 + q + kAhead, fill, n);
+        } else {
+          if (write) put(fill, n, out[n]);
+        }
+      };
+      step((u & 1) ? b1 : b0, (u & 1) ? b0 : b1, next, load);
+      if (q + 2 < count) {
+        if (q + 4 < count)
           wait_barrier<kVm2, kLgkm>();
-        else if (s + 3 < count)
+        else if (q + 3 < count)
           wait_barrier<kVm1, kLgkm>();
         else
           wait_barrier<kVm0, kLgkm>();
       }
       advance();
-#pragma unroll
-      for (int j = 0; j < S::NT; ++j) b0[j] = b1[j];
-      if constexpr (!Direct) {
-#pragma unroll
-        for (int i = 0; i < S::PER; ++i) held[1][i] = held[0][i];
+    };
+    using std::integral_constant;
+    auto whole_stages = [&]() __attribute__((always_inline)) {
+      const int first = s0 + s + kAhead;  // the next stage to load
+      const int limit = min(s1, (first >= per_seg ? 2 : 1) * per_seg - (ragged ? 1 : 0));
+      a_next = base_of(true, first);
+      b_next = base_of(false, first);
+#pragma unroll 1
+      for (int t = first; t + kTurns <= limit; t += kTurns) {
+        steady(integral_constant<int, 0>{});
+        steady(integral_constant<int, 1>{});
+        if constexpr (kTurns == 4) {
+          steady(integral_constant<int, 2>{});
+          steady(integral_constant<int, 3>{});
+        }
+        s += kTurns;
+      }
+    };
+    auto other_stages = [&](int end) __attribute__((always_inline)) {
+#pragma unroll 1
+      for (; s < end; s += kTurns) {
+        other(integral_constant<int, 0>{});
+        other(integral_constant<int, 1>{});
+        if constexpr (kTurns == 4) {
+          other(integral_constant<int, 2>{});
+          other(integral_constant<int, 3>{});
+        }
+      }
+    };
+    // (through registers, stage s + 3 on its way to LDS and stage s + 6 to load
+    // have to be of one segment)
+    if (Direct || Mode != kDx || s0 + 3 >= per_seg || s0 + kAhead < per_seg) whole_stages();
+    if constexpr (Mode == kDx) {
+      // past the first segment's end: until the next stage to load (through
+      // registers: to store) is of the second
+      if (s0 < per_seg && s1 > per_seg) {
+        other_stages(min(count, per_seg - s0 - (Direct ? kAhead : 3)));
+        whole_stages();
       }
     }
+    other_stages(count);
   }
 
   // lane (g, m) of tile (i, j) holds row 16 i + m, columns 16 j + 4 g .. + 3
@@ -426,12 +523,12 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   }
 }
 
-template <typename T, int Mode, typename S>
-static hipError_t launch_shape(const GemmArgs& p, bool aligned, int splits, float* partial, hipStream_t stream) {
+template <typename T, int Mode, typename S, bool Direct>
+static hipError_t launch_shape(const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
   constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;
   const int mt = (int)((p.m + S::BM - 1) / S::BM), nt = (p.n + kCols - 1) / kCols;
   const int64_t blocks = (int64_t)mt * nt * p.outputs * splits;
-  const hipError_t e = launch_kernel(aligned ? gemm_tile_kernel<T, Mode, S, true> : gemm_tile_kernel<T, Mode, S, false>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
+  const hipError_t e = launch_kernel(gemm_tile_kernel<T, Mode, S, Direct>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
                                      p, mt, nt, splits, partial);
   if (e != hipSuccess || splits == 1) return e;
   return launch_gemm_join(T::code, (enum Mode)Mode, p, splits, partial, stream);
@@ -444,9 +541,13 @@ typedef TileShape<128, 128, 2, 2> Small;
 template <typename T, int Mode>
 static hipError_t launch_mode(const GemmArgs& p, bool aligned, const TilePlan& t, float* partial, hipStream_t stream) {
   switch (t.shape) {
-    case 0: return launch_shape<T, Mode, Large>(p, aligned, t.splits, partial, stream);
-    case 1: return launch_shape<T, Mode, Wide>(p, aligned, t.splits, partial, stream);
-    default: return launch_shape<T, Mode, Small>(p, aligned, t.splits, partial, stream);
+    case 0: return launch_shape<T, Mode, Large, true>(p, t.splits, partial, stream);
+    case 1:
+      return aligned ? launch_shape<T, Mode, Wide, true>(p, t.splits, partial, stream)
+                     : launch_shape<T, Mode, Wide, false>(p, t.splits, partial, stream);
+    default:
+      return aligned ? launch_shape<T, Mode, Small, true>(p, t.splits, partial, stream)
+                     : launch_shape<T, Mode, Small, false>(p, t.splits, partial, stream);
   }
 }
 
@@ -467,28 +568,36 @@ hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, bool aligne
                              : launch_typed<F16>(mode, p, aligned, t, partial, stream);
 }
 
-// Tile shape and K split of a product: the one whose time a simple model puts
-// lowest.
-TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
-  struct { int bm, bn; double rate; int per_cu; } const shapes[3] = {
-      {256, 256, 1.0, 1}, {128, 256, 0.75, 1}, {128, 128, 0.6, 2}};
+// Tile shape and K split of a product: the ones whose modelled time is least.
+// Stage times in us, measured at K = 3584 with one block on few CUs and with
+// all CUs busy (they share HBM and power): 256 x 256 0.63 / 0.87, 128 x 256
+// 0.42 / 0.58, 128 x 128 0.35 / 0.39 and 0.65 where two share a CU; each round
+// of blocks starts and ends in about 2 us; a split costs 5 us and its sums
+// twice at 4.2 TB/s. So large tiles where they fill the CUs (4096 x 3584 ->
+// 4096: 98 us against 129 and 150), small ones for few rows (128 rows, 3584 ->
+// 4096, 8 splits: 17.9 us; 256 x 256, 12 splits: 23.7). Through registers
+// (unaligned) the large tile's accumulators leave no room for the loads.
+TilePlan plan_tiles(Mode mode, const GemmArgs& p, bool aligned, size_t partial_bytes) {
+  struct Cost { int bm, bn; double few, full; } const shapes[3] = {
+      {256, 256, 0.63, 0.87}, {128, 256, 0.42, 0.58}, {128, 128, 0.35, 0.39}};
+  const double pair = 0.65;
   const double steps = (double)((p.red + kStep - 1) / kStep) * p.segments;
   const int planes = mode == kGated ? 2 : p.outputs;
-  TilePlan best{0, 1};
+  TilePlan best{2, 1};
   double best_t = 0;
-  for (int k = 0; k < 3; ++k) {
-    const int bn = mode == kGated ? shapes[k].bn / 2 : shapes[k].bn;
-    const double tiles = (double)((p.m + shapes[k].bm - 1) / shapes[k].bm) * ((p.n + bn - 1) / bn) * p.outputs;
-    // microseconds of one stage of a block that has its CU to itself
-    const double stage = 0.6 * shapes[k].bm * shapes[k].bn / 65536.0 / shapes[k].rate;
+  for (int k = aligned ? 0 : 1; k < 3; ++k) {
+    const Cost& c = shapes[k];
+    const int bn = mode == kGated ? c.bn / 2 : c.bn;
+    const int64_t tiles = (int64_t)((p.m + c.bm - 1) / c.bm) * ((p.n + bn - 1) / bn) * p.outputs;
     for (int s = 1; s <= 16; ++s) {
       const double bytes = 4.0 * p.m * ((p.n + 3) & ~3) * planes * s;
-      if (s > 1 && (bytes > (double)partial_bytes || steps / s < 8 || (p.n & 3) != 0)) break;
-      const double slots = 256.0 * shapes[k].per_cu;
-      const double blocks = tiles * s;
-      const double rounds = blocks <= 256 ? 1.0 : (double)(int64_t)((blocks + slots - 1) / slots) * shapes[k].per_cu;
-      double t = rounds * (steps / s + 6) * stage;
-      if (s > 1) t += 4.0 + 2.0 * bytes / 4e6;
+      if (s > 1 && (bytes > (double)partial_bytes || steps / s < 4)) break;
+      const int64_t blocks = tiles * s, slots = k == 2 ? 512 : 256;
+      const int64_t rounds = (blocks - 1) / slots, rest = blocks - rounds * slots;
+      const double busy = rounds > 0 ? 1.0 : std::min(1.0, (double)rest / 256.0);
+      const double last = rest > 256 ? pair : c.few + (c.full - c.few) * busy;
+      double t = (double)rounds * (steps / s * (k == 2 ? pair : c.full) + 2.0) + steps / s * last + 2.0;
+      if (s > 1) t += 5.0 + 2.0 * bytes / 4.2e6;
       if (best_t == 0 || t < best_t) {
         best = TilePlan{k, s};
         best_t = t;
