@@ -19,15 +19,16 @@ struct block_norm_plan {
 
 // Workspace of the matrix operators: the products' counters, their split sums
 // (up to off_dz), then dz (linear) or dg and du (gated) with their rows padded
-// to a multiple of 8 elements, and the partial column sums of dbias.
+// to a multiple of 8 elements, the partial column sums of dbias, and padded
+// copies of x and (if their rows are no multiple of 8) the weights.
 struct block_gated_plan {
   block_gated_config cfg;
-  size_t partial_bytes, off_dz, off_du, ws_bytes;
+  size_t partial_bytes, off_dz, off_du, off_x, off_w, w_bytes, ws_bytes;
 };
 
 struct block_linear_plan {
   block_linear_config cfg;
-  size_t partial_bytes, off_dz, off_sum, ws_bytes;
+  size_t partial_bytes, off_dz, off_sum, off_x, off_w, w_bytes, ws_bytes;
 };
 
 namespace {
@@ -73,6 +74,21 @@ block::Workspace products(const Plan* plan, void* workspace) {
   return block::Workspace{reinterpret_cast<uint32_t*>(base), reinterpret_cast<float*>(base + block::kCounterBytes),
                           plan->partial_bytes};
 }
+
+// The copies a call makes so that the tile kernel can read its operands.
+struct Copies {
+  block::Copy c[3];
+  int n = 0;
+  // *p, [rows][len] of stride *ld, is copied to dst if it has to be (and dst
+  // is there); *p and *ld then describe the copy.
+  void use(const void** p, int64_t* ld, int64_t rows, int len, void* dst) {
+    if (dst == nullptr || !block::needs_copy(*p, *ld, len)) return;
+    c[n++] = block::Copy{*p, dst, *ld, rows, len};
+    *p = dst;
+    *ld = padded(len);
+  }
+  int launch(hipStream_t s) const { return status_of(block::launch_copies(c, n, s)); }
+};
 
 template <typename Plan, typename Config>
 Plan* new_plan(const Config& cfg) {
@@ -193,7 +209,10 @@ int block_gated_prepare(const block_gated_config* cfg, block_gated_plan** out) {
   const size_t dz = cfg->training ? round256((size_t)cfg->rows * padded(cfg->inner) * 2) : 0;
   p->off_dz = block::kCounterBytes + p->partial_bytes;
   p->off_du = p->off_dz + dz;
-  p->ws_bytes = p->off_du + dz;
+  p->off_x = p->off_du + dz;
+  p->off_w = p->off_x + round256((size_t)cfg->rows * padded(cfg->inputs) * 2);
+  p->w_bytes = (cfg->inner & 7) != 0 ? round256((size_t)cfg->inputs * padded(cfg->inner) * 2) : 0;
+  p->ws_bytes = p->off_w + 2 * p->w_bytes;
   *out = p;
   return ROUTE_OK;
 }
@@ -228,6 +247,16 @@ int block_gated(const block_gated_plan* plan, const void* x, int64_t x_stride, c
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
+  if (!block::gemm_streams(block::kGated, rows, c.inner, c.inputs)) {
+    char* ws = static_cast<char*>(workspace);
+    Copies copies;
+    int64_t ld = a.ldb;
+    copies.use(&a.a[0], &a.lda, rows, c.inputs, ws + plan->off_x);
+    copies.use(&a.b[0], &ld, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w : nullptr);
+    copies.use(&a.b[1], &a.ldb, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w + plan->w_bytes : nullptr);
+    if (int st = copies.launch(static_cast<hipStream_t>(stream))) return st;
+    a.padded = true;
+  }
   return status_of(block::launch_gemm(c.dtype, block::kGated, a, products(plan, workspace),
                                       static_cast<hipStream_t>(stream)));
 }
@@ -255,14 +284,23 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   const void* slopes[2] = {d_gate, d_up};
   int st = status_of(block::launch_scale(c.dtype, dh, dh_stride, slopes, 2, dz, padded(c.inner), rows, c.inner, s));
   if (st != ROUTE_OK) return st;
+  Copies copies;
+  int64_t ldg = c.inner, ldu = c.inner;
+  if (dx != nullptr && !block::gemm_streams(block::kDx, rows, c.inputs, c.inner)) {
+    copies.use(&w_gate, &ldg, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w : nullptr);
+    copies.use(&w_up, &ldu, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w + plan->w_bytes : nullptr);
+  }
+  if (dw_gate != nullptr) copies.use(&x, &x_stride, rows, c.inputs, ws + plan->off_x);
+  if ((st = copies.launch(s)) != ROUTE_OK) return st;
   if (dx != nullptr && rows != 0) {
     GemmArgs a{};
+    a.padded = true;
     a.a[0] = dz[0];
     a.a[1] = dz[1];
     a.lda = padded(c.inner);
     a.b[0] = w_gate;
     a.b[1] = w_up;
-    a.ldb = c.inner;
+    a.ldb = ldu;
     a.c[0] = dx;
     a.ldc = dx_stride;
     a.m = rows;
@@ -275,6 +313,7 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   }
   if (dw_gate == nullptr) return ROUTE_OK;
   GemmArgs a{};
+  a.padded = true;
   a.a[0] = x;
   a.lda = x_stride;
   a.b[0] = dz[0];
@@ -307,11 +346,13 @@ int block_linear_prepare(const block_linear_config* cfg, block_linear_plan** out
   if (int st = find_device(cfg->device)) return st;
   block_linear_plan* p = new_plan<block_linear_plan>(*cfg);
   if (p == nullptr) return ROUTE_E_ARG;
-  const bool dz = cfg->training && cfg->activation != BLOCK_ACT_NONE;
   p->partial_bytes = partial_area(block::kLinear, cfg->rows, cfg->inputs, cfg->outputs, 1, cfg->training != 0);
   p->off_dz = block::kCounterBytes + p->partial_bytes;
-  p->off_sum = p->off_dz + (dz ? round256((size_t)cfg->rows * padded(cfg->outputs) * 2) : 0);
-  p->ws_bytes = p->off_sum + (cfg->training ? round256(block::column_sum_bytes(cfg->rows, cfg->outputs)) : 0);
+  p->off_sum = p->off_dz + (cfg->training ? round256((size_t)cfg->rows * padded(cfg->outputs) * 2) : 0);
+  p->off_x = p->off_sum + (cfg->training ? round256(block::column_sum_bytes(cfg->rows, cfg->outputs)) : 0);
+  p->off_w = p->off_x + round256((size_t)cfg->rows * padded(cfg->inputs) * 2);
+  p->w_bytes = (cfg->outputs & 7) != 0 ? round256((size_t)cfg->inputs * padded(cfg->outputs) * 2) : 0;
+  p->ws_bytes = p->off_w + p->w_bytes;
   *out = p;
   return ROUTE_OK;
 }
@@ -349,6 +390,14 @@ int block_linear(const block_linear_plan* plan, const void* x, int64_t x_stride,
   a.red = c.inputs;
   a.segments = a.outputs = 1;
   a.act = c.activation;
+  if (!block::gemm_streams(block::kLinear, rows, c.outputs, c.inputs)) {
+    char* ws = static_cast<char*>(workspace);
+    Copies copies;
+    copies.use(&a.a[0], &a.lda, rows, c.inputs, ws + plan->off_x);
+    copies.use(&a.b[0], &a.ldb, c.inputs, c.outputs, plan->w_bytes ? ws + plan->off_w : nullptr);
+    if (int st = copies.launch(static_cast<hipStream_t>(stream))) return st;
+    a.padded = true;
+  }
   return status_of(block::launch_gemm(c.dtype, block::kLinear, a, products(plan, workspace),
                                       static_cast<hipStream_t>(stream)));
 }
@@ -385,12 +434,20 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
                                                       reinterpret_cast<float*>(ws + plan->off_sum), s));
     if (st != ROUTE_OK) return st;
   }
+  Copies copies;
+  int64_t ldw = c.outputs;
+  const bool tiled_dx = dx != nullptr && !block::gemm_streams(block::kDx, rows, c.inputs, c.outputs);
+  if (tiled_dx) copies.use(&w, &ldw, c.inputs, c.outputs, plan->w_bytes ? ws + plan->off_w : nullptr);
+  if (dw != nullptr) copies.use(&x, &x_stride, rows, c.inputs, ws + plan->off_x);
+  if (!scaled && (tiled_dx || dw != nullptr)) copies.use(&dz, &ldz, rows, c.outputs, ws + plan->off_dz);
+  if (int st = copies.launch(s)) return st;
   if (dx != nullptr && rows != 0) {
     GemmArgs a{};
+    a.padded = true;
     a.a[0] = dz;
     a.lda = ldz;
     a.b[0] = w;
-    a.ldb = c.outputs;
+    a.ldb = ldw;
     a.c[0] = dx;
     a.ldc = dx_stride;
     a.m = rows;
@@ -402,6 +459,7 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   }
   if (dw == nullptr) return ROUTE_OK;
   GemmArgs a{};
+  a.padded = true;
   a.a[0] = x;
   a.lda = x_stride;
   a.b[0] = dz;

@@ -3,10 +3,12 @@
 
 namespace block {
 
-// Products with an operand of fewer than 8 contiguous elements, which no
-// 16-byte load fits: 64 x 64 output tiles, four waves of 32 x 32 each,
-// reduction steps of 32 staged element by element through LDS with r
-// contiguous.
+// Products that the tile kernel's 16-byte loads do not fit: weights whose
+// rows are multiples of 8 long, for which no copy is kept, at an address that
+// is no multiple of 16. 64 x 64 output tiles, four waves of
+// 32 x 32 each, reduction steps of 32 staged element by element through LDS
+// with r contiguous; right for everything, at about a fifth of the tile
+// kernel's rate.
 constexpr int kTile = 64;
 constexpr int kStep = 32;
 constexpr int kPitch = kStep + 8;  // 16-byte aligned, spreads rows over banks
@@ -152,18 +154,20 @@ hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& p, int splits,
                              : join_typed<F16>(mode, p, splits, partial, stream);
 }
 
-// Asynchronous 16-byte loads: every row of every operand starts on a 16-byte
-// boundary and its contiguous length is a multiple of 8.
-static bool aligned16(Mode mode, const GemmArgs& p) {
+// Whether the tile kernel can read every operand.
+static int64_t lengths(Mode mode, const GemmArgs& p) {
+  return (mode == kDw ? p.m : p.red) | (mode == kDx ? p.red : p.n);
+}
+
+static bool tileable(Mode mode, const GemmArgs& p) {
   uintptr_t bits = 0;
   for (int i = 0; i < 2; ++i)
     bits |= reinterpret_cast<uintptr_t>(p.a[i]) | reinterpret_cast<uintptr_t>(p.b[i]);
-  const int64_t a_len = mode == kDw ? p.m : p.red, b_len = mode == kDx ? p.red : p.n;
-  return (bits & 15) == 0 && ((p.lda | p.ldb | a_len | b_len) & 7) == 0;
+  return (bits & 15) == 0 && ((p.lda | p.ldb) & 7) == 0 && (p.padded || (lengths(mode, p) & 7) == 0);
 }
 
-static bool narrow(Mode mode, const GemmArgs& p) {
-  return (mode == kDw ? p.m : p.red) < 8 || (mode == kDx ? p.red : p.n) < 8;
+bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red) {
+  return mode != kDw && m <= kStreamRows && red >= 8 && n >= 8;
 }
 
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
@@ -174,16 +178,46 @@ size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
 }
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, const Workspace& ws, hipStream_t stream) {
-  if (narrow(mode, p)) return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream)
-                                                  : launch_narrow<F16>(mode, p, stream);
-  if (mode != kDw && p.m <= kStreamRows)
+  if (gemm_streams(mode, p.m, p.n, p.red))
     return launch_gemm_stream(dtype, mode, p, ws, stream);
-  const bool aligned = aligned16(mode, p);
-  return launch_gemm_tile(dtype, mode, p, aligned, plan_tiles(mode, p, aligned, ws.partial_bytes), ws.partial,
-                          stream);
+  if (tileable(mode, p))
+    return launch_gemm_tile(dtype, mode, p, plan_tiles(mode, p, ws.partial_bytes), ws.partial, stream);
+  return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream) : launch_narrow<F16>(mode, p, stream);
 }
 
 // ------------------------------------------------------------- elementwise --
+
+struct Copies {
+  Copy c[3];
+  int64_t end[3];  // pieces of 8 values, counted through
+};
+
+__global__ __launch_bounds__(256) void copy_kernel(Copies p) {
+  int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (id >= p.end[2]) return;
+  const int k = id < p.end[0] ? 0 : id < p.end[1] ? 1 : 2;
+  const Copy& c = p.c[k];
+  if (k > 0) id -= p.end[k - 1];
+  const int64_t per_row = (c.len + 7) >> 3;
+  const int64_t row = id / per_row;
+  const int col = (int)(id - row * per_row) * 8;
+  const u32x4 v = load8(static_cast<const uint16_t*>(c.src) + row * c.ld + col, c.len - col);
+  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(c.dst) + id * 8) = v;
+}
+
+hipError_t launch_copies(const Copy* copies, int count, hipStream_t stream) {
+  Copies p{};
+  int64_t end = 0;
+  for (int k = 0; k < 3; ++k) {
+    if (k < count) {
+      p.c[k] = copies[k];
+      end += copies[k].rows * ((copies[k].len + 7) >> 3);
+    }
+    p.end[k] = end;
+  }
+  if (end == 0) return hipSuccess;
+  return launch_kernel(copy_kernel, dim3((unsigned)((end + 255) / 256)), dim3(256), stream, p);
+}
 
 struct ScaleArgs {
   const void* dy;

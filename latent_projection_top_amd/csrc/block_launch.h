@@ -36,6 +36,7 @@ struct GemmArgs {
   int segments;
   int outputs;
   int act;
+  bool padded;  // contiguous lengths are zero-padded to multiples of 8 in memory
 };
 
 // What a product uses of its operator's workspace: a counter per column tile,
@@ -49,17 +50,35 @@ constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 128) * 64;
 constexpr int kMaxSplits = 64;
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
+// Whether launch_gemm takes the operands as they are (few rows): the other
+// products want them copied where needs_copy says so.
+bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red);
 // The area that products of up to m rows can use for split sums.
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs);
 
-// Tile kernel: shape 0..2 and K split; `aligned`: 16-byte loads fit.
+// Tile kernel: every operand 16-byte aligned, with row strides that are
+// multiples of 8 and contiguous lengths that are, or are zero-padded to,
+// multiples of 8. shape 0..2 and K split.
 struct TilePlan {
   int shape;
   int splits;
 };
-TilePlan plan_tiles(Mode mode, const GemmArgs& args, bool aligned, size_t partial_bytes);
-hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, bool aligned, const TilePlan& plan,
-                            float* partial, hipStream_t stream);
+TilePlan plan_tiles(Mode mode, const GemmArgs& args, size_t partial_bytes);
+hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, const TilePlan& plan, float* partial,
+                            hipStream_t stream);
+
+// A copy of a matrix of 16-bit values that the tile kernel can read: rows of
+// `len` values padded with zeros to a multiple of 8, which is the stride.
+struct Copy {
+  const void* src;
+  void* dst;
+  int64_t ld, rows;
+  int len;
+};
+hipError_t launch_copies(const Copy* copies, int count, hipStream_t stream);
+inline bool needs_copy(const void* p, int64_t ld, int64_t len) {
+  return (reinterpret_cast<uintptr_t>(p) & 15) != 0 || ((ld | len) & 7) != 0;
+}
 
 // Adds the splits' sums [splits][planes][m][n rounded up to 4] in split order
 // and ends the product (planes: 2 for kGated, else `outputs`).

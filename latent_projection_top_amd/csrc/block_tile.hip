@@ -93,25 +93,7 @@ struct Operand {
   static constexpr int kPair = 2048;
 };
 
-// `v` moved down by d elements of 16 bits, zeros from above (d >= 8: all).
-__device__ __forceinline__ u32x4 shift_down(u32x4 v, int d) {
-  if (d & 4) v = u32x4{v[2], v[3], 0, 0};
-  if (d & 2) v = u32x4{v[1], v[2], v[3], 0};
-  if (d & 1)
-    v = u32x4{v[0] >> 16 | v[1] << 16, v[1] >> 16 | v[2] << 16, v[2] >> 16 | v[3] << 16, v[3] >> 16};
-  return d >= 8 ? u32x4{0, 0, 0, 0} : v;
-}
-
-// (the address space is said where a pointer is made from an integer: a flat
-// load would also wait for LDS)
-#define global_mem __attribute__((address_space(1)))
-struct __attribute__((packed, aligned(4))) Dwords4 { u32x4 v; };
-
-// Direct: operands go from global memory straight to LDS. Otherwise (rows
-// that start at any element, contiguous lengths of any size from 8) they pass
-// through registers: a 16-byte load that would run past a row's end starts
-// earlier and is shifted into place before it is stored to LDS.
-template <typename T, int Mode, typename S, bool Direct>
+template <typename T, int Mode, typename S>
 __global__ __launch_bounds__(64 * S::NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* partial) {
   typedef Operand<Mode != kDw> A;
@@ -147,15 +129,14 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   const int s1 = (int)((int64_t)all * (split + 1) / splits);
   const int red = (int)p.red;
   const bool ragged = (red & (kStep - 1)) != 0;
-  // the tile reaches past an operand's rows or columns
-  const bool edge = row0 + S::BM > p.m || col0 + kCols > p.n;
 
   // ---- global -> LDS -------------------------------------------------------
   // Rows past the matrix's end repeat its last one and columns its last eight
   // (their sums are not stored); past the reduction's end lanes load zeros.
   // off: this lane's byte offset of each of the wave's loads from the stage's
   // first byte of its matrix (a wave's loads of B are all of one matrix).
-  // (through registers the offset of an r-contiguous piece leaves out r)
+  // Contiguous lengths that are no multiple of 8 are padded to one in memory.
+  const int64_t m8 = (p.m + 7) & ~7, n8 = (p.n + 7) & ~7;
   uint32_t off[S::PER];
   int red_of[S::PER];
   auto b_row = [&](int c) {
@@ -171,11 +152,11 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     const int k = is_a ? A::red(c, lane) : B::red(c, lane);
     red_of[i] = k;
     if (is_a)
-      off[i] = Mode != kDw ? (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + (Direct ? k : 0)) * 2u
-                           : (uint32_t)(k * p.lda + min(row0 + r, p.m - 8)) * 2u;
+      off[i] = Mode != kDw ? (uint32_t)((min(row0 + r, p.m - 1) - row0) * p.lda + k) * 2u
+                           : (uint32_t)(k * p.lda + min(row0 + r, m8 - 8)) * 2u;
     else
-      off[i] = Mode == kDx ? (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + (Direct ? k : 0)) * 2u
-                           : (uint32_t)(k * p.ldb + min(col0 + r, p.n - 8)) * 2u;
+      off[i] = Mode == kDx ? (uint32_t)((min(col0 + r, p.n - 1) - col0) * p.ldb + k) * 2u
+                           : (uint32_t)(k * p.ldb + min(col0 + r, (int)n8 - 8)) * 2u;
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(lds_void*)smem;
   // the matrices at stage 0 of each segment, and from one stage to the next
@@ -194,7 +175,7 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     return (is_a ? 0 : S::A_BYTES) + (wave + S::NW * (is_a ? i : i - S::A_PER)) * 1024;
   };
 
-  // Direct. Any stage; the last of a segment may be short.
+  // Any stage; the last of a segment may be short.
   auto issue_any = [&](int s, uint32_t buf, int i) __attribute__((always_inline)) {
     const int ks = s >= per_seg ? s - per_seg : s;
     const char* base = reinterpret_cast<const char*>(base_of(i < S::A_PER, s));
@@ -204,76 +185,6 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     } else {
       dma16(base, off[i], buf + slot(i));
     }
-  };
-
-  // Through registers. The r of an r-contiguous piece, the r row of the
-  // others, and their first column are clamped to the matrix; `shift_down`
-  // says by how much on the way to LDS. Rows may start at odd elements: a
-  // piece is loaded as the four dwords from its first element's and the dword
-  // of its last, and v_alignbit_b32 moves it into place.
-  struct Held {
-    u32x4 v;
-    uint32_t last;
-  };
-  Held held[4][Direct ? 1 : S::PER];  // stage q in set q % 4
-  auto fetch_at = [&](uintptr_t base, uint32_t o) __attribute__((always_inline)) -> Held {
-    o += (uint32_t)(base & 2);
-    base &= ~(uintptr_t)3;
-    Held h;
-    h.v = reinterpret_cast<const global_mem Dwords4*>(base + (o & ~3u))->v;
-    h.last = *reinterpret_cast<const global_mem uint32_t*>(base + ((o + 14) & ~3u));
-    return h;
-  };
-  constexpr bool kAr = Mode != kDw, kBr = Mode == kDx;  // r-contiguous
-  // offset of load i of any stage: what the clamps make of it
-  auto off_any = [&](int s, int i) __attribute__((always_inline)) -> uint32_t {
-    const int ks = s >= per_seg ? s - per_seg : s;
-    const int k = ks * kStep + red_of[i];
-    if (i < S::A_PER ? kAr : kBr) return off[i] + (uint32_t)(min(k, red - 8) - ks * kStep) * 2u;
-    return off[i] - (uint32_t)max(k - (red - 1), 0) * (uint32_t)(i < S::A_PER ? p.lda : p.ldb) * 2u;
-  };
-  auto align = [&](Held& h, uint32_t o) __attribute__((always_inline)) {
-    const uint32_t by = (o & 2) * 8;
-#pragma unroll
-    for (int q = 0; q < 3; ++q) h.v[q] = __builtin_amdgcn_alignbit(h.v[q + 1], h.v[q], by);
-    h.v[3] = __builtin_amdgcn_alignbit(h.last, h.v[3], by);
-  };
-  auto trim = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
-    const int ks = s >= per_seg ? s - per_seg : s;
-#pragma unroll
-    for (int i = 0; i < S::PER; ++i) {
-      const bool is_a = i < S::A_PER;
-      const int c = wave + S::NW * (is_a ? i : i - S::A_PER);
-      const int k = ks * kStep + red_of[i];
-      if (is_a ? kAr : kBr) {
-        h[i].v = shift_down(h[i].v, min(max(k - (red - 8), 0), 8));
-      } else {
-        const int over = is_a ? (int)(row0 + A::row(c, lane) - (p.m - 8)) : col0 + b_row(c) - (p.n - 8);
-        h[i].v = shift_down(h[i].v, k >= red ? 8 : min(max(over, 0), 8));
-      }
-    }
-  };
-  auto put = [&](uint32_t buf, int i, const Held& h) __attribute__((always_inline)) {
-    *(__attribute__((address_space(3))) u32x4*)(uintptr_t)(buf + slot(i) + lane * 16) = h.v;
-  };
-  auto fetch_any = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < S::PER; ++i) {
-      uintptr_t base = base_of(i < S::A_PER, s);
-      uint32_t o = off_any(s, i);
-      // a clamped r can lie before the stage's first: count from the row's
-      if (i < S::A_PER ? kAr : kBr) {
-        const uint32_t at = (uint32_t)(s >= per_seg ? s - per_seg : s) * (kStep * 2);
-        base -= at;
-        o += at;
-      }
-      h[i] = fetch_at(base, o);
-    }
-  };
-  auto arrange_any = [&](int s, Held(&h)[Direct ? 1 : S::PER]) __attribute__((always_inline)) {
-#pragma unroll
-    for (int i = 0; i < S::PER; ++i) align(h[i], off_any(s, i) + (uint32_t)(base_of(i < S::A_PER, s) & 2));
-    if (edge || (s >= per_seg ? s - per_seg : s) == per_seg - 1) trim(s, h);
   };
 
   // ---- LDS -> registers ----------------------------------------------------
@@ -292,11 +203,8 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
 
   // Stage s's MFMAs. Meanwhile the operands of stage s + 1 are read (a[i] as
   // soon as its last MFMA is issued, B into the other register set) and this
-  // wave's loads of a later stage go out. Direct: stage s + 4's, into the
+  // wave's loads of stage s + 4 go out, load(n) the n-th of them, into the
   // buffer of stage s - 1, which the barrier before this step has freed.
-  // Through registers: stage s + 6's, into one of four sets, while the set of
-  // stage s + 3 goes to LDS (into the buffer of stage s - 2), so that a load
-  // has three steps to arrive. load(n) does the n-th of PER shares of it.
   auto step = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT], uint32_t next, auto load) __attribute__((always_inline)) {
     constexpr int kEvery = S::MT * S::NT / S::PER;
 #pragma unroll
@@ -312,148 +220,87 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     }
   };
   static_assert(S::MT >= S::NT, "every B operand is read");
-  // At the end of stage s: stage s + 2 has to be in LDS (Direct: at most the
-  // loads of the stages after it still in flight; through registers: it was
-  // stored a step ago), and every read of stage s's buffer has to have
-  // returned (at most the reads of stage s + 1 outstanding).
+  // At the end of stage s: stage s + 2 has to be in LDS (at most the loads of
+  // the stages after it still in flight), and every read of stage s's buffer
+  // has to have returned (at most the reads of stage s + 1 outstanding).
   constexpr int kLgkm = kReads < 15 ? kReads : 15;
-  // (through registers the compiler waits for its own loads)
-  constexpr int kVm1 = Direct ? S::PER : 63, kVm2 = Direct ? 2 * S::PER : 63, kVm0 = Direct ? 0 : 63;
 
   const int count = s1 - s0;
   if (count > 0) {
-    // the first four stages; through registers: three, and three held
-    if constexpr (Direct) {
 #pragma unroll 1
-      for (int s = 0; s < min(count, 4); ++s)
+    for (int s = 0; s < min(count, 4); ++s)
 #pragma unroll
-        for (int i = 0; i < S::PER; ++i) issue_any(s0 + s, lds0 + s * S::STAGE, i);
-    } else {
-      // (stages past the end repeat the last one: no branches here)
-#pragma unroll
-      for (int s = 0; s < 4; ++s) fetch_any(min(s0 + s, s1 - 1), held[s]);
-#pragma unroll
-      for (int s = 0; s < 3; ++s) {
-        arrange_any(min(s0 + s, s1 - 1), held[s]);
-#pragma unroll
-        for (int i = 0; i < S::PER; ++i) put(lds0 + s * S::STAGE, i, held[s][i]);
-      }
-#pragma unroll
-      for (int s = 4; s < 6; ++s) fetch_any(min(s0 + s, s1 - 1), held[s & 3]);
-    }
+      for (int i = 0; i < S::PER; ++i) issue_any(s0 + s, lds0 + s * S::STAGE, i);
     if (count >= 4)
-      wait_barrier<kVm2, 0>();
+      wait_barrier<2 * S::PER, 0>();
     else
-      wait_barrier<kVm0, 0>();
+      wait_barrier<0, 0>();
 #pragma unroll
     for (int i = 0; i < S::MT; ++i) a[i] = read_a(lds0, i);
 #pragma unroll
     for (int j = 0; j < S::NT; ++j) b0[j] = read_b(lds0, j);
 
     constexpr uint32_t kEnd = kStages * S::STAGE;
-    // buffers of stage s + 1, and of stage s + 4 (through registers s + 3)
-    uint32_t next = lds0 + S::STAGE, fill = lds0 + (Direct ? 4 : 3) * S::STAGE;
+    uint32_t next = lds0 + S::STAGE, fill = lds0 + 4 * S::STAGE;  // buffers of stages s + 1 and s + 4
     auto advance = [&]() __attribute__((always_inline)) {
       next = next + S::STAGE == lds0 + kEnd ? lds0 : next + S::STAGE;
       fill = fill + S::STAGE == lds0 + kEnd ? lds0 : fill + S::STAGE;
     };
-    // step s with s % kTurns == u: register sets by number
-    constexpr int kTurns = Direct ? 2 : 4, kAhead = Direct ? 4 : 6;
+    // Steady state: the stages to load are whole and follow each other. Two
+    // steps a turn, for the two B register sets.
     int s = 0;
-    // Steady state: the stages to load are whole and follow each other.
     uintptr_t a_next = 0, b_next = 0;
-    auto steady = [&](auto u_) __attribute__((always_inline)) {
-      constexpr int u = decltype(u_)::value;
-      Held(&in)[Direct ? 1 : S::PER] = held[(u + 2) & 3];
-      Held(&out)[Direct ? 1 : S::PER] = held[(u + 3) & 3];
-      if constexpr (!Direct) {
-#pragma unroll
-        for (int i = 0; i < S::PER; ++i) {
-          const bool is_a = i < S::A_PER;
-          const uint32_t o = off[i] + ((is_a ? kAr : kBr) ? 2u * red_of[i] : 0u);
-          in[i] = fetch_at(is_a ? a_next : b_next, o);
-          align(out[i], o + (uint32_t)((is_a ? a_next : b_next) & 2));
-        }
-        if (edge) trim(s0 + s + u + 3, out);
-      }
+    auto steady = [&](u32x4(&b)[S::NT], u32x4(&bn)[S::NT]) __attribute__((always_inline)) {
       auto load = [&](int n) __attribute__((always_inline)) {
-        if constexpr (Direct)
-          dma16(reinterpret_cast<const char*>(n < S::A_PER ? a_next : b_next), off[n], fill + slot(n));
-        else
-          put(fill, n, out[n]);
+        dma16(reinterpret_cast<const char*>(n < S::A_PER ? a_next : b_next), off[n], fill + slot(n));
       };
-      step((u & 1) ? b1 : b0, (u & 1) ? b0 : b1, next, load);
-      wait_barrier<kVm2, kLgkm>();
+      step(b, bn, next, load);
+      wait_barrier<2 * S::PER, kLgkm>();
       advance();
       a_next += a_step;
       b_next += b_step;
     };
     // Any step: the ends of the segments.
-    auto other = [&](auto u_) __attribute__((always_inline)) {
-      constexpr int u = decltype(u_)::value;
-      const int q = s + u;
+    auto other = [&](int q, u32x4(&b)[S::NT], u32x4(&bn)[S::NT]) __attribute__((always_inline)) {
       if (q >= count) return;
-      const bool issue = q + kAhead < count, write = q + 3 < count;
-      Held(&in)[Direct ? 1 : S::PER] = held[(u + 2) & 3];
-      Held(&out)[Direct ? 1 : S::PER] = held[(u + 3) & 3];
-      if constexpr (!Direct) {
-        if (issue) fetch_any(s0 + q + kAhead, in);
-        if (write) arrange_any(s0 + q + 3, out);
-      }
+      const bool issue = q + 4 < count;
       auto load = [&](int n) __attribute__((always_inline)) {
-        if constexpr (Direct) {
-          if (issue) issue_any(s0 + q + kAhead, fill, n);
-        } else {
-          if (write) put(fill, n, out[n]);
-        }
+        if (issue) issue_any(s0 + q + 4, fill, n);
       };
-      step((u & 1) ? b1 : b0, (u & 1) ? b0 : b1, next, load);
+      step(b, bn, next, load);
       if (q + 2 < count) {
         if (q + 4 < count)
-          wait_barrier<kVm2, kLgkm>();
+          wait_barrier<2 * S::PER, kLgkm>();
         else if (q + 3 < count)
-          wait_barrier<kVm1, kLgkm>();
+          wait_barrier<S::PER, kLgkm>();
         else
-          wait_barrier<kVm0, kLgkm>();
+          wait_barrier<0, kLgkm>();
       }
       advance();
     };
-    using std::integral_constant;
     auto whole_stages = [&]() __attribute__((always_inline)) {
-      const int first = s0 + s + kAhead;  // the next stage to load
+      const int first = s0 + s + 4;  // the next stage to load
       const int limit = min(s1, (first >= per_seg ? 2 : 1) * per_seg - (ragged ? 1 : 0));
       a_next = base_of(true, first);
       b_next = base_of(false, first);
 #pragma unroll 1
-      for (int t = first; t + kTurns <= limit; t += kTurns) {
-        steady(integral_constant<int, 0>{});
-        steady(integral_constant<int, 1>{});
-        if constexpr (kTurns == 4) {
-          steady(integral_constant<int, 2>{});
-          steady(integral_constant<int, 3>{});
-        }
-        s += kTurns;
+      for (int t = first; t + 2 <= limit; t += 2) {
+        steady(b0, b1);
+        steady(b1, b0);
+        s += 2;
       }
     };
     auto other_stages = [&](int end) __attribute__((always_inline)) {
 #pragma unroll 1
-      for (; s < end; s += kTurns) {
-        other(integral_constant<int, 0>{});
-        other(integral_constant<int, 1>{});
-        if constexpr (kTurns == 4) {
-          other(integral_constant<int, 2>{});
-          other(integral_constant<int, 3>{});
-        }
+      for (; s < end; s += 2) {
+        other(s, b0, b1);
+        other(s + 1, b1, b0);
       }
     };
-    // (through registers, stage s + 3 on its way to LDS and stage s + 6 to load
-    // have to be of one segment)
-    if (Direct || Mode != kDx || s0 + 3 >= per_seg || s0 + kAhead < per_seg) whole_stages();
+    whole_stages();
     if constexpr (Mode == kDx) {
-      // past the first segment's end: until the next stage to load (through
-      // registers: to store) is of the second
-      if (s0 < per_seg && s1 > per_seg) {
-        other_stages(min(count, per_seg - s0 - (Direct ? kAhead : 3)));
+      if (s0 < per_seg && s1 > per_seg) {  // over to the second segment
+        other_stages(min(count, per_seg - s0 - 4));
         whole_stages();
       }
     }
@@ -523,12 +370,12 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   }
 }
 
-template <typename T, int Mode, typename S, bool Direct>
+template <typename T, int Mode, typename S>
 static hipError_t launch_shape(const GemmArgs& p, int splits, float* partial, hipStream_t stream) {
   constexpr int kCols = Mode == kGated ? S::BN / 2 : S::BN;
   const int mt = (int)((p.m + S::BM - 1) / S::BM), nt = (p.n + kCols - 1) / kCols;
   const int64_t blocks = (int64_t)mt * nt * p.outputs * splits;
-  const hipError_t e = launch_kernel(gemm_tile_kernel<T, Mode, S, Direct>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
+  const hipError_t e = launch_kernel(gemm_tile_kernel<T, Mode, S>, dim3((unsigned)blocks), dim3(64 * S::NW), stream,
                                      p, mt, nt, splits, partial);
   if (e != hipSuccess || splits == 1) return e;
   return launch_gemm_join(T::code, (enum Mode)Mode, p, splits, partial, stream);
@@ -539,33 +386,29 @@ typedef TileShape<128, 256, 2, 4> Wide;
 typedef TileShape<128, 128, 2, 2> Small;
 
 template <typename T, int Mode>
-static hipError_t launch_mode(const GemmArgs& p, bool aligned, const TilePlan& t, float* partial, hipStream_t stream) {
+static hipError_t launch_mode(const GemmArgs& p, const TilePlan& t, float* partial, hipStream_t stream) {
   switch (t.shape) {
-    case 0: return launch_shape<T, Mode, Large, true>(p, t.splits, partial, stream);
-    case 1:
-      return aligned ? launch_shape<T, Mode, Wide, true>(p, t.splits, partial, stream)
-                     : launch_shape<T, Mode, Wide, false>(p, t.splits, partial, stream);
-    default:
-      return aligned ? launch_shape<T, Mode, Small, true>(p, t.splits, partial, stream)
-                     : launch_shape<T, Mode, Small, false>(p, t.splits, partial, stream);
+    case 0: return launch_shape<T, Mode, Large>(p, t.splits, partial, stream);
+    case 1: return launch_shape<T, Mode, Wide>(p, t.splits, partial, stream);
+    default: return launch_shape<T, Mode, Small>(p, t.splits, partial, stream);
   }
 }
 
 template <typename T>
-static hipError_t launch_typed(Mode mode, const GemmArgs& p, bool aligned, const TilePlan& t, float* partial,
+static hipError_t launch_typed(Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
                                hipStream_t stream) {
   switch (mode) {
-    case kLinear: return launch_mode<T, kLinear>(p, aligned, t, partial, stream);
-    case kGated: return launch_mode<T, kGated>(p, aligned, t, partial, stream);
-    case kDx: return launch_mode<T, kDx>(p, aligned, t, partial, stream);
-    default: return launch_mode<T, kDw>(p, aligned, t, partial, stream);
+    case kLinear: return launch_mode<T, kLinear>(p, t, partial, stream);
+    case kGated: return launch_mode<T, kGated>(p, t, partial, stream);
+    case kDx: return launch_mode<T, kDx>(p, t, partial, stream);
+    default: return launch_mode<T, kDw>(p, t, partial, stream);
   }
 }
 
-hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, bool aligned, const TilePlan& t, float* partial,
+hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TilePlan& t, float* partial,
                             hipStream_t stream) {
-  return dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, aligned, t, partial, stream)
-                             : launch_typed<F16>(mode, p, aligned, t, partial, stream);
+  return dtype == BLOCK_BF16 ? launch_typed<BF16>(mode, p, t, partial, stream)
+                             : launch_typed<F16>(mode, p, t, partial, stream);
 }
 
 // Tile shape and K split of a product: the ones whose modelled time is least.
@@ -575,9 +418,8 @@ hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, bool aligne
 // of blocks starts and ends in about 2 us; a split costs 5 us and its sums
 // twice at 4.2 TB/s. So large tiles where they fill the CUs (4096 x 3584 ->
 // 4096: 98 us against 129 and 150), small ones for few rows (128 rows, 3584 ->
-// 4096, 8 splits: 17.9 us; 256 x 256, 12 splits: 23.7). Through registers
-// (unaligned) the large tile's accumulators leave no room for the loads.
-TilePlan plan_tiles(Mode mode, const GemmArgs& p, bool aligned, size_t partial_bytes) {
+// 4096, 8 splits: 17.9 us; 256 x 256, 12 splits: 23.7).
+TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   struct Cost { int bm, bn; double few, full; } const shapes[3] = {
       {256, 256, 0.63, 0.87}, {128, 256, 0.42, 0.58}, {128, 128, 0.35, 0.39}};
   const double pair = 0.65;
@@ -585,7 +427,7 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& p, bool aligned, size_t partial_b
   const int planes = mode == kGated ? 2 : p.outputs;
   TilePlan best{2, 1};
   double best_t = 0;
-  for (int k = aligned ? 0 : 1; k < 3; ++k) {
+  for (int k = 0; k < 3; ++k) {
     const Cost& c = shapes[k];
     const int bn = mode == kGated ? c.bn / 2 : c.bn;
     const int64_t tiles = (int64_t)((p.m + c.bm - 1) / c.bm) * ((p.n + bn - 1) / bn) * p.outputs;
