@@ -282,7 +282,8 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   char* ws = static_cast<char*>(workspace);
   void* dz[2] = {ws + plan->off_dz, ws + plan->off_du};
   const void* slopes[2] = {d_gate, d_up};
-  int st = status_of(block::launch_scale(c.dtype, dh, dh_stride, slopes, 2, dz, padded(c.inner), rows, c.inner, s));
+  int st = status_of(block::launch_scale(c.dtype, dh, dh_stride, slopes, 2, dz, padded(c.inner), rows, c.inner,
+                                          nullptr, nullptr, s));
   if (st != ROUTE_OK) return st;
   Copies copies;
   int64_t ldg = c.inner, ldu = c.inner;
@@ -421,18 +422,16 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   char* ws = static_cast<char*>(workspace);
   const void* dz = dy;
   int64_t ldz = dy_stride;
-  if (scaled) {
-    void* out = ws + plan->off_dz;
-    const int st = status_of(block::launch_scale(c.dtype, dy, dy_stride, &slope, 1, &out, padded(c.outputs), rows,
-                                                 c.outputs, s));
+  void* out = scaled && (dx != nullptr || dw != nullptr) ? ws + plan->off_dz : nullptr;
+  if (scaled || dbias != nullptr) {
+    const int st = status_of(block::launch_scale(c.dtype, dy, dy_stride, &slope, scaled ? 1 : 0, &out,
+                                                 padded(c.outputs), rows, c.outputs, dbias,
+                                                 reinterpret_cast<float*>(ws + plan->off_sum), s));
     if (st != ROUTE_OK) return st;
+  }
+  if (scaled) {
     dz = out;
     ldz = padded(c.outputs);
-  }
-  if (dbias != nullptr) {
-    const int st = status_of(block::launch_column_sum(c.dtype, dz, ldz, rows, c.outputs, dbias,
-                                                      reinterpret_cast<float*>(ws + plan->off_sum), s));
-    if (st != ROUTE_OK) return st;
   }
   Copies copies;
   int64_t ldw = c.outputs;

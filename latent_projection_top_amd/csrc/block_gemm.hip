@@ -219,88 +219,121 @@ hipError_t launch_copies(const Copy* copies, int count, hipStream_t stream) {
   return launch_kernel(copy_kernel, dim3((unsigned)((end + 255) / 256)), dim3(256), stream, p);
 }
 
+// The first half of a backward pass: out[k] = dy * s[k], rounded to the
+// products' type, and where dbias is wanted the column sums of the unrounded
+// out[0] (of dy itself where there is no s). One pass over its inputs, bound
+// by HBM: a thread owns eight columns and walks down every gridDim.y-th row.
 struct ScaleArgs {
   const void* dy;
   const void* s[2];
   void* out[2];
-  int64_t dy_stride, ld;
+  float* partial;  // [gridDim.y][n rounded up to 8], or NULL
+  int64_t dy_stride, ld, rows;
   int n;
 };
 
-template <typename T, int Count>
+template <typename T, int Count, bool Sum>
 __global__ __launch_bounds__(256) void scale_kernel(ScaleArgs p) {
-  const int64_t row = blockIdx.y;
   const int col = 8 * (blockIdx.x * 256 + threadIdx.x);
   if (col >= p.n) return;
   const int count = min(8, p.n - col);
-  const u32x4 dy = load8(static_cast<const uint16_t*>(p.dy) + row * p.dy_stride + col, count);
+  float sum[8] = {};
+#pragma unroll 2
+  for (int64_t row = blockIdx.y; row < p.rows; row += gridDim.y) {
+    const u32x4 dy = load8(static_cast<const uint16_t*>(p.dy) + row * p.dy_stride + col, count);
+    float d[8];
 #pragma unroll
-  for (int k = 0; k < Count; ++k) {
-    const u32x4 s = load8(static_cast<const uint16_t*>(p.s[k]) + row * p.n + col, count);
-    u32x4 o = {0, 0, 0, 0};
+    for (int i = 0; i < 8; ++i) d[i] = T::load((uint16_t)(dy[i >> 1] >> (16 * (i & 1))));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float v = T::load((uint16_t)(dy[i >> 1] >> (16 * (i & 1)))) *
-                      T::load((uint16_t)(s[i >> 1] >> (16 * (i & 1))));
-      o[i >> 1] |= (uint32_t)T::store(v) << (16 * (i & 1));
+    for (int k = 0; k < Count; ++k) {
+      const u32x4 s = load8(static_cast<const uint16_t*>(p.s[k]) + row * p.n + col, count);
+      u32x4 o = {0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float v = d[i] * T::load((uint16_t)(s[i >> 1] >> (16 * (i & 1))));
+        o[i >> 1] |= (uint32_t)T::store(v) << (16 * (i & 1));
+        if (Sum) sum[i] += v;
+      }
+      // the row stride is a multiple of 8: the last piece pads with zeros
+      if (p.out[k] != nullptr)
+        *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out[k]) + row * p.ld + col) = o;
     }
-    // the row stride is a multiple of 8, so the last piece may run past n
-    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out[k]) + row * p.ld + col) = o;
+    if (Sum && Count == 0)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sum[i] += d[i];
+  }
+  if (Sum) {
+    float* d = p.partial + (int64_t)blockIdx.y * ((p.n + 7) & ~7) + col;
+    *reinterpret_cast<f32x4*>(d) = f32x4{sum[0], sum[1], sum[2], sum[3]};
+    *reinterpret_cast<f32x4*>(d + 4) = f32x4{sum[4], sum[5], sum[6], sum[7]};
   }
 }
 
+// Adds the blocks' column sums: 32 columns per block, 32 slices of the
+// blocks, each slice and then the slices in order.
 template <typename T>
-static hipError_t scale_typed(const ScaleArgs& p, int count, int64_t rows, hipStream_t stream) {
-  // rows in launches of at most 65535 (the grid's y limit)
-  for (int64_t r = 0; r < rows; r += 65535) {
-    ScaleArgs q = p;
-    q.dy = static_cast<const uint16_t*>(p.dy) + r * p.dy_stride;
-    for (int k = 0; k < count; ++k) {
-      q.s[k] = static_cast<const uint16_t*>(p.s[k]) + r * p.n;
-      q.out[k] = static_cast<uint16_t*>(p.out[k]) + r * p.ld;
-    }
-    const dim3 grid((p.n + 2047) / 2048, (unsigned)(rows - r < 65535 ? rows - r : 65535));
-    const hipError_t e = count == 2 ? launch_kernel(scale_kernel<T, 2>, grid, dim3(256), stream, q)
-                                    : launch_kernel(scale_kernel<T, 1>, grid, dim3(256), stream, q);
-    if (e != hipSuccess) return e;
-  }
-  return hipSuccess;
+__global__ __launch_bounds__(256) void column_join_kernel(const float* partial, int blocks, int n, uint16_t* dst) {
+  __shared__ f32x4 part[32][8];
+  const int64_t ld = (n + 7) & ~7;
+  const int q = threadIdx.x & 7, slice = threadIdx.x >> 3;
+  const int c = (blockIdx.x * 8 + q) * 4;
+  f32x4 s = {0.f, 0.f, 0.f, 0.f};
+  if (c < n)
+#pragma unroll 8
+    for (int b = slice; b < blocks; b += 32) s += *reinterpret_cast<const f32x4*>(partial + (int64_t)b * ld + c);
+  part[slice][q] = s;
+  __syncthreads();
+  const int t = threadIdx.x, col = blockIdx.x * 32 + t;
+  if (t >= 32 || col >= n) return;
+  float v = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v += part[i][t >> 2][t & 3];
+  dst[col] = T::store(v);
+}
+
+// Blocks of rows: enough to fill the CUs, and for sums no more (each writes a
+// row of partial sums).
+static int scale_blocks(int64_t rows, int n, bool sum) {
+  const int64_t across = ((int64_t)n + 2047) / 2048;
+  int64_t most = (sum ? 1024 : 2048) / across;
+  if (most < 1) most = 1;
+  return (int)(rows < most ? (rows > 0 ? rows : 1) : most);
+}
+
+template <typename T>
+static hipError_t scale_typed(const ScaleArgs& p, int count, void* dbias, hipStream_t stream) {
+  const int blocks = scale_blocks(p.rows, p.n, dbias != nullptr);
+  const dim3 grid((p.n + 2047) / 2048, blocks);
+  hipError_t e;
+  if (dbias == nullptr)
+    e = launch_kernel(count == 2 ? scale_kernel<T, 2, false> : scale_kernel<T, 1, false>, grid, dim3(256), stream, p);
+  else
+    e = launch_kernel(count == 1 ? scale_kernel<T, 1, true> : scale_kernel<T, 0, true>, grid, dim3(256), stream, p);
+  if (e != hipSuccess || dbias == nullptr) return e;
+  return launch_kernel(column_join_kernel<T>, dim3((p.n + 31) / 32), dim3(256), stream,
+                       static_cast<const float*>(p.partial), blocks, p.n, static_cast<uint16_t*>(dbias));
 }
 
 hipError_t launch_scale(int dtype, const void* dy, int64_t dy_stride, const void* const* s, int count,
-                        void* const* out, int64_t ld, int64_t rows, int n, hipStream_t stream) {
-  ScaleArgs p{dy, {s[0], count > 1 ? s[1] : nullptr}, {out[0], count > 1 ? out[1] : nullptr}, dy_stride, ld, n};
-  return dtype == BLOCK_BF16 ? scale_typed<BF16>(p, count, rows, stream)
-                             : scale_typed<F16>(p, count, rows, stream);
+                        void* const* out, int64_t ld, int64_t rows, int n, void* dbias, float* partial,
+                        hipStream_t stream) {
+  ScaleArgs p{};
+  p.dy = dy;
+  for (int k = 0; k < count; ++k) {
+    p.s[k] = s[k];
+    p.out[k] = out[k];
+  }
+  p.partial = partial;
+  p.dy_stride = dy_stride;
+  p.ld = ld;
+  p.rows = rows;
+  p.n = n;
+  return dtype == BLOCK_BF16 ? scale_typed<BF16>(p, count, dbias, stream)
+                             : scale_typed<F16>(p, count, dbias, stream);
 }
 
-// Column sums: blocks of 64 columns, four row lanes each, the four joined in
-// a fixed order.
-template <typename T>
-__global__ __launch_bounds__(256) void column_sum_kernel(const uint16_t* src, int64_t ld, int64_t rows, int n,
-                                                         uint16_t* dst) {
-  __shared__ float red[256];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63);
-  float s = 0.f;
-  if (col < n)
-    for (int64_t r = threadIdx.x >> 6; r < rows; r += 4) s += T::load(src[r * ld + col]);
-  red[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x < 64 && col < n)
-    dst[col] = T::store((red[threadIdx.x] + red[threadIdx.x + 64]) +
-                        (red[threadIdx.x + 128] + red[threadIdx.x + 192]));
+size_t column_sum_bytes(int64_t rows, int n) {
+  return (size_t)scale_blocks(rows, n, true) * ((n + 7) & ~7) * 4;
 }
-
-hipError_t launch_column_sum(int dtype, const void* src, int64_t ld, int64_t rows, int n, void* dst,
-                             float* partial, hipStream_t stream) {
-  (void)partial;
-  const dim3 grid((n + 63) / 64);
-  const uint16_t* s = static_cast<const uint16_t*>(src);
-  uint16_t* d = static_cast<uint16_t*>(dst);
-  return dtype == BLOCK_BF16 ? launch_kernel(column_sum_kernel<BF16>, grid, dim3(256), stream, s, ld, rows, n, d)
-                             : launch_kernel(column_sum_kernel<F16>, grid, dim3(256), stream, s, ld, rows, n, d);
-}
-
-size_t column_sum_bytes(int64_t, int) { return 0; }
 
 }  // namespace block

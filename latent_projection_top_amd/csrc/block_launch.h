@@ -89,13 +89,12 @@ hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& args, int spli
 constexpr int kStreamRows = 32;
 hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
 
-// Elementwise first half of the backward passes, and the column sums.
-// out[i] [rows][ld] = dy * s[i]; n columns.
+// out[k] [rows][ld] = dy * s[k] for `count` (0..2) matrices of derivatives
+// [rows][n]; out[k] may be NULL. With dbias [n] (count 0 or 1), also the column
+// sums, through `partial` (column_sum_bytes).
 hipError_t launch_scale(int dtype, const void* dy, int64_t dy_stride, const void* const* s, int count,
-                        void* const* out, int64_t ld, int64_t rows, int n, hipStream_t stream);
-// dst[n] (dtype) = sum over rows of src.
-hipError_t launch_column_sum(int dtype, const void* src, int64_t ld, int64_t rows, int n, void* dst,
-                             float* partial, hipStream_t stream);
+                        void* const* out, int64_t ld, int64_t rows, int n, void* dbias, float* partial,
+                        hipStream_t stream);
 size_t column_sum_bytes(int64_t rows, int n);
 
 struct NormArgs {
