@@ -79,26 +79,32 @@ struct ValueSlope {
   float d;  // act'(z)
 };
 
-// The arguments of terms that vanish for large |z| are clamped where the term
-// is already 0 in FP32, so that they stay 0 and not infinity times 0.
+// sigmoid(z) from v_exp_f32 and v_rcp_f32 (1 ulp each; a full division would
+// double the instructions of an epilogue that is bound by them).
+__device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf(1.f + __expf(-z)); }
+
+// The tanh form of GELU is z sigmoid(2 y), y = sqrt(2/pi) (z + 0.044715 z^3).
+// In derivatives the arguments of terms that vanish for large |z| are clamped
+// where the term is already 0 in FP32, so that they stay 0 and not infinity
+// times 0.
 template <int Act>
 __device__ __forceinline__ ValueSlope activate(float z) {
-  if constexpr (Act == BLOCK_ACT_RELU) {
+  if constexpr (Act == BLOCK_ACT_NONE) {
+    return {z, 1.f};
+  } else if constexpr (Act == BLOCK_ACT_RELU) {
     return {z < 0.f ? 0.f : z, z > 0.f ? 1.f : (z == z ? 0.f : z)};
   } else if constexpr (Act == BLOCK_ACT_SILU) {
-    const float s = 1.f / (1.f + __expf(-z));
+    const float s = sigmoid(z);
     return {z * s, s * (1.f + z * (1.f - s))};
   } else if constexpr (Act == BLOCK_ACT_GELU) {
     const float cdf = 0.5f * (1.f + erff(z * 0.70710678118654752f));
     const float zc = fminf(fmaxf(z, -20.f), 20.f);  // exp(-200) is 0 in FP32
     return {z * cdf, cdf + zc * (__expf(-0.5f * zc * zc) * 0.39894228040143268f)};
   } else {
-    const float c = 0.79788456080286536f;
-    const float zc = fminf(fmaxf(z, -10.f), 10.f);  // tanh of +-43 is +-1 in FP32
-    const float q = zc * zc;
-    const float t = 1.f - 2.f / (1.f + __expf(2.f * c * zc * (1.f + 0.044715f * q)));
-    const float half = 0.5f * (1.f + t);
-    return {z * half, half + 0.5f * zc * (1.f - t * t) * c * (1.f + 3.f * 0.044715f * q)};
+    const float c = 1.5957691216057308f;  // 2 sqrt(2/pi)
+    const float s = sigmoid(c * z * (1.f + 0.044715f * z * z));
+    const float zc = fminf(fmaxf(z, -10.f), 10.f);  // 1 - s is 0 or s is below 1e-37
+    return {z * s, s + zc * s * (1.f - s) * c * (1.f + 3.f * 0.044715f * zc * zc)};
   }
 }
 
@@ -107,6 +113,7 @@ __device__ __forceinline__ ValueSlope activate(float z) {
 template <typename F>
 __device__ __forceinline__ void with_activation(int act, F f) {
   switch (act) {
+    case BLOCK_ACT_NONE: f(std::integral_constant<int, BLOCK_ACT_NONE>{}); break;
     case BLOCK_ACT_RELU: f(std::integral_constant<int, BLOCK_ACT_RELU>{}); break;
     case BLOCK_ACT_SILU: f(std::integral_constant<int, BLOCK_ACT_SILU>{}); break;
     case BLOCK_ACT_GELU: f(std::integral_constant<int, BLOCK_ACT_GELU>{}); break;
@@ -157,65 +164,65 @@ __device__ __forceinline__ void load_cols(const typename T::raw* p, float (&v)[C
 }
 
 // The end of a product: `v` (and for the gated product `u`) are the FP32 sums
-// of columns col .. col + C - 1 of output row `row`; `which` selects the
-// output matrix of a product with two. Everything happens in FP32 and each
-// output is rounded once. The derivatives kept for the backward pass are
-// rounded to the activations' type like everything else a training step
-// keeps: FP32 would double the bytes of what is, per layer, the largest
-// thing kept. It costs one rounding of three in the gradients (an RMS of 1.7
-// instead of 1.4 roundings).
+// of columns col .. col + C - 1 of output row `row`, `bias` and `residual`
+// (kLinear; zeros if there is none) what is added before and after the
+// activation; `which` selects the output matrix of a product with two.
+// Everything happens in FP32 and each output is rounded once. Save: also the
+// derivatives for the backward pass, rounded to the activations' type like
+// everything else a training step keeps: FP32 would double the bytes of what
+// is, per layer, the largest thing kept. It costs one rounding of three in
+// the gradients (an RMS of 1.7 instead of 1.4 roundings).
+template <typename T, int Mode, int Act, bool Save, int C>
+__device__ __forceinline__ void finish(const GemmArgs& p, int which, int64_t row, int col, float (&v)[C],
+                                       const float (&u)[C], const float (&bias)[C], const float (&residual)[C]) {
+  typedef typename T::raw raw;
+  const int count = p.n - col;
+  if (row >= p.m || count <= 0) return;
+  if constexpr (Mode == kGated || Mode == kLinear) {
+    float d0[C], d1[C];
+#pragma unroll
+    for (int t = 0; t < C; ++t) {
+      const ValueSlope s = activate<Act>(Mode == kLinear ? v[t] + bias[t] : v[t]);
+      v[t] = Mode == kLinear ? s.a + residual[t] : s.a * u[t];
+      d0[t] = Mode == kLinear ? s.d : s.d * u[t];
+      d1[t] = s.a;
+    }
+    if constexpr (Save) {
+      store_cols<T, C>(static_cast<raw*>(p.saved[0]) + row * p.n + col, d0, count);
+      if (Mode == kGated) store_cols<T, C>(static_cast<raw*>(p.saved[1]) + row * p.n + col, d1, count);
+    }
+  }
+  store_cols<T, C>(static_cast<raw*>(p.c[which]) + row * p.ldc + col, v, count);
+}
+
+// Calls f(activation constant, save constant) for the product `p` ends in.
+template <int Mode, typename F>
+__device__ __forceinline__ void with_ending(const GemmArgs& p, F f) {
+  if constexpr (Mode == kGated || Mode == kLinear) {
+    with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+      if constexpr (Mode == kGated && decltype(act)::value == BLOCK_ACT_NONE) return;  // not a gated activation
+      else if (decltype(act)::value != BLOCK_ACT_NONE && p.saved[0] != nullptr) f(act, std::true_type{});
+      else f(act, std::false_type{});
+    });
+  } else {
+    f(std::integral_constant<int, BLOCK_ACT_NONE>{}, std::false_type{});
+  }
+}
+
+// finish() for one group of columns, bias and residual read here.
 template <typename T, int Mode, int C>
 __device__ __forceinline__ void epilogue(const GemmArgs& p, int which, int64_t row, int col, float (&v)[C],
                                          float (&u)[C]) {
   typedef typename T::raw raw;
-  const int count = p.n - col;
-  if (row >= p.m || count <= 0) return;
-  raw* c = static_cast<raw*>(p.c[which]) + row * p.ldc + col;
-  if constexpr (Mode == kGated) {
-    float dg[C], du[C];
-    with_activation(p.act, [&](auto act) {
-#pragma unroll
-      for (int t = 0; t < C; ++t) {
-        const ValueSlope s = activate<decltype(act)::value>(v[t]);
-        v[t] = s.a * u[t];
-        dg[t] = s.d * u[t];
-        du[t] = s.a;
-      }
-    });
-    store_cols<T, C>(c, v, count);
-    if (p.saved[0] != nullptr) {
-      store_cols<T, C>(static_cast<raw*>(p.saved[0]) + row * p.n + col, dg, count);
-      store_cols<T, C>(static_cast<raw*>(p.saved[1]) + row * p.n + col, du, count);
-    }
-  } else if constexpr (Mode == kLinear) {
-    if (p.bias != nullptr) {
-      float b[C];
-      load_cols<T, C>(static_cast<const raw*>(p.bias) + col, b, count);
-#pragma unroll
-      for (int t = 0; t < C; ++t) v[t] += b[t];
-    }
-    if (p.act != BLOCK_ACT_NONE) {
-      float d[C];
-      with_activation(p.act, [&](auto act) {
-#pragma unroll
-        for (int t = 0; t < C; ++t) {
-          const ValueSlope s = activate<decltype(act)::value>(v[t]);
-          v[t] = s.a;
-          d[t] = s.d;
-        }
-      });
-      if (p.saved[0] != nullptr) store_cols<T, C>(static_cast<raw*>(p.saved[0]) + row * p.n + col, d, count);
-    }
-    if (p.residual != nullptr) {
-      float r[C];
-      load_cols<T, C>(static_cast<const raw*>(p.residual) + row * p.ldr + col, r, count);
-#pragma unroll
-      for (int t = 0; t < C; ++t) v[t] += r[t];
-    }
-    store_cols<T, C>(c, v, count);
-  } else {
-    store_cols<T, C>(c, v, count);
+  float bias[C] = {}, residual[C] = {};
+  if (Mode == kLinear && row < p.m && col < p.n) {
+    if (p.bias != nullptr) load_cols<T, C>(static_cast<const raw*>(p.bias) + col, bias, p.n - col);
+    if (p.residual != nullptr)
+      load_cols<T, C>(static_cast<const raw*>(p.residual) + row * p.ldr + col, residual, p.n - col);
   }
+  with_ending<Mode>(p, [&](auto act, auto save) __attribute__((always_inline)) {
+    finish<T, Mode, decltype(act)::value, decltype(save)::value, C>(p, which, row, col, v, u, bias, residual);
+  });
 }
 
 }  // namespace block

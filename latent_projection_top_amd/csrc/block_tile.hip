@@ -338,34 +338,79 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   static_assert(S::NW * 16 * kRows * kPitch * 4 <= kStages * S::STAGE && S::MT % kRows == 0, "LDS");
   constexpr int kWide = Mode == kGated ? 8 * S::NT : 16 * S::NT;  // output columns of a wave
   constexpr int kLanes = kWide / 8;                               // lanes of a row
+  constexpr int kStepRows = 64 / kLanes;                          // rows of a wave at once
+  constexpr int kSteps = 16 * kRows / kStepRows, kGroup = kSteps < 4 ? kSteps : 4;
   float* turn = reinterpret_cast<float*>(smem) + wave * 16 * kRows * kPitch;
   const int64_t wrow = row0 + 16 * S::MT * wm + lane / kLanes;
-  const int wcol = 8 * (lane % kLanes);
+  const int wcol = 8 * (lane % kLanes), col = col0 + kWide * wn + wcol;
+  float bias[8] = {};
+  if (Mode == kLinear && p.bias != nullptr && col < p.n)
+    load_cols<T, 8>(static_cast<const typename T::raw*>(p.bias) + col, bias, p.n - col);
+  // The residual's loads are a group of steps ahead of their use: read where
+  // it is used, each of them would cost the wave a trip to HBM (17 us of a
+  // 2048 x 3584 -> 7168 product).
+  const bool add = Mode == kLinear && p.residual != nullptr;
+  u32x4 res[kGroup], ahead[kGroup];
+  auto fetch = [&](u32x4(&d)[kGroup], int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kGroup; ++q) {
+      d[q] = u32x4{0, 0, 0, 0};
+      const int64_t r = row + q * kStepRows;
+      const uint16_t* src = static_cast<const uint16_t*>(p.residual) + r * p.ldr + col;
+      if (r < p.m && col + 8 <= p.n) {
+        d[q] = reinterpret_cast<const Any16*>(src)->v;
+      } else if (r < p.m) {
+#pragma unroll
+        for (int t = 0; t < 7; ++t)
+          if (col + t < p.n) d[q][t >> 1] |= (uint32_t)src[t] << (16 * (t & 1));
+      }
+    }
+  };
+  if (add) fetch(ahead, wrow);
   __syncthreads();
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < S::MT / kRows; ++c) {
+    // (the sums' registers are known by number only: one branch per turn)
 #pragma unroll
-    for (int i = 0; i < kRows; ++i)
+    for (int cc = 0; cc < S::MT / kRows; ++cc)
+      if (c == cc)
 #pragma unroll
-      for (int j = 0; j < S::NT; ++j)
-        *reinterpret_cast<f32x4*>(turn + (16 * i + m) * kPitch + 16 * j + 4 * g) = acc[kRows * c + i][j];
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int j = 0; j < S::NT; ++j)
+            *reinterpret_cast<f32x4*>(turn + (16 * i + m) * kPitch + 16 * j + 4 * g) = acc[kRows * cc + i][j];
     __builtin_amdgcn_wave_barrier();
-#pragma unroll 2
-    for (int r = 0; r < 16 * kRows; r += 64 / kLanes) {
-      const float* t = turn + (r + lane / kLanes) * kPitch + wcol;
-      float v[8], u[8];
+    with_ending<Mode>(p, [&](auto act, auto save) __attribute__((always_inline)) {
+#pragma unroll 1
+      for (int k = 0; k < kSteps; k += kGroup) {
+        const int64_t row = wrow + 16 * kRows * c + k * kStepRows;
+        if (add) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q) {
-        const f32x4 x = *reinterpret_cast<const f32x4*>(t + 4 * q);
-        const f32x4 y = *reinterpret_cast<const f32x4*>(t + 4 * q + (Mode == kGated ? 8 * S::NT : 0));
+          for (int q = 0; q < kGroup; ++q) res[q] = ahead[q];
+          fetch(ahead, row + kGroup * kStepRows);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          v[4 * q + e] = x[e];
-          u[4 * q + e] = y[e];
+        for (int q = 0; q < kGroup; ++q) {
+          const float* t = turn + ((k + q) * kStepRows + lane / kLanes) * kPitch + wcol;
+          float v[8], u[8], r[8];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(t + 4 * h);
+            const f32x4 y = *reinterpret_cast<const f32x4*>(t + 4 * h + (Mode == kGated ? 8 * S::NT : 0));
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              v[4 * h + f] = x[f];
+              u[4 * h + f] = y[f];
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < 8; ++f)
+            r[f] = add ? T::load((uint16_t)(res[q][f >> 1] >> (16 * (f & 1)))) : 0.f;
+          finish<T, Mode, decltype(act)::value, decltype(save)::value, 8>(p, which, row + q * kStepRows, col, v, u,
+                                                                          bias, r);
         }
       }
-      epilogue<T, Mode, 8>(p, which, wrow + 16 * kRows * c + r, col0 + kWide * wn + wcol, v, u);
-    }
+    });
     __builtin_amdgcn_wave_barrier();
   }
 }
