@@ -225,6 +225,45 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
   // has to have returned (at most the reads of stage s + 1 outstanding).
   constexpr int kLgkm = kReads < 15 ? kReads : 15;
 
+  // Each wave turns its sums around in LDS (its own part, so only the first
+  // use waits for the block), 16 * kRows rows at a time, so that a lane ends
+  // eight columns of a row at once: 16-byte accesses to every matrix, whole
+  // lines per row, and the activation's code is there once per turn instead
+  // of once per MFMA tile (32 copies cost the 256 x 256 kernel a fifth of
+  // its time in instruction fetches).
+  constexpr int kPitch = 16 * S::NT + 4;
+  constexpr int kRows = S::NW * 64 * kPitch * 4 <= kStages * S::STAGE ? 4 : 2;
+  static_assert(S::NW * 16 * kRows * kPitch * 4 <= kStages * S::STAGE && S::MT % kRows == 0, "LDS");
+  constexpr int kWide = Mode == kGated ? 8 * S::NT : 16 * S::NT;  // output columns of a wave
+  constexpr int kLanes = kWide / 8;                               // lanes of a row
+  constexpr int kStepRows = 64 / kLanes;                          // rows of a wave at once
+  constexpr int kSteps = 16 * kRows / kStepRows, kGroup = kSteps < 4 ? kSteps : 4;
+  float* turn = reinterpret_cast<float*>(smem) + wave * 16 * kRows * kPitch;
+  const int64_t wrow = row0 + 16 * S::MT * wm + lane / kLanes;
+  const int wcol = 8 * (lane % kLanes), col = col0 + kWide * wn + wcol;
+  float bias[8] = {};
+  if (Mode == kLinear && p.bias != nullptr && col < p.n)
+    load_cols<T, 8>(static_cast<const typename T::raw*>(p.bias) + col, bias, p.n - col);
+  // The residual's loads are a group of steps ahead of their use: read where
+  // it is used, each of them would cost the wave a trip to HBM (17 us of a
+  // 2048 x 3584 -> 7168 product).
+  const bool add = Mode == kLinear && p.residual != nullptr;
+  u32x4 res[kGroup], ahead[kGroup];
+  auto fetch = [&](u32x4(&d)[kGroup], int64_t row) __attribute__((always_inline)) {
+#pragma unroll
+    for (int q = 0; q < kGroup; ++q) {
+      d[q] = u32x4{0, 0, 0, 0};
+      const int64_t r = row + q * kStepRows;
+      const uint16_t* src = static_cast<const uint16_t*>(p.residual) + r * p.ldr + col;
+      if (r < p.m && col + 8 <= p.n) {
+        d[q] = reinterpret_cast<const Any16*>(src)->v;
+      } else if (r < p.m) {
+#pragma unroll
+        for (int t = 0; t < 7; ++t)
+          if (col + t < p.n) d[q][t >> 1] |= (uint32_t)src[t] << (16 * (t & 1));
+      }
+    }
+  };
   const int count = s1 - s0;
   if (count > 0) {
 #pragma unroll 1
@@ -304,7 +343,12 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
         whole_stages();
       }
     }
+    // the residual's first loads go out with the last stages still to do (they
+    // only make the counted waits stricter)
+    if (add && splits == 1) fetch(ahead, wrow);
     other_stages(count);
+  } else if (add && splits == 1) {
+    fetch(ahead, wrow);
   }
 
   // lane (g, m) of tile (i, j) holds row 16 i + m, columns 16 j + 4 g .. + 3
@@ -327,46 +371,6 @@ void gemm_tile_kernel(GemmArgs p, int mtiles, int ntiles, int splits, float* par
     }
     return;
   }
-  // Each wave turns its sums around in LDS (its own part, so only the first
-  // use waits for the block), 16 * kRows rows at a time, so that a lane ends
-  // eight columns of a row at once: 16-byte accesses to every matrix, whole
-  // lines per row, and the activation's code is there once per turn instead
-  // of once per MFMA tile (32 copies cost the 256 x 256 kernel a fifth of
-  // its time in instruction fetches).
-  constexpr int kPitch = 16 * S::NT + 4;
-  constexpr int kRows = S::NW * 64 * kPitch * 4 <= kStages * S::STAGE ? 4 : 2;
-  static_assert(S::NW * 16 * kRows * kPitch * 4 <= kStages * S::STAGE && S::MT % kRows == 0, "LDS");
-  constexpr int kWide = Mode == kGated ? 8 * S::NT : 16 * S::NT;  // output columns of a wave
-  constexpr int kLanes = kWide / 8;                               // lanes of a row
-  constexpr int kStepRows = 64 / kLanes;                          // rows of a wave at once
-  constexpr int kSteps = 16 * kRows / kStepRows, kGroup = kSteps < 4 ? kSteps : 4;
-  float* turn = reinterpret_cast<float*>(smem) + wave * 16 * kRows * kPitch;
-  const int64_t wrow = row0 + 16 * S::MT * wm + lane / kLanes;
-  const int wcol = 8 * (lane % kLanes), col = col0 + kWide * wn + wcol;
-  float bias[8] = {};
-  if (Mode == kLinear && p.bias != nullptr && col < p.n)
-    load_cols<T, 8>(static_cast<const typename T::raw*>(p.bias) + col, bias, p.n - col);
-  // The residual's loads are a group of steps ahead of their use: read where
-  // it is used, each of them would cost the wave a trip to HBM (17 us of a
-  // 2048 x 3584 -> 7168 product).
-  const bool add = Mode == kLinear && p.residual != nullptr;
-  u32x4 res[kGroup], ahead[kGroup];
-  auto fetch = [&](u32x4(&d)[kGroup], int64_t row) __attribute__((always_inline)) {
-#pragma unroll
-    for (int q = 0; q < kGroup; ++q) {
-      d[q] = u32x4{0, 0, 0, 0};
-      const int64_t r = row + q * kStepRows;
-      const uint16_t* src = static_cast<const uint16_t*>(p.residual) + r * p.ldr + col;
-      if (r < p.m && col + 8 <= p.n) {
-        d[q] = reinterpret_cast<const Any16*>(src)->v;
-      } else if (r < p.m) {
-#pragma unroll
-        for (int t = 0; t < 7; ++t)
-          if (col + t < p.n) d[q][t >> 1] |= (uint32_t)src[t] << (16 * (t & 1));
-      }
-    }
-  };
-  if (add) fetch(ahead, wrow);
   __syncthreads();
 #pragma unroll 1
   for (int c = 0; c < S::MT / kRows; ++c) {
