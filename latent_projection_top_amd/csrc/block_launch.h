@@ -46,7 +46,7 @@ struct Workspace {
   float* partial;
   size_t partial_bytes;
 };
-constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 128) * 64;
+constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 64) * 64;
 constexpr int kMaxSplits = 64;
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);

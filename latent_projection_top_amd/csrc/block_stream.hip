@@ -2,30 +2,34 @@
 // of rows, so the time is the weights' way from HBM, and the kernel is built
 // around keeping many of their bytes in flight.
 //
-// A wave takes 128 columns by 32 of the reduction at a time, straight into
-// registers (8 loads of 16 bytes per lane, the next step's under way while
-// this one is multiplied), and multiplies on the matrix cores with the rows
-// padded to 16. The eight waves of a block take its steps in turn and their
-// sums meet in LDS. With few column tiles the reduction is also split over
-// blocks: their FP32 sums go through the workspace and are added in split
-// order, by the last block of a tile to arrive where they are few (Join), by
-// a second kernel where they are many.
+// A wave takes 8 KB of weights at a time, straight into registers (8 loads of
+// 16 bytes per lane, the next step's under way while this one is multiplied),
+// and multiplies on the matrix cores with the rows padded to 16. The eight
+// waves of a block take its steps in turn and their sums meet in LDS. With
+// few column tiles the reduction is also split over blocks: their FP32 sums
+// go through the workspace and are added in split order, by the last block of
+// a tile to arrive where they are few (Join), by a second kernel where they
+// are many.
 //
-// Weights with contiguous columns ([K][N], forward): lane (g, m) loads rows
-// 8 g .. 8 g + 7 of columns 8 m .. 8 m + 7 (256-byte segments) and transposes
-// the 8 x 8 block with v_perm_b32: fragment c holds columns 8 m + c.
-// Weights with a contiguous reduction (backward, W^T): lane (g, m) loads
-// 8 values of columns 8 m + c, c = 0..7, which are the fragments as they are.
+// Weights with contiguous columns ([K][N], forward): a step is 128 columns by
+// 32 of the reduction. Lane (g, m) loads rows 8 g .. 8 g + 7 of columns 8 m ..
+// 8 m + 7 (256-byte segments) and transposes the 8 x 8 block with v_perm_b32:
+// fragment c holds columns 8 m + c.
+// Weights with a contiguous reduction (backward, W^T): a step is 64 columns by
+// 64 of the reduction. Lane (g, m) loads values 16 g .. 16 g + 15 of columns
+// 4 m + c, c = 0..3 (whole 128-byte lines; with half the reduction and twice
+// the columns, 64-byte segments, one row of 7168 -> 7168 took 25.1 us instead of
+// 23.3), which are two fragments as they are: the order of a reduction is
+// free as long as both operands have it.
 #include "block_device.h"
 
 #include <algorithm>
 
 namespace block {
 
-constexpr int kCols = 128;   // columns of a tile
-constexpr int kRed = 32;     // reduction of a step
 constexpr int kWaves = 8;
-constexpr int kPart = kCols + 4;  // floats of a row of partial sums in LDS
+constexpr int stream_cols(int mode) { return mode == kDx ? 64 : 128; }  // of a step and tile
+constexpr int stream_red(int mode) { return mode == kDx ? 64 : 32; }    // of a step
 
 // `v` moved down by d elements of 16 bits, zeros from above (d >= 8: all).
 __device__ __forceinline__ u32x4 drop_low(u32x4 v, int d) {
@@ -57,7 +61,11 @@ __device__ __forceinline__ void get2(const float* p, float& a, float& b) {
 template <typename T, int Mode, int RT, bool Join>
 __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, int splits, float* partial,
                                                                   uint32_t* counters) {
-  constexpr bool kTurn = Mode != kDx;                  // weights need the transpose
+  constexpr bool kTurn = Mode != kDx;  // weights need the transpose
+  constexpr int kCols = stream_cols(Mode), kRed = stream_red(Mode);
+  constexpr int kMine = kCols / 16;        // columns of a lane, kMine m + c
+  constexpr int kHalves = kRed / 32;       // MFMAs deep
+  constexpr int kPart = kCols + 4;         // floats of a row of partial sums
   constexpr int kTeam = Mode == kGated ? kWaves / 2 : kWaves;  // waves of one matrix
   __shared__ __attribute__((aligned(16))) float part[kWaves][16 * RT][kPart];
 
@@ -74,7 +82,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
 
   struct Step {
     u32x4 w[8];
-    u32x4 x[RT];
+    u32x4 x[RT][kHalves];
   };
   // Everything a lane loads is inside the matrices: columns past the end
   // repeat the last eight (or the last one), the reduction past the end is
@@ -83,7 +91,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
     const int s = s0 + i * kTeam;
     const int seg = s >= per_seg ? 1 : 0;
     const int k0 = (s - seg * per_seg) * kRed;
-    const int k = k0 + 8 * g;
+    const int k = k0 + 8 * kHalves * g;
     const uint16_t* w = static_cast<const uint16_t*>(p.b[Mode == kGated ? wave / kTeam : seg]);
     if constexpr (kTurn) {
       const int col = min(col0 + 8 * m, p.n - 8);
@@ -91,45 +99,55 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
       for (int r = 0; r < 8; ++r) d.w[r] = load16(w + (int64_t)min(k + r, red - 1) * p.ldb + col);
     } else {
 #pragma unroll
-      for (int c = 0; c < 8; ++c)
-        d.w[c] = load16(w + (int64_t)min(col0 + 8 * m + c, p.n - 1) * p.ldb + min(k, red - 8));
-    }
-    const uint16_t* x = static_cast<const uint16_t*>(p.a[seg]) + min(k, red - 8);
+      for (int c = 0; c < kMine; ++c)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) d.x[r] = load16(x + min((int64_t)(16 * r + m), p.m - 1) * p.lda);
+        for (int h = 0; h < kHalves; ++h)
+          d.w[c * kHalves + h] =
+              load16(w + (int64_t)min(col0 + kMine * m + c, p.n - 1) * p.ldb + min(k + 8 * h, red - 8));
+    }
+    const uint16_t* x = static_cast<const uint16_t*>(p.a[seg]);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int h = 0; h < kHalves; ++h)
+        d.x[r][h] = load16(x + min((int64_t)(16 * r + m), p.m - 1) * p.lda + min(k + 8 * h, red - 8));
   };
 
-  f32x4 acc[8][RT] = {};
+  f32x4 acc[kMine][RT] = {};
   auto multiply = [&](Step& d, int i) {
     const int s = s0 + i * kTeam;
     const int ks = s >= per_seg ? s - per_seg : s;
     if (ks == per_seg - 1) {  // the reduction may end inside: zeros from there
-      const int k = ks * kRed + 8 * g;
-      const int over = min(max(k - (red - 8), 0), 8);
+      const int k = ks * kRed + 8 * kHalves * g;
 #pragma unroll
-      for (int r = 0; r < RT; ++r) d.x[r] = drop_low(d.x[r], over);
+      for (int h = 0; h < kHalves; ++h) {
+        const int over = min(max(k + 8 * h - (red - 8), 0), 8);
 #pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        if constexpr (kTurn)
-          d.w[r] = k + r < red ? d.w[r] : u32x4{0, 0, 0, 0};
-        else
-          d.w[r] = drop_low(d.w[r], over);
+        for (int r = 0; r < RT; ++r) d.x[r][h] = drop_low(d.x[r][h], over);
+        if constexpr (!kTurn)
+#pragma unroll
+          for (int c = 0; c < kMine; ++c) d.w[c * kHalves + h] = drop_low(d.w[c * kHalves + h], over);
       }
+      if constexpr (kTurn)
+#pragma unroll
+        for (int r = 0; r < 8; ++r) d.w[r] = k + r < red ? d.w[r] : u32x4{0, 0, 0, 0};
     }
 #pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      u32x4 f;
-      if constexpr (kTurn) {
-        constexpr uint32_t kLow = 0x05040100, kHigh = 0x07060302;
+    for (int c = 0; c < kMine; ++c)
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-          f[q] = __builtin_amdgcn_perm(d.w[2 * q + 1][c >> 1], d.w[2 * q][c >> 1], (c & 1) ? kHigh : kLow);
-      } else {
-        f = d.w[c];
+      for (int h = 0; h < kHalves; ++h) {
+        u32x4 f;
+        if constexpr (kTurn) {
+          constexpr uint32_t kLow = 0x05040100, kHigh = 0x07060302;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            f[q] = __builtin_amdgcn_perm(d.w[2 * q + 1][c >> 1], d.w[2 * q][c >> 1], (c & 1) ? kHigh : kLow);
+        } else {
+          f = d.w[c * kHalves + h];
+        }
+#pragma unroll
+        for (int r = 0; r < RT; ++r) acc[c][r] = T::mfma(f, d.x[r][h], acc[c][r]);
       }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) acc[c][r] = T::mfma(f, d.x[r], acc[c][r]);
-    }
   };
 
   if (count > 0) {
@@ -155,20 +173,21 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
     }
   }
 
-  // lane (g, m) holds row 16 r + m; acc[c][r][t] is column 8 (4 g + t) + c
+  // lane (g, m) holds row 16 r + m; acc[c][r][t] is column kMine (4 g + t) + c
   const int64_t pn = (p.n + 3) & ~3;
 #pragma unroll
   for (int r = 0; r < RT; ++r) {
-    float* d = &part[wave][16 * r + m][32 * g];
+    float* d = &part[wave][16 * r + m][4 * kMine * g];
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      *reinterpret_cast<f32x4*>(d + 8 * t) = f32x4{acc[0][r][t], acc[1][r][t], acc[2][r][t], acc[3][r][t]};
-      *reinterpret_cast<f32x4*>(d + 8 * t + 4) = f32x4{acc[4][r][t], acc[5][r][t], acc[6][r][t], acc[7][r][t]};
-    }
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int c = 0; c < kMine; c += 4)
+        *reinterpret_cast<f32x4*>(d + kMine * t + c) =
+            f32x4{acc[c][r][t], acc[c + 1][r][t], acc[c + 2][r][t], acc[c + 3][r][t]};
   }
   __syncthreads();
-  for (int id = threadIdx.x; id < (int)p.m * 16; id += 64 * kWaves) {
-    const int row = id >> 4, run = id & 15;
+  for (int id = threadIdx.x; id < (int)p.m * (kCols / 8); id += 64 * kWaves) {
+    const int row = id / (kCols / 8), run = id % (kCols / 8);
     const int col = col0 + 8 * run;
     if (col >= p.n) continue;
     float v[8] = {}, u[8] = {};
@@ -263,6 +282,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
 template <typename T, int Mode>
 static hipError_t launch_rows(const GemmArgs& p, int splits, bool join, float* partial, uint32_t* counters,
                               hipStream_t stream) {
+  constexpr int kCols = stream_cols(Mode);
   const dim3 grid((p.n + kCols - 1) / kCols, splits), block(64 * kWaves);
   const bool one = p.m <= 16;
   if (join)
@@ -290,9 +310,9 @@ struct StreamPlan {
 // At most a block per CU: a second round costs another start and end (16 rows
 // of 3584 x 7168: 4 splits, 224 blocks, 15.3 us; 5 splits, 280 blocks, 20.4;
 // 9 splits, 504 blocks, 17.2). Within that, the split whose modelled time is
-// least: the weights at 5.2 TB/s, or 0.12 us for each step of a block if that
-// is more; 0.6 us for each of a wave's steps in turn; 3.3 us for a join by the
-// last block, or 5.3 for one by a second kernel and the sums twice at 4 TB/s
+// least: the weights at 5.2 TB/s, or 0.12 us (backward 0.2) for each step of a
+// block if that is more; 0.6 us (1.0) for each of a wave's steps in turn; 3.0 us and 0.07 a
+// split for a join by the last block, or 5.3 for one by a second kernel and the sums twice at 4 TB/s
 // (1000 x 776, 1 row: 6.6 us unsplit, 5.6 with 8 splits; 512 x 512: 4.0
 // unsplit, 4.8 with 8).
 // The last block joins up to 8 rows of sums (8 rows of 2048 x 7168, 4 splits:
@@ -300,19 +320,21 @@ struct StreamPlan {
 // 12.3); beyond, its one CU takes longer than a second kernel on all of them
 // (16 rows of 3584 x 7168, 4 splits: 16.3 against 15.3).
 static StreamPlan plan_stream(Mode mode, const GemmArgs& p, size_t partial_bytes) {
-  const int64_t tiles = (p.n + kCols - 1) / kCols;
-  const int64_t steps = (p.red + kRed - 1) / kRed * p.segments;
+  const int cols = stream_cols(mode), red = stream_red(mode);
+  const int64_t tiles = (p.n + cols - 1) / cols;
+  const int64_t steps = (p.red + red - 1) / red * p.segments;
   const int planes = mode == kGated ? 2 : 1, team = kWaves / planes;
   const double plane = (double)p.m * ((p.n + 3) & ~3) * 4 * planes;
-  const double bytes = (double)tiles * steps * planes * (kCols * kRed * 2);
+  const double bytes = (double)tiles * steps * planes * (cols * red * 2);
   const bool join = p.m * planes <= 8;
+  const double per_step = mode == kDx ? 0.2 : 0.12, per_turn = mode == kDx ? 1.0 : 0.6;
   StreamPlan best{1, false};
   double best_t = 0;
   for (int s = 1; s <= kMaxSplits; ++s) {
     if (s > 1 && (plane * s > (double)partial_bytes || tiles * s > 256 || s > steps)) break;
     const int64_t block_steps = (steps + s - 1) / s;
-    const double t = std::max(bytes / 5.2e6, 0.12 * (double)(block_steps * planes)) +
-                     0.6 * (double)((block_steps + team - 1) / team) + (s == 1 ? 0.0 : join ? 3.3 : 5.3 + 2.0 * s * plane / 4e6);
+    const double t = std::max(bytes / 5.2e6, per_step * (double)(block_steps * planes)) +
+                     per_turn * (double)((block_steps + team - 1) / team) + (s == 1 ? 0.0 : join ? 3.0 + 0.07 * s : 5.3 + 2.0 * s * plane / 4e6);
     if (s == 1 || t <= best_t) {
       best = StreamPlan{s, join && s > 1};
       best_t = t;

@@ -461,17 +461,19 @@ hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TileP
 }
 
 // Tile shape and K split of a product: the ones whose modelled time is least.
-// Stage times in us, measured at K = 3584 with one block on few CUs and with
-// all CUs busy (they share HBM and power): 256 x 256 0.63 / 0.87, 128 x 256
-// 0.42 / 0.58, 128 x 128 0.35 / 0.39 and 0.65 where two share a CU; each round
-// of blocks starts and ends in about 2 us; a split costs 5 us and its sums
-// twice at 4.2 TB/s. So large tiles where they fill the CUs (4096 x 3584 ->
-// 4096: 98 us against 129 and 150), small ones for few rows (128 rows, 3584 ->
-// 4096, 8 splits: 17.9 us; 256 x 256, 12 splits: 23.7).
+// Stage times in us, measured at K = 3584 with few CUs busy and with all (they
+// share HBM and power): 256 x 256 0.55 / 0.81, 128 x 256 0.37 / 0.57, 128 x
+// 128 0.25 / 0.31 and 0.64 where two share a CU; each round of blocks starts
+// and ends in about 2 us; a split costs 5 us and its sums twice at 4.2 TB/s.
+// So large tiles where they fill the CUs (4096 x 3584 -> 4096: 97 us against
+// 126 and 144), small ones for few rows (128 rows, 3584 -> 4096, 8 splits:
+// 19.4 us; 256 x 256, 12 splits: 24.1), splits where even those are too few
+// (2048 rows, 7168 -> 3584: 115 us in 2 splits of 256 x 256, 129 in one of
+// 128 x 256).
 TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   struct Cost { int bm, bn; double few, full; } const shapes[3] = {
-      {256, 256, 0.63, 0.87}, {128, 256, 0.42, 0.58}, {128, 128, 0.35, 0.39}};
-  const double pair = 0.65;
+      {256, 256, 0.55, 0.81}, {128, 256, 0.37, 0.57}, {128, 128, 0.25, 0.31}};
+  const double pair = 0.64;
   const double steps = (double)((p.red + kStep - 1) / kStep) * p.segments;
   const int planes = mode == kGated ? 2 : p.outputs;
   TilePlan best{2, 1};
