@@ -71,6 +71,8 @@ __device__ __forceinline__ void load_params(const void* p, int i, int dtype, flo
   }
 }
 
+struct __attribute__((packed, aligned(4))) AnyF4 { f32x4 v; };
+
 // ----------------------------------------------------------------- reduction --
 
 template <int Ctrl>
@@ -298,13 +300,41 @@ __global__ __launch_bounds__(Lanes < 256 ? 256 : Lanes) void norm_backward_kerne
     }
   }
   if (p.dweight == nullptr && p.dbias == nullptr) return;
-  // the block's sums: groups joined in LDS in group order, then out
+  // the block's sums: groups joined in LDS in group order, then out; those of
+  // a block alone are the result
+  const bool alone = gridDim.x == 1;
+  auto result = [&](int k, int c, float v) {
+    void* dst = k == 0 ? p.dweight : p.dbias;
+    if (dst != nullptr) store_param(dst, c, p.param_dtype, v);
+  };
   const int64_t wp = (p.width + 3) & ~3;
   float* out = p.partial + (int64_t)blockIdx.x * 2 * wp;
   if constexpr (kRows == 1) {
 #pragma unroll
     for (int i = 0; i < P; ++i) {
       float* o = out + col.start[i];
+      if (alone && E >= 4 && col.skip[i] == 0 && p.param_dtype == BLOCK_F32) {
+#pragma unroll
+        for (int e = 0; e + 4 <= E; e += 4) {
+          const int c = col.start[i] + e;
+          if (p.dweight)
+            reinterpret_cast<AnyF4*>(static_cast<float*>(p.dweight) + c)->v =
+                f32x4{dw[i][e], dw[i][e + 1], dw[i][e + 2], dw[i][e + 3]};
+          if (p.dbias)
+            reinterpret_cast<AnyF4*>(static_cast<float*>(p.dbias) + c)->v =
+                f32x4{db[i][e], db[i][e + 1], db[i][e + 2], db[i][e + 3]};
+        }
+        continue;
+      }
+      if (alone) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+          if (e >= col.skip[i]) {
+            result(0, col.start[i] + e, dw[i][e]);
+            result(1, col.start[i] + e, db[i][e]);
+          }
+        continue;
+      }
       if (E >= 4 && col.skip[i] == 0) {
 #pragma unroll
         for (int e = 0; e + 4 <= E; e += 4) {
@@ -335,7 +365,10 @@ __global__ __launch_bounds__(Lanes < 256 ? 256 : Lanes) void norm_backward_kerne
         float s = 0.f;
 #pragma unroll
         for (int r = 0; r < kRows; ++r) s += join[r][c];
-        out[k * wp + c] = s;
+        if (alone)
+          result(k, c, s);
+        else
+          out[k * wp + c] = s;
       }
     }
   }
@@ -433,28 +466,32 @@ __global__ __launch_bounds__(1024) void norm_wide_dx_kernel(NormArgs p) {
   }
 }
 
-// Blocks of 64 columns, four row lanes each, joined in a fixed order.
+// Blocks of 64 columns, sixteen row lanes each, joined in a fixed order.
 template <typename T>
-__global__ __launch_bounds__(256) void norm_wide_dparam_kernel(NormArgs p) {
-  __shared__ float rw[256], rb[256];
-  const int col = blockIdx.x * 64 + (threadIdx.x & 63);
+__global__ __launch_bounds__(1024) void norm_wide_dparam_kernel(NormArgs p) {
+  __shared__ float part[2][16][64];
+  const int c = threadIdx.x & 63, lane = threadIdx.x >> 6;
+  const int col = blockIdx.x * 64 + c;
   float sw = 0.f, sb = 0.f;
   if (col < p.width) {
-    for (int64_t r = threadIdx.x >> 6; r < p.rows; r += 4) {
+#pragma unroll 4
+    for (int64_t r = lane; r < p.rows; r += 16) {
       const float dy = T::load(static_cast<const typename T::raw*>(p.dy)[r * p.lddy + col]);
       const float x = T::load(static_cast<const typename T::raw*>(p.x)[r * p.ldx + col]);
       sb += dy;
       sw += dy * ((x - p.mean[r]) * p.rstd[r]);
     }
   }
-  rw[threadIdx.x] = sw;
-  rb[threadIdx.x] = sb;
+  part[0][lane][c] = sw;
+  part[1][lane][c] = sb;
   __syncthreads();
-  const int t = threadIdx.x;
-  if (t < 64 && col < p.width) {
-    if (p.dweight) store_param(p.dweight, col, p.param_dtype, (rw[t] + rw[t + 64]) + (rw[t + 128] + rw[t + 192]));
-    if (p.dbias) store_param(p.dbias, col, p.param_dtype, (rb[t] + rb[t + 64]) + (rb[t + 128] + rb[t + 192]));
-  }
+  if (lane > 1 || col >= p.width) return;
+  void* dst = lane == 0 ? p.dweight : p.dbias;
+  if (dst == nullptr) return;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) s += part[lane][i][c];
+  store_param(dst, col, p.param_dtype, s);
 }
 
 // ------------------------------------------------------------------ launches --
@@ -475,15 +512,20 @@ static bool with_layout(int width, F f) {
   return false;
 }
 
+// (most: no more than that many pieces)
 template <typename T, typename F>
-static bool with_row_layout(int width, F f) {
+static bool with_row_layout(int width, int most, F f) {
   constexpr int kE = 16 / sizeof(typename T::raw);
   if (width < kE) {
     f(std::integral_constant<int, 16>{}, std::integral_constant<int, 1>{}, std::integral_constant<int, 1>{});
     return true;
   }
-  return with_layout<kE>(width, f);
+  return (width + kE - 1) / kE <= most && with_layout<kE>(width, f);
 }
+// Backward, rows of more than 2048 pieces keep twice as many sums per thread
+// as its registers hold (2048 x 20000: 378 us spilling, 144 by the wide
+// kernels).
+constexpr int kForwardPieces = 4096, kBackwardPieces = 2048;
 
 // Blocks that stay, at most `most` of them, each with whole groups of rows.
 static int64_t norm_blocks(int64_t rows, int lanes, int64_t most) {
@@ -505,13 +547,16 @@ static int64_t forward_blocks(int64_t rows, int lanes) {
 static int64_t backward_blocks(int64_t rows, int lanes, int width) {
   const int64_t most = 256 * 512 / (lanes < 256 ? 256 : lanes);
   const int64_t best = (int64_t)std::sqrt(375000.0 * (double)rows / (double)width) + 1;
-  return norm_blocks(rows, lanes, best < most ? best : most);
+  const int64_t blocks = norm_blocks(rows, lanes, best < most ? best : most);
+  // one block needs no join: for narrow rows up to four turns of it cost less
+  // than a launch (80 x 80, both passes: 19.5 us of eager calls against 23.8)
+  return lanes < 256 && norm_blocks(rows, lanes, 5) < 5 ? 1 : blocks;
 }
 
 template <typename T>
 static hipError_t norm_typed(const NormArgs& p, hipStream_t stream) {
   hipError_t e = hipSuccess;
-  const bool held = with_row_layout<T>(p.width, [&](auto lanes, auto pieces, auto el) {
+  const bool held = with_row_layout<T>(p.width, kForwardPieces, [&](auto lanes, auto pieces, auto el) {
     constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value, E = decltype(el)::value;
     e = launch_kernel(norm_kernel<T, L, P, E>, dim3((unsigned)forward_blocks(p.rows, L)),
                       dim3(L < 256 ? 256 : L), stream, p);
@@ -524,20 +569,21 @@ static hipError_t norm_backward_typed(const NormArgs& p, hipStream_t stream) {
   const bool params = p.dweight != nullptr || p.dbias != nullptr;
   hipError_t e = hipSuccess;
   int64_t blocks = 0;
-  const bool held = with_row_layout<T>(p.width, [&](auto lanes, auto pieces, auto el) {
+  const bool held = with_row_layout<T>(p.width, kBackwardPieces, [&](auto lanes, auto pieces, auto el) {
     constexpr int L = decltype(lanes)::value, P = decltype(pieces)::value, E = decltype(el)::value;
     blocks = backward_blocks(p.rows, L, p.width);
-    if (blocks > 0)
-      e = launch_kernel(norm_backward_kernel<T, L, P, E>, dim3((unsigned)blocks), dim3(L < 256 ? 256 : L), stream, p);
+    if constexpr (P <= 2)
+      if (blocks > 0)
+        e = launch_kernel(norm_backward_kernel<T, L, P, E>, dim3((unsigned)blocks), dim3(L < 256 ? 256 : L), stream, p);
   });
   if (e != hipSuccess) return e;
   if (held)
-    return params ? launch_kernel(norm_join_kernel, dim3((p.width + 31) / 32, 2), dim3(256), stream, p, (int)blocks)
+    return params && blocks != 1 ? launch_kernel(norm_join_kernel, dim3((p.width + 31) / 32, 2), dim3(256), stream, p, (int)blocks)
                   : hipSuccess;
   if (p.dx != nullptr && p.rows > 0)
     e = launch_kernel(norm_wide_dx_kernel<T>, dim3((unsigned)p.rows), dim3(1024), stream, p);
   if (e != hipSuccess || !params) return e;
-  return launch_kernel(norm_wide_dparam_kernel<T>, dim3((p.width + 63) / 64), dim3(256), stream, p);
+  return launch_kernel(norm_wide_dparam_kernel<T>, dim3((p.width + 63) / 64), dim3(1024), stream, p);
 }
 
 hipError_t launch_norm(int dtype, const NormArgs& p, hipStream_t stream) {
@@ -555,7 +601,7 @@ hipError_t launch_norm_backward(int dtype, const NormArgs& p, hipStream_t stream
 template <typename T>
 static size_t backward_bytes(int64_t rows, int width) {
   size_t bytes = 0;
-  with_row_layout<T>(width, [&](auto lanes, auto, auto) {
+  with_row_layout<T>(width, kBackwardPieces, [&](auto lanes, auto, auto) {
     bytes = (size_t)backward_blocks(rows, decltype(lanes)::value, width) * 2 * ((width + 3) & ~3) * 4;
   });
   return bytes;
