@@ -58,12 +58,16 @@ __device__ __forceinline__ void wait_barrier() {
 // An operand's tile of `Rows` rows (or columns) by 32 of the reduction, and
 // how it lies in a stage.
 //   RContig (the reduction is contiguous in memory): 64-byte rows; the
-//     16-byte piece c of row r sits at position c ^ ((r >> 2) & 3), so that
-//     the 16 rows that the lanes of one group read take 16 different bank
-//     groups. Read with ds_read_b128.
+//     16-byte piece c of row r sits at position c ^ swizzle(r >> 2). Read with
+//     ds_read_b128, which serves the lanes 0-3, 12-15, 20-27 at once, then
+//     4-11, 16-19, 28-31, and likewise the upper half: with the swizzle 0, 2,
+//     3, 1 each of these sixteen takes another 16-byte column of the 64 banks
+//     (with 0, 1, 2, 3 every read met a two-way conflict).
 //   otherwise (rows contiguous): blocks of [32 r][32 rows], 64-byte lines,
 //     whose two halves are swapped where bit 3 of r is set. The MFMA wants 8
 //     consecutive r of one row per lane, which ds_read_tr16_b64 delivers.
+__device__ __forceinline__ int swizzle(int r4) { return ((r4 ^ (r4 >> 1)) & 1) << 1 | ((r4 >> 1) & 1); }
+
 template <bool RContig>
 struct Operand {
   // this lane's source of load `c` (1 KB): row within the tile and r within
@@ -73,14 +77,14 @@ struct Operand {
     return 32 * (c >> 1) + 8 * ((lane & 3) ^ ((lane >> 5) << 1));
   }
   static __device__ __forceinline__ int red(int c, int lane) {
-    if constexpr (RContig) return 8 * ((lane & 3) ^ ((lane >> 4) & 3));
+    if constexpr (RContig) return 8 * ((lane & 3) ^ swizzle(lane >> 4));
     return 16 * (c & 1) + (lane >> 2);
   }
   // addresses of this lane's part of a 16-row fragment: rows 16 t, t even
   // (h = 0) or odd (h = 1), relative to the even tile
   static __device__ __forceinline__ uint32_t base(int lane, int h) {
     const int g = lane >> 4, m = lane & 15;
-    if constexpr (RContig) return (uint32_t)((16 * h + m) * 64 + ((g ^ ((m >> 2) & 3)) * 16));
+    if constexpr (RContig) return (uint32_t)((16 * h + m) * 64 + ((g ^ swizzle(m >> 2)) * 16));
     return (uint32_t)((8 * g + (m >> 2)) * 64 + (2 * (h ^ (g & 1)) + ((m & 3) >> 1)) * 16 + (m & 1) * 8);
   }
   static constexpr int kReads = RContig ? 1 : 2;  // LDS reads per fragment
