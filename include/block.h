@@ -37,8 +37,12 @@
  * the row stride given in elements beside its pointer (at least its width, at
  * most BLOCK_MAX_STRIDE). d_gate, d_up and slope are contiguous
  * [rows][inner | outputs]. Any size, stride and element-aligned pointer is
- * accepted; 16-byte aligned pointers with sizes and strides that are
- * multiples of 8 take faster kernels.
+ * accepted. Above 32 rows, 16-byte aligned pointers with sizes and strides
+ * that are multiples of 8 are fastest: other operands are copied first, into
+ * the workspace (which holds room for the rows, and for weights whose rows
+ * are no multiple of 8 long), and weights whose rows are a multiple of 8 long
+ * at an address that is no multiple of 16 take a kernel of a fifth of the
+ * rate.
  *
  * Ownership, threading, capture: as in route.h. The caller owns every buffer,
  * run calls only enqueue kernels on `stream` and can be captured into a HIP

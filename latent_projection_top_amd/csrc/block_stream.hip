@@ -21,6 +21,10 @@
 // the columns, 64-byte segments, one row of 7168 -> 7168 took 25.1 us instead of
 // 23.3), which are two fragments as they are: the order of a reduction is
 // free as long as both operands have it.
+//
+//   1 row of gated 7168 x 7168: 41 us (5.0 TB/s); 20 rows of gated 7168 x 2048:
+//   14 us and 4 for the join; 8 rows of 2048 x 7168: 8.4-10 us. Around the
+//   stream, a start of about 3 us and a join of 2 to 5.
 #include "block_device.h"
 
 #include <algorithm>
@@ -311,10 +315,10 @@ struct StreamPlan {
 // of 3584 x 7168: 4 splits, 224 blocks, 15.3 us; 5 splits, 280 blocks, 20.4;
 // 9 splits, 504 blocks, 17.2). Within that, the split whose modelled time is
 // least: the weights at 5.2 TB/s, or 0.12 us (backward 0.2) for each step of a
-// block if that is more; 0.6 us (1.0) for each of a wave's steps in turn; 3.0 us and 0.07 a
-// split for a join by the last block, or 5.3 for one by a second kernel and the sums twice at 4 TB/s
-// (1000 x 776, 1 row: 6.6 us unsplit, 5.6 with 8 splits; 512 x 512: 4.0
-// unsplit, 4.8 with 8).
+// block if that is more; 0.6 us (1.0) for each of a wave's steps in turn; 3.0
+// us and 0.07 a split for a join by the last block, or 5.3 for one by a second
+// kernel and the sums twice at 4 TB/s (1000 x 776, 1 row: 6.6 us unsplit, 5.6
+// with 8 splits; 512 x 512: 4.0 unsplit, 4.8 with 8).
 // The last block joins up to 8 rows of sums (8 rows of 2048 x 7168, 4 splits:
 // 10.7 us against 11.4; 1 row of gated 3584 x 2048, 16 splits: 10.4 against
 // 12.3); beyond, its one CU takes longer than a second kernel on all of them

@@ -1,5 +1,19 @@
 // Matrix products of the layer's operators: the tile kernel, for row counts
 // that make the matrix cores, not the weights' bandwidth, the bound.
+//
+// C[m][n] = sum over r of A(m, r) B(r, n) on v_mfma_f32_16x16x32, one FP32
+// accumulator per output from the first r to the last. A 256 x 256 tile has
+// eight waves of 128 x 64 outputs in 128 accumulator registers each: two
+// waves per SIMD, so that one's LDS reads and barrier run under the other's
+// MFMAs, and 12 operand reads for 32 MFMAs, so that LDS, written by the loads
+// and read by eight waves, is busy a third of the time. The reduction runs in
+// stages of 32 through five LDS buffers (160 KB): one being multiplied, one
+// being read into registers, three on their way from memory, which gives a
+// load about three stages (2 us) to arrive. One tile per CU at a time.
+//   4096 x 4096 x 4096: 103-112 us (1220-1330 TFLOP/s), matrix cores busy
+//   0.71-0.77 of the cycles at 1.9-2.1 GHz; 4096 x 3584 x 8192: 172-177 us
+//   (1360-1400). The rest is the barrier of every stage and the ends of a
+//   tile, which nothing overlaps.
 #include "block_device.h"
 
 #include <algorithm>
