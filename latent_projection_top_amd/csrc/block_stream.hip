@@ -239,7 +239,7 @@ __global__ __launch_bounds__(64 * kWaves) void gemm_stream_kernel(GemmArgs p, in
     // The tile's last block adds the splits' sums. Its counter goes back to
     // zero for the next call.
     __shared__ uint32_t arrived;
-    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0): this wave's sums are out
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
     __syncthreads();
     if (threadIdx.x == 0) {
       uint32_t* c = counters + 16 * tile;
