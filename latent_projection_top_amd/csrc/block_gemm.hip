@@ -247,13 +247,15 @@ __global__ __launch_bounds__(256) void scale_kernel(ScaleArgs p) {
 #pragma unroll
     for (int k = 0; k < Count; ++k) {
       const u32x4 s = load8(static_cast<const uint16_t*>(p.s[k]) + row * p.n + col, count);
-      u32x4 o = {0, 0, 0, 0};
+      float v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float v = d[i] * T::load((uint16_t)(s[i >> 1] >> (16 * (i & 1))));
-        o[i >> 1] |= (uint32_t)T::store(v) << (16 * (i & 1));
-        if (Sum) sum[i] += v;
+        v[i] = d[i] * T::load((uint16_t)(s[i >> 1] >> (16 * (i & 1))));
+        if (Sum) sum[i] += v[i];
       }
+      u32x4 o;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) o[i] = T::store2(v[2 * i], v[2 * i + 1]);
       // the row stride is a multiple of 8: the last piece pads with zeros
       if (p.out[k] != nullptr)
         *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out[k]) + row * p.ld + col) = o;

@@ -49,7 +49,7 @@ struct Piece {
       u32x4 w;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        w[i] = (uint32_t)T::store(f[2 * i]) | (uint32_t)T::store(f[2 * i + 1]) << 16;
+        w[i] = T::store2(f[2 * i], f[2 * i + 1]);
       reinterpret_cast<Any16*>(p)->v = w;
     }
   }
