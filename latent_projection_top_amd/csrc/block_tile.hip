@@ -482,7 +482,10 @@ hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TileP
 // Stage times in us, measured at K = 3584 with few CUs busy and with all (they
 // share HBM and power): 256 x 256 0.55 / 0.81, 128 x 256 0.37 / 0.57, 128 x
 // 128 0.25 / 0.31 and 0.64 where two share a CU; each round of blocks starts
-// and ends in about 2 us; a split costs 5 us and its sums twice at 4.2 TB/s.
+// and ends in about 2 us; a split costs 3.5 us and its sums twice at 4.2 TB/s,
+// against which forward tiles that end by themselves take 1 us more, with
+// GELU 4 (its instructions on few CUs). Over 106 shapes of 40-2048 rows the
+// choice is 1.1 % from the best of all shapes and splits (geometric mean).
 // So large tiles where they fill the CUs (4096 x 3584 -> 4096: 97 us against
 // 126 and 144), small ones for few rows (128 rows, 3584 -> 4096, 8 splits:
 // 19.4 us; 256 x 256, 12 splits: 24.1), splits where even those are too few
@@ -492,6 +495,9 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   struct Cost { int bm, bn; double few, full; } const shapes[3] = {
       {256, 256, 0.55, 0.81}, {128, 256, 0.37, 0.57}, {128, 128, 0.25, 0.31}};
   const double pair = 0.64;
+  const double ending = mode == kDx || mode == kDw                   ? 0.0
+                        : mode == kLinear && p.act == BLOCK_ACT_GELU ? 4.0
+                                                                     : 1.0;
   const double steps = (double)((p.red + kStep - 1) / kStep) * p.segments;
   const int planes = mode == kGated ? 2 : p.outputs;
   TilePlan best{2, 1};
@@ -508,7 +514,7 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
       const double busy = rounds > 0 ? 1.0 : std::min(1.0, (double)rest / 256.0);
       const double last = rest > 256 ? pair : c.few + (c.full - c.few) * busy;
       double t = (double)rounds * (steps / s * (k == 2 ? pair : c.full) + 2.0) + steps / s * last + 2.0;
-      if (s > 1) t += 5.0 + 2.0 * bytes / 4.2e6;
+      t += s > 1 ? 3.5 + 2.0 * bytes / 4.2e6 : ending;
       if (best_t == 0 || t < best_t) {
         best = TilePlan{k, s};
         best_t = t;
