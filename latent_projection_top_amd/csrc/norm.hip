@@ -10,8 +10,8 @@
 // Backward, each thread also keeps the FP32 sums of its columns' dweight and
 // dbias over the block's rows; a second kernel adds the blocks' sums in block
 // order.
-//   16384 x 7168 BF16: forward 95-102 us (4.6-4.9 TB/s), backward 140-147
-//   (4.8-5.0; a copy reaches 5.06); 1 x 7168: 2.8 us forward, 4.0 backward.
+//   16384 x 7168 BF16: forward 82-97 us (4.8-5.7 TB/s), backward 140-153
+//   (4.6-5.0; a copy reaches 5.06); 1 x 7168: 2.7 us forward, 4.0 backward.
 #include "block_device.h"
 
 #include <cmath>
