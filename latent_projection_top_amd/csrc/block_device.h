@@ -112,7 +112,8 @@ __device__ __forceinline__ ValueSlope activate(float z) {
     return {z < 0.f ? 0.f : z, z > 0.f ? 1.f : (z == z ? 0.f : z)};
   } else if constexpr (Act == BLOCK_ACT_SILU) {
     const float s = sigmoid(z);
-    return {z * s, s * (1.f + z * (1.f - s))};
+    const float zc = fminf(fmaxf(z, -100.f), 100.f);  // s or 1 - s is 0 beyond 89
+    return {z * s, s * (1.f + zc * (1.f - s))};
   } else if constexpr (Act == BLOCK_ACT_GELU) {
     const float x = fabsf(z), t = __builtin_amdgcn_rcpf(fmaf(0.3f, x, 1.f));
     float q = 0.0354313701f;
