@@ -103,7 +103,7 @@ typedef struct block_norm_plan block_norm_plan;
  * plan given to a training call (ROUTE_E_ARG), then the current device
  * (ROUTE_E_DEVICE). An argument error launches nothing. */
 int block_norm_prepare(const block_norm_config* cfg, block_norm_plan** out);
-size_t block_norm_workspace_bytes(const block_norm_plan* plan); /* for the backward call */
+size_t block_norm_workspace_bytes(const block_norm_plan* plan); /* for the backward call; at least 256 */
 /* weight and bias may each be NULL (1 and 0); mean and rstd (both or neither)
  * are kept for the backward call. */
 int block_norm(const block_norm_plan* plan, const void* x, int64_t x_stride, const void* weight,

@@ -97,7 +97,7 @@ class _Plan:
         self.handle = handle
         self.rows = cfg.rows
         self.device = cfg.device
-        self.workspace_bytes = max(int(getattr(LIB, f"block_{self.OP}_workspace_bytes")(handle)), 256)
+        self.workspace_bytes = int(getattr(LIB, f"block_{self.OP}_workspace_bytes")(handle))
 
     def new_workspace(self) -> torch.Tensor:
         """A zero-filled workspace tensor of the size this plan needs."""

@@ -115,7 +115,9 @@ int block_norm_prepare(const block_norm_config* cfg, block_norm_plan** out) {
   if (int st = find_device(cfg->device)) return st;
   block_norm_plan* p = new_plan<block_norm_plan>(*cfg);
   if (p == nullptr) return ROUTE_E_ARG;
-  p->ws_bytes = round256(block::norm_backward_bytes(cfg->dtype, cfg->rows, cfg->width));
+  // never 0: the backward call takes no NULL workspace, and an allocation of 0
+  // bytes is one
+  p->ws_bytes = std::max<size_t>(round256(block::norm_backward_bytes(cfg->dtype, cfg->rows, cfg->width)), 256);
   *out = p;
   return ROUTE_OK;
 }
