@@ -1,6 +1,8 @@
 // Matrix products of the layer's operators on the matrix cores.
 #include "block_device.h"
 
+#include <algorithm>
+
 namespace block {
 
 // Products that the tile kernel's 16-byte loads do not fit: weights whose
@@ -193,16 +195,16 @@ struct Copies {
 };
 
 __global__ __launch_bounds__(256) void copy_kernel(Copies p) {
-  int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (id >= p.end[2]) return;
-  const int k = id < p.end[0] ? 0 : id < p.end[1] ? 1 : 2;
-  const Copy& c = p.c[k];
-  if (k > 0) id -= p.end[k - 1];
-  const int64_t per_row = (c.len + 7) >> 3;
-  const int64_t row = id / per_row;
-  const int col = (int)(id - row * per_row) * 8;
-  const u32x4 v = load8(static_cast<const uint16_t*>(c.src) + row * c.ld + col, c.len - col);
-  *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(c.dst) + id * 8) = v;
+  for (int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x; at < p.end[2]; at += (int64_t)gridDim.x * 256) {
+    const int k = at < p.end[0] ? 0 : at < p.end[1] ? 1 : 2;
+    const Copy& c = p.c[k];
+    const int64_t id = k > 0 ? at - p.end[k - 1] : at;
+    const int64_t per_row = (c.len + 7) >> 3;
+    const int64_t row = id / per_row;
+    const int col = (int)(id - row * per_row) * 8;
+    const u32x4 v = load8(static_cast<const uint16_t*>(c.src) + row * c.ld + col, c.len - col);
+    *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(c.dst) + id * 8) = v;
+  }
 }
 
 hipError_t launch_copies(const Copy* copies, int count, hipStream_t stream) {
@@ -216,7 +218,10 @@ hipError_t launch_copies(const Copy* copies, int count, hipStream_t stream) {
     p.end[k] = end;
   }
   if (end == 0) return hipSuccess;
-  return launch_kernel(copy_kernel, dim3((unsigned)((end + 255) / 256)), dim3(256), stream, p);
+  // A launch has fewer than 2^32 threads, and 2^20 rows of 131072 values are
+  // 2^34 pieces: beyond 2^28 threads each takes several.
+  const int64_t blocks = std::min<int64_t>((end + 255) / 256, 1 << 20);
+  return launch_kernel(copy_kernel, dim3((unsigned)blocks), dim3(256), stream, p);
 }
 
 // The first half of a backward pass: out[k] = dy * s[k], rounded to the
