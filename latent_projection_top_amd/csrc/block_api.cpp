@@ -257,7 +257,6 @@ int block_gated(const block_gated_plan* plan, const void* x, int64_t x_stride, c
     copies.use(&a.b[0], &ld, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w : nullptr);
     copies.use(&a.b[1], &a.ldb, c.inputs, c.inner, plan->w_bytes ? ws + plan->off_w + plan->w_bytes : nullptr);
     if (int st = copies.launch(static_cast<hipStream_t>(stream))) return st;
-    a.padded = true;
   }
   return status_of(block::launch_gemm(c.dtype, block::kGated, a, products(plan, workspace),
                                       static_cast<hipStream_t>(stream)));
@@ -297,7 +296,6 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   if ((st = copies.launch(s)) != ROUTE_OK) return st;
   if (dx != nullptr && rows != 0) {
     GemmArgs a{};
-    a.padded = true;
     a.a[0] = dz[0];
     a.a[1] = dz[1];
     a.lda = padded(c.inner);
@@ -316,7 +314,6 @@ int block_gated_backward(const block_gated_plan* plan, const void* dh, int64_t d
   }
   if (dw_gate == nullptr) return ROUTE_OK;
   GemmArgs a{};
-  a.padded = true;
   a.a[0] = x;
   a.lda = x_stride;
   a.b[0] = dz[0];
@@ -399,7 +396,6 @@ int block_linear(const block_linear_plan* plan, const void* x, int64_t x_stride,
     copies.use(&a.a[0], &a.lda, rows, c.inputs, ws + plan->off_x);
     copies.use(&a.b[0], &a.ldb, c.inputs, c.outputs, plan->w_bytes ? ws + plan->off_w : nullptr);
     if (int st = copies.launch(static_cast<hipStream_t>(stream))) return st;
-    a.padded = true;
   }
   return status_of(block::launch_gemm(c.dtype, block::kLinear, a, products(plan, workspace),
                                       static_cast<hipStream_t>(stream)));
@@ -444,7 +440,6 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   if (int st = copies.launch(s)) return st;
   if (dx != nullptr && rows != 0) {
     GemmArgs a{};
-    a.padded = true;
     a.a[0] = dz;
     a.lda = ldz;
     a.b[0] = w;
@@ -460,7 +455,6 @@ int block_linear_backward(const block_linear_plan* plan, const void* dy, int64_t
   }
   if (dw == nullptr) return ROUTE_OK;
   GemmArgs a{};
-  a.padded = true;
   a.a[0] = x;
   a.lda = x_stride;
   a.b[0] = dz;

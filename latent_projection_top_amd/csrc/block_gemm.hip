@@ -5,12 +5,12 @@
 
 namespace block {
 
-// Products that the tile kernel's 16-byte loads do not fit: weights whose
-// rows are multiples of 8 long, for which no copy is kept, at an address that
-// is no multiple of 16. 64 x 64 output tiles, four waves of
-// 32 x 32 each, reduction steps of 32 staged element by element through LDS
-// with r contiguous; right for everything, at about a fifth of the tile
-// kernel's rate.
+// Forward products and dx whose weights the tile kernel's 16-byte loads do not
+// fit: rows a multiple of 8 long, for which no copy is kept, at an address
+// that is no multiple of 16. (Every other operand is aligned or copied, so dw
+// never comes here.) 64 x 64 output tiles, four waves of 32 x 32 each,
+// reduction steps of 32 staged element by element through LDS with r
+// contiguous, at about a fifth of the tile kernel's rate.
 constexpr int kTile = 64;
 constexpr int kStep = 32;
 constexpr int kPitch = kStep + 8;  // 16-byte aligned, spreads rows over banks
@@ -48,24 +48,23 @@ __device__ __forceinline__ void stage(uint16_t* lds, const uint16_t* src, int64_
 
 template <typename T, int Mode>
 __global__ __launch_bounds__(256) void gemm_narrow_kernel(GemmArgs p) {
-  constexpr bool kAContig = Mode != kDw, kBContig = Mode == kDx;
+  constexpr bool kBContig = Mode == kDx;
   constexpr int kB = Mode == kGated ? 2 : 1;
   __shared__ __attribute__((aligned(16))) uint16_t sa[kTile * kPitch];
   __shared__ __attribute__((aligned(16))) uint16_t sb[kB][kTile * kPitch];
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, g = lane >> 4, m = lane & 15;
   const int64_t row0 = (int64_t)blockIdx.y * kTile;
   const int col0 = blockIdx.x * kTile;
-  const int which = blockIdx.z;
   const int wr = 32 * (wave >> 1), wc = 32 * (wave & 1);
   f32x4 acc[kB][2][2] = {};
   for (int s = 0; s < p.segments; ++s) {
     const uint16_t* a = static_cast<const uint16_t*>(p.a[s]);
     for (int64_t r0 = 0; r0 < p.red; r0 += kStep) {
-      stage<kAContig>(sa, a, p.lda, row0, p.m, r0, p.red);
+      stage<true>(sa, a, p.lda, row0, p.m, r0, p.red);
 #pragma unroll
       for (int b = 0; b < kB; ++b)
-        stage<kBContig>(sb[b], static_cast<const uint16_t*>(p.b[Mode == kGated ? b : s + which]), p.ldb, col0,
-                        p.n, r0, p.red);
+        stage<kBContig>(sb[b], static_cast<const uint16_t*>(p.b[Mode == kGated ? b : s]), p.ldb, col0, p.n, r0,
+                        p.red);
       __syncthreads();
       u32x4 av[2];
 #pragma unroll
@@ -94,18 +93,17 @@ __global__ __launch_bounds__(256) void gemm_narrow_kernel(GemmArgs p) {
         v[t] = acc[0][i][j][t];
         u[t] = acc[kB - 1][i][j][t];
       }
-      epilogue<T, Mode, 4>(p, which, row0 + wr + 16 * i + m, col0 + wc + 16 * j + 4 * g, v, u);
+      epilogue<T, Mode, 4>(p, 0, row0 + wr + 16 * i + m, col0 + wc + 16 * j + 4 * g, v, u);
     }
 }
 
 template <typename T>
 static hipError_t launch_narrow(Mode mode, const GemmArgs& p, hipStream_t stream) {
-  const dim3 grid((p.n + kTile - 1) / kTile, (unsigned)((p.m + kTile - 1) / kTile), mode == kDw ? p.outputs : 1);
+  const dim3 grid((p.n + kTile - 1) / kTile, (unsigned)((p.m + kTile - 1) / kTile));
   switch (mode) {
     case kLinear: return launch_kernel(gemm_narrow_kernel<T, kLinear>, grid, dim3(256), stream, p);
     case kGated: return launch_kernel(gemm_narrow_kernel<T, kGated>, grid, dim3(256), stream, p);
-    case kDx: return launch_kernel(gemm_narrow_kernel<T, kDx>, grid, dim3(256), stream, p);
-    default: return launch_kernel(gemm_narrow_kernel<T, kDw>, grid, dim3(256), stream, p);
+    default: return launch_kernel(gemm_narrow_kernel<T, kDx>, grid, dim3(256), stream, p);
   }
 }
 
@@ -156,16 +154,13 @@ hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& p, int splits,
                              : join_typed<F16>(mode, p, splits, partial, stream);
 }
 
-// Whether the tile kernel can read every operand.
-static int64_t lengths(Mode mode, const GemmArgs& p) {
-  return (mode == kDw ? p.m : p.red) | (mode == kDx ? p.red : p.n);
-}
-
-static bool tileable(Mode mode, const GemmArgs& p) {
+// Whether the tile kernel can read every operand (contiguous lengths that are
+// no multiple of 8 come as padded copies).
+static bool tileable(const GemmArgs& p) {
   uintptr_t bits = 0;
   for (int i = 0; i < 2; ++i)
     bits |= reinterpret_cast<uintptr_t>(p.a[i]) | reinterpret_cast<uintptr_t>(p.b[i]);
-  return (bits & 15) == 0 && ((p.lda | p.ldb) & 7) == 0 && (p.padded || (lengths(mode, p) & 7) == 0);
+  return (bits & 15) == 0 && ((p.lda | p.ldb) & 7) == 0;
 }
 
 bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red) {
@@ -182,7 +177,7 @@ size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, const Workspace& ws, hipStream_t stream) {
   if (gemm_streams(mode, p.m, p.n, p.red))
     return launch_gemm_stream(dtype, mode, p, ws, stream);
-  if (tileable(mode, p))
+  if (tileable(p))
     return launch_gemm_tile(dtype, mode, p, plan_tiles(mode, p, ws.partial_bytes), ws.partial, stream);
   return dtype == BLOCK_BF16 ? launch_narrow<BF16>(mode, p, stream) : launch_narrow<F16>(mode, p, stream);
 }

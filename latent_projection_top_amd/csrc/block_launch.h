@@ -36,7 +36,6 @@ struct GemmArgs {
   int segments;
   int outputs;
   int act;
-  bool padded;  // contiguous lengths are zero-padded to multiples of 8 in memory
 };
 
 // What a product uses of its operator's workspace: a counter per column tile,
@@ -50,8 +49,10 @@ constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 64) * 64;
 constexpr int kMaxSplits = 64;
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
-// Whether launch_gemm takes the operands as they are (few rows): the other
-// products want them copied where needs_copy says so.
+// Whether launch_gemm takes the operands as they are (few rows). The other
+// products want them copied where needs_copy says so, but for weights at an
+// unaligned address whose rows are a multiple of 8 long: contiguous lengths
+// are, or are zero-padded to, multiples of 8 in memory.
 bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red);
 // The area that products of up to m rows can use for split sums.
 size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs);
