@@ -46,14 +46,16 @@
  *
  * Ownership, threading, capture: as in route.h. The caller owns every buffer,
  * run calls only enqueue kernels on `stream` and can be captured into a HIP
- * graph. The workspace (block_*_workspace_bytes, 256-byte aligned) is
- * zero-filled once before its first use and must not be modified between
- * calls; calls that overlap in time use different workspaces. A call passes
- * 0..(plan rows) rows: with 0 rows the forward calls do nothing, the backward
- * calls write zero weight gradients, and row matrices may be NULL. Results do
- * not depend on timing: every sum has a fixed order for a given plan, row
- * count and alignment. An output may share memory with no other argument,
- * except that y of block_linear may be the residual (same pointer and stride).
+ * graph. The first BLOCK_WORKSPACE_ZEROED bytes of a gated or linear plan's
+ * workspace (block_*_workspace_bytes, 256-byte aligned) are zero-filled once
+ * before its first use and must not be modified between calls; the rest, and
+ * the norm's, may hold anything. Calls that overlap in time use different
+ * workspaces. A call passes 0..(plan rows) rows: with 0 rows the forward calls
+ * do nothing, the backward calls write zero weight gradients, and row matrices
+ * may be NULL. Results do not depend on timing: every sum has a fixed order for
+ * a given plan, row count and alignment. An output may share memory with no
+ * other argument, except that y of block_linear may be the residual (same
+ * pointer and stride).
  */
 #ifndef BLOCK_H
 #define BLOCK_H
@@ -68,6 +70,7 @@ extern "C" {
 #define BLOCK_MAX_ROWS 1048576   /* 2^20 */
 #define BLOCK_MAX_SIZE 131072    /* width, inputs, inner, outputs */
 #define BLOCK_MAX_STRIDE 1048576 /* elements */
+#define BLOCK_WORKSPACE_ZEROED 131072 /* bytes */
 
 typedef enum { BLOCK_BF16 = 0, BLOCK_F16 = 1, BLOCK_F32 = 2 } block_dtype;
 typedef enum {

@@ -60,10 +60,10 @@ int check_current(int32_t device) {
 // The most any of an operator's products can use for split sums: its forward
 // product and, for training, dx [rows][k] and dw `outputs` x [k][n].
 size_t partial_area(block::Mode mode, int64_t rows, int k, int n, int outputs, bool training) {
-  size_t b = block::gemm_partial_bytes(mode, rows, n, 1);
+  size_t b = block::gemm_partial_bytes(mode, rows, n, k, 1, 1);
   if (training) {
-    b = std::max(b, block::gemm_partial_bytes(block::kDx, rows, k, 1));
-    b = std::max(b, block::gemm_partial_bytes(block::kDw, k, n, outputs));
+    b = std::max(b, block::gemm_partial_bytes(block::kDx, rows, k, n, outputs, 1));
+    b = std::max(b, block::gemm_partial_bytes(block::kDw, k, n, rows, 1, outputs));
   }
   return round256(b);
 }

@@ -167,11 +167,22 @@ bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red) {
   return mode != kDw && m <= kStreamRows && red >= 8 && n >= 8;
 }
 
-size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs) {
-  const size_t plane = (size_t)m * ((n + 3) & ~3) * 4 * (mode == kGated ? 2 : outputs);
-  // only products of few tiles are split
-  const size_t most = (size_t)64 << 20;
-  return plane * kMaxSplits < most ? plane * kMaxSplits : most;
+// 64 MB at most: sums that large cost more on their way out and back than a
+// split gains.
+size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int64_t red, int segments, int outputs) {
+  const size_t row = (size_t)((n + 3) & ~3) * 4 * (mode == kGated ? 2 : outputs), most = (size_t)64 << 20;
+  size_t bytes = 0;
+  if (gemm_streams(mode, 1, n, red)) {
+    const size_t splits = most_stream_splits(mode, n, red, segments);
+    if (splits > 1) bytes = splits * (size_t)std::min<int64_t>(m, kStreamRows) * row;
+  }
+  if (!gemm_streams(mode, m, n, red)) {  // the tile kernel too
+    const size_t splits = most_tile_splits(red, segments), plane = (size_t)m * row;
+    // dw is of this size in every call; the others may be of any up to it
+    const size_t tile = mode == kDw ? std::min(splits, most / plane) * plane : std::min(splits * plane, most);
+    if (splits > 1 && (mode != kDw || tile > plane)) bytes = std::max(bytes, tile);
+  }
+  return bytes;
 }
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& p, const Workspace& ws, hipStream_t stream) {

@@ -46,7 +46,7 @@ struct Workspace {
   size_t partial_bytes;
 };
 constexpr size_t kCounterBytes = (size_t)(BLOCK_MAX_SIZE / 64) * 64;
-constexpr int kMaxSplits = 64;
+static_assert(kCounterBytes == BLOCK_WORKSPACE_ZEROED, "what the caller clears");
 
 hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
 // Whether launch_gemm takes the operands as they are (few rows). The other
@@ -54,8 +54,9 @@ hipError_t launch_gemm(int dtype, Mode mode, const GemmArgs& args, const Workspa
 // unaligned address whose rows are a multiple of 8 long: contiguous lengths
 // are, or are zero-padded to, multiples of 8 in memory.
 bool gemm_streams(Mode mode, int64_t m, int64_t n, int64_t red);
-// The area that products of up to m rows can use for split sums.
-size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int outputs);
+// The most that products of up to m rows (dw: of m rows, and a reduction of up
+// to `red`) can use for split sums.
+size_t gemm_partial_bytes(Mode mode, int64_t m, int n, int64_t red, int segments, int outputs);
 
 // Tile kernel: every operand 16-byte aligned, with row strides that are
 // multiples of 8 and contiguous lengths that are, or are zero-padded to,
@@ -65,6 +66,7 @@ struct TilePlan {
   int splits;
 };
 TilePlan plan_tiles(Mode mode, const GemmArgs& args, size_t partial_bytes);
+int most_tile_splits(int64_t red, int segments);
 hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& args, const TilePlan& plan, float* partial,
                             hipStream_t stream);
 
@@ -88,6 +90,7 @@ hipError_t launch_gemm_join(int dtype, Mode mode, const GemmArgs& args, int spli
 
 // At most kStreamRows rows; not kDw.
 constexpr int kStreamRows = 32;
+int most_stream_splits(Mode mode, int n, int64_t red, int segments);
 hipError_t launch_gemm_stream(int dtype, Mode mode, const GemmArgs& args, const Workspace& ws, hipStream_t stream);
 
 // out[k] [rows][ld] = dy * s[k] for `count` (0..2) matrices of derivatives

@@ -311,6 +311,14 @@ struct StreamPlan {
   bool join;  // by the last block of each tile
 };
 
+constexpr int kMaxSplits = 64;
+
+int most_stream_splits(Mode mode, int n, int64_t red, int segments) {
+  const int64_t tiles = (n + stream_cols(mode) - 1) / stream_cols(mode);
+  const int64_t steps = (red + stream_red(mode) - 1) / stream_red(mode) * segments;
+  return (int)std::max<int64_t>(1, std::min({(int64_t)kMaxSplits, steps, 256 / tiles}));
+}
+
 // At most a block per CU: a second round costs another start and end (16 rows
 // of 3584 x 7168: 4 splits, 224 blocks, 15.3 us; 5 splits, 280 blocks, 20.4;
 // 9 splits, 504 blocks, 17.2). Within that, the split whose modelled time is
@@ -326,6 +334,7 @@ struct StreamPlan {
 static StreamPlan plan_stream(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   const int cols = stream_cols(mode), red = stream_red(mode);
   const int64_t tiles = (p.n + cols - 1) / cols;
+  const int most = most_stream_splits(mode, p.n, p.red, p.segments);
   const int64_t steps = (p.red + red - 1) / red * p.segments;
   const int planes = mode == kGated ? 2 : 1, team = kWaves / planes;
   const double plane = (double)p.m * ((p.n + 3) & ~3) * 4 * planes;
@@ -334,8 +343,8 @@ static StreamPlan plan_stream(Mode mode, const GemmArgs& p, size_t partial_bytes
   const double per_step = mode == kDx ? 0.2 : 0.12, per_turn = mode == kDx ? 1.0 : 0.6;
   StreamPlan best{1, false};
   double best_t = 0;
-  for (int s = 1; s <= kMaxSplits; ++s) {
-    if (s > 1 && (plane * s > (double)partial_bytes || tiles * s > 256 || s > steps)) break;
+  for (int s = 1; s <= most; ++s) {
+    if (s > 1 && plane * s > (double)partial_bytes) break;
     const int64_t block_steps = (steps + s - 1) / s;
     const double t = std::max(bytes / 5.2e6, per_step * (double)(block_steps * planes)) +
                      per_turn * (double)((block_steps + team - 1) / team) + (s == 1 ? 0.0 : join ? 3.0 + 0.07 * s : 5.3 + 2.0 * s * plane / 4e6);

@@ -480,6 +480,11 @@ hipError_t launch_gemm_tile(int dtype, Mode mode, const GemmArgs& p, const TileP
                              : launch_typed<F16>(mode, p, t, partial, stream);
 }
 
+int most_tile_splits(int64_t red, int segments) {
+  // four stages each at least
+  return (int)std::max<int64_t>(1, std::min<int64_t>(16, (red + kStep - 1) / kStep * segments / 4));
+}
+
 // Tile shape and K split of a product: the ones whose modelled time is least.
 // Stage times in us, measured at K = 3584 with few CUs busy and with all (they
 // share HBM and power): 256 x 256 0.55 / 0.81, 128 x 256 0.37 / 0.57, 128 x
@@ -501,16 +506,16 @@ TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
                         : mode == kLinear && p.act == BLOCK_ACT_GELU ? 4.0
                                                                      : 1.0;
   const double steps = (double)((p.red + kStep - 1) / kStep) * p.segments;
-  const int planes = mode == kGated ? 2 : p.outputs;
+  const int planes = mode == kGated ? 2 : p.outputs, most = most_tile_splits(p.red, p.segments);
   TilePlan best{2, 1};
   double best_t = 0;
   for (int k = 0; k < 3; ++k) {
     const Cost& c = shapes[k];
     const int bn = mode == kGated ? c.bn / 2 : c.bn;
     const int64_t tiles = (int64_t)((p.m + c.bm - 1) / c.bm) * ((p.n + bn - 1) / bn) * p.outputs;
-    for (int s = 1; s <= 16; ++s) {
+    for (int s = 1; s <= most; ++s) {
       const double bytes = 4.0 * p.m * ((p.n + 3) & ~3) * planes * s;
-      if (s > 1 && (bytes > (double)partial_bytes || steps / s < 4)) break;
+      if (s > 1 && bytes > (double)partial_bytes) break;
       const int64_t blocks = tiles * s, slots = k == 2 ? 512 : 256;
       const int64_t rounds = (blocks - 1) / slots, rest = blocks - rounds * slots;
       const double busy = rounds > 0 ? 1.0 : std::min(1.0, (double)rest / 256.0);
