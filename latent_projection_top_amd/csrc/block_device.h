@@ -93,10 +93,13 @@ __device__ __forceinline__ float sigmoid(float z) { return __builtin_amdgcn_rcpf
 
 // GELU is z Phi(z), Phi the normal distribution's, and its slope Phi(z) +
 // z exp(-z^2 / 2) / sqrt(2 pi). One exponential serves both: Phi(-|z|) =
-// exp(-z^2 / 2) t Q(t), t = 1 / (1 + 0.3 |z|), where Q of degree 7 is the
+// exp(-z^2 / 2) t Q(t), t = 1 / (1 + 0.3 |z|), where Q of degree 7 is a
 // minimax fit (linear programme in the Chebyshev basis) of the relative error
-// over 0 <= |z| <= 14.5: 1.25e-7, and 2e-7 absolute evaluated in FP32. The
-// negative tail keeps its relative precision, which (1 + erf) / 2 does not.
+// over 0 <= |z| <= 14.5; with the coefficients as they stand that error is
+// 2.3e-7. Evaluated in FP32 the tail is off by 2.1e-7 absolute, and relative by
+// 6e-7 up to |z| = 2, 2.2e-6 up to 6 and 8e-6 up to 13: the rounding of the
+// exponential's argument, which grows with z^2. (1 + erf) / 2 would lose the
+// negative tail altogether from -5.5 on.
 // The ending of a tile whose CU has no other is bound by these instructions
 // (200 rows of 1000 x 776 in whole tiles, with the slope kept: 25.1 us by the
 // library's erff and one conversion per stored value, 19.6 like this).
