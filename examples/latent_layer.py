@@ -6,7 +6,9 @@ decode_round   a decode round of 1..20 rows: layer norm of the hidden rows, the
                back to the hidden width onto the residual stream.
 TrainStep      a training step of the layer's dense branch (a shared expert on
                the hidden rows): norm, gated, linear with residual, and the
-               whole backward pass, every gradient from the library's kernels.
+               whole backward pass, every gradient from the library's kernels;
+               dx gets the residual branch's share, dy itself, by one addition
+               of torch's after them.
 
 Weights and inputs are random; run it on an MI355X with
     python examples/latent_layer.py
