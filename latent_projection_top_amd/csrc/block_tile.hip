@@ -490,14 +490,16 @@ int most_tile_splits(int64_t red, int segments) {
 // share HBM and power): 256 x 256 0.55 / 0.81, 128 x 256 0.37 / 0.57, 128 x
 // 128 0.25 / 0.31 and 0.64 where two share a CU; each round of blocks starts
 // and ends in about 2 us; a split costs 3.5 us and its sums twice at 4.2 TB/s,
-// against which forward tiles that end by themselves take 1 us more, with
-// GELU 4 (its instructions on few CUs). Over 106 shapes of 40-2048 rows the
-// choice is 1.1 % from the best of all shapes and splits (geometric mean).
-// So large tiles where they fill the CUs (4096 x 3584 -> 4096: 97 us against
-// 126 and 144), small ones for few rows (128 rows, 3584 -> 4096, 8 splits:
-// 19.4 us; 256 x 256, 12 splits: 24.1), splits where even those are too few
-// (2048 rows, 7168 -> 3584: 115 us in 2 splits of 256 x 256, 129 in one of
-// 128 x 256).
+// against which forward tiles that end by themselves take 1 us more, the linear
+// product's with GELU 4 (its instructions on few CUs); the gated product's GELU
+// and the derivatives kept for training are not in the model. Over 106 shapes
+// of 40-2048 rows, forward, dx and dw, the choice takes 1.3 % longer than the
+// best of all shapes and splits (geometric mean; worst 25 %, 160 rows of gated
+// 3584 x 7168: 57 us, 46 in 4 splits of 256 x 256). So large tiles where they
+// fill the CUs (4096 x 3584 -> 4096: 99 us against 131 and 152), small ones for
+// few rows (128 rows, 3584 -> 4096, 8 splits: 17.8 us; 256 x 256, 12 splits:
+// 23.5), splits where even those are too few (2048 rows, 7168 -> 3584: 115 us
+// in 2 splits of 256 x 256, 121 in one of 128 x 256).
 TilePlan plan_tiles(Mode mode, const GemmArgs& p, size_t partial_bytes) {
   struct Cost { int bm, bn; double few, full; } const shapes[3] = {
       {256, 256, 0.55, 0.81}, {128, 256, 0.37, 0.57}, {128, 128, 0.25, 0.31}};

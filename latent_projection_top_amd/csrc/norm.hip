@@ -11,7 +11,7 @@
 // dbias over the block's rows; a second kernel adds the blocks' sums in block
 // order.
 //   16384 x 7168 BF16: forward 82-97 us (4.8-5.7 TB/s), backward 140-153
-//   (4.6-5.0; a copy reaches 5.06); 1 x 7168: 2.7 us forward, 4.0 backward.
+//   (4.6-5.0; a copy reaches 5.06-5.14); 1 x 7168: 2.7 us forward, 4.0 backward.
 #include "block_device.h"
 
 #include <cmath>
@@ -531,7 +531,7 @@ static bool with_row_layout(int width, int most, F f) {
   return (width + kE - 1) / kE <= most && with_layout<kE>(width, f);
 }
 // Backward, rows of more than 2048 pieces keep twice as many sums per thread
-// as its registers hold (2048 x 20000: 378 us spilling, 144 by the wide
+// as its registers hold (2048 x 20000: 374 us spilling, 120 by the wide
 // kernels).
 constexpr int kForwardPieces = 4096, kBackwardPieces = 2048;
 
