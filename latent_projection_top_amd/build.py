@@ -20,8 +20,10 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
 SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hip", "prefill_gemm.hip",
-           "block_api.cpp", "norm.hip", "block_gemm.hip", "block_tile.hip", "block_stream.hip"]
-HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h"]
+           "block_api.cpp", "norm.hip", "block_gemm.hip", "block_tile.hip", "block_stream.hip",
+           "experts_api.cpp", "experts_sort.hip", "experts_rows.hip", "experts_quantise.hip",
+           "experts_product.hip"]
+HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h", "experts_launch.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
