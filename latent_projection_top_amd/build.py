@@ -22,8 +22,9 @@ ARCH = "gfx950"
 SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hip", "prefill_gemm.hip",
            "block_api.cpp", "norm.hip", "block_gemm.hip", "block_tile.hip", "block_stream.hip",
            "experts_api.cpp", "experts_sort.hip", "experts_rows.hip", "experts_quantise.hip",
-           "experts_product.hip"]
-HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h", "experts_launch.h"]
+           "experts_stream.hip", "experts_tile.hip"]
+HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h", "lds_device.h",
+           "experts_launch.h", "experts_device.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",
@@ -41,7 +42,8 @@ COMMON_FLAGS = [
 # (same bits).
 EXTRA_FLAGS = {"prefill_gemm.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form",
                                     "-mllvm", "-amdgpu-sched-strategy=iterative-ilp"],
-               "block_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
+               "block_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"],
+               "experts_tile.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form"]}
 
 
 def _compile(src: str) -> str:

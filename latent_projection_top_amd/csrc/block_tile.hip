@@ -14,13 +14,11 @@
 //   0.71-0.77 of the cycles at 1.9-2.1 GHz; 4096 x 3584 x 8192: 172-177 us
 //   (1360-1400). The rest is the barrier of every stage and the ends of a
 //   tile, which nothing overlaps.
-#include "block_device.h"
+#include "lds_device.h"
 
 #include <algorithm>
 
 namespace block {
-
-typedef __attribute__((address_space(3))) void lds_void;
 
 constexpr int kStep = 32;    // reduction per stage: one MFMA deep
 constexpr int kStages = 5;   // LDS buffers
@@ -41,32 +39,9 @@ struct TileShape {
 // 16 bytes that lanes outside the reduction's range load.
 __device__ __attribute__((aligned(16))) const uint32_t kZeros[4] = {0, 0, 0, 0};
 
-// Global -> LDS, 16 bytes per lane: lane l's bytes land at lds + 16 l. Inline
-// assembly, so that the compiler does not wait for every load in flight
-// before each LDS read (it cannot tell the stages apart); the kernel's own
-// vmcnt waits order them, and the volatile barriers below keep the LDS reads
-// on their side.
-__device__ __forceinline__ void dma16(const char* base, uint32_t off, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, %1" : : "v"(off), "s"(base), "{m0}"(lds));
-}
-__device__ __forceinline__ void dma16(const char* addr, uint32_t lds) {
-  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(addr), "{m0}"(lds));
-}
-
-__device__ __forceinline__ u32x4 lds_b128(uint32_t addr) {
-  return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)addr;
-}
 __device__ __forceinline__ u32x2 lds_tr16(uint32_t addr) {
   return __builtin_bit_cast(
       u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(uintptr_t)addr));
-}
-
-// Wait until at most Vm of this wave's loads are in flight and at most Lgkm
-// LDS reads are outstanding, then meet the block.
-template <int Vm, int Lgkm>
-__device__ __forceinline__ void wait_barrier() {
-  static_assert(Vm >= 0 && Vm < 64 && Lgkm >= 0 && Lgkm < 16, "counter range");
-  asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(%1)\n\ts_barrier" : : "n"(Vm), "n"(Lgkm) : "memory");
 }
 
 // An operand's tile of `Rows` rows (or columns) by 32 of the reduction, and
@@ -80,8 +55,6 @@ __device__ __forceinline__ void wait_barrier() {
 //   otherwise (rows contiguous): blocks of [32 r][32 rows], 64-byte lines,
 //     whose two halves are swapped where bit 3 of r is set. The MFMA wants 8
 //     consecutive r of one row per lane, which ds_read_tr16_b64 delivers.
-__device__ __forceinline__ int swizzle(int r4) { return ((r4 ^ (r4 >> 1)) & 1) << 1 | ((r4 >> 1) & 1); }
-
 template <bool RContig>
 struct Operand {
   // this lane's source of load `c` (1 KB): row within the tile and r within

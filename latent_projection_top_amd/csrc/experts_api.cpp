@@ -22,11 +22,11 @@ struct experts_combine_plan {
 
 namespace {
 
-// Workspace of the 8-bit products: the zeroed part, the list of items with its
-// count in front, the rows as integers and their scales.
+// Workspace of the 8-bit products: the zeroed part (counters), split sums, the
+// lists of items, the rows as integers and their scales.
 struct Product8 {
   int32_t device, rows, tokens, inputs, outputs, experts, dtype, activation;
-  size_t off_items, off_q, off_step, ws_bytes, packed_bytes;
+  size_t off_lists, off_q, off_step, ws_bytes, packed_bytes;
 };
 
 bool misaligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) != 0; }
@@ -62,8 +62,8 @@ int prepare_product(Product8* p, int planes) {
   if (bad(p->rows, EXPERTS_MAX_CHOICES) || bad(p->tokens, EXPERTS_MAX_CHOICES)) return ROUTE_E_ROWS;
   if (int st = find_device(p->device)) return st;
   const size_t stride = (size_t)experts::red_blocks(p->inputs) * experts::kBlockRed;
-  p->off_items = EXPERTS_WORKSPACE_ZEROED;
-  p->off_q = p->off_items + round256(sizeof(experts::Item) * (1 + experts::most_items(p->rows, p->experts)));
+  p->off_lists = EXPERTS_WORKSPACE_ZEROED + experts::kPartialBytes;
+  p->off_q = p->off_lists + round256(experts::list_bytes(p->rows, p->experts));
   p->off_step = p->off_q + round256((size_t)p->tokens * stride);
   p->ws_bytes = p->off_step + round256((size_t)p->tokens * sizeof(float));
   p->packed_bytes = (size_t)p->experts * planes * experts::column_tiles(p->outputs) *
@@ -92,7 +92,6 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   if (rows == 0) return ROUTE_OK;
   hipStream_t s = static_cast<hipStream_t>(stream);
   char* ws = static_cast<char*>(workspace);
-  experts::Item* items = reinterpret_cast<experts::Item*>(ws + c.off_items);
   experts::ProductArgs a{};
   a.q = reinterpret_cast<int8_t*>(ws + c.off_q);
   a.step = reinterpret_cast<float*>(ws + c.off_step);
@@ -105,20 +104,25 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.y = y;
   a.ldy = y_stride;
   a.token = token;
-  a.items = offsets != nullptr ? items + 1 : nullptr;
-  a.count = &items->expert;
+  if (offsets != nullptr) a.lists = experts::lists_at(ws + c.off_lists, rows, c.experts);
+  a.counters = reinterpret_cast<uint32_t*>(ws);
+  a.partial = reinterpret_cast<int32_t*>(ws + EXPERTS_WORKSPACE_ZEROED);
   a.tokens = tokens;
   a.rows = rows;
   a.n = c.outputs;
   a.blocks = experts::red_blocks(c.inputs);
   a.act = c.activation;
   a.gated = planes == 2;
-  const int st = status_of(experts::launch_quantise(c.dtype, x, x_stride, tokens, c.inputs,
-                                                    reinterpret_cast<int8_t*>(ws + c.off_q),
-                                                    reinterpret_cast<float*>(ws + c.off_step), offsets, c.experts,
-                                                    rows, items + 1, &items->expert, s));
-  if (st != ROUTE_OK) return st;
-  return status_of(experts::launch_product(c.dtype, a, c.experts, s));
+  int st = status_of(experts::launch_quantise(c.dtype, x, x_stride, tokens, c.inputs,
+                                              reinterpret_cast<int8_t*>(ws + c.off_q),
+                                              reinterpret_cast<float*>(ws + c.off_step), offsets, c.experts, rows,
+                                              ws + c.off_lists, s));
+  // which experts have few rows is known on the device only: both kernels go
+  // through their lists
+  if (st == ROUTE_OK && (offsets != nullptr || rows <= experts::kStreamRows))
+    st = status_of(experts::launch_stream(c.dtype, a, c.experts, s));
+  if (st == ROUTE_OK && rows > experts::kStreamRows) st = status_of(experts::launch_tiles(c.dtype, a, c.experts, s));
+  return st;
 }
 
 int run_quantize(const Product8& c, const void* w, int8_t* w8, float* scale, void* stream) {

@@ -1,0 +1,90 @@
+// Device-side building blocks of the 8-bit products (gfx950, wave64).
+#pragma once
+
+#include "block_device.h"
+#include "experts_launch.h"
+
+namespace experts {
+
+using block::BF16;
+using block::F16;
+using block::kWave;
+using block::u32x4;
+
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
+
+// Lane (g, m) = (l / 16, l % 16) of the result holds column m of `b` (a row of
+// x) and rows 4 g .. 4 g + 3 of `a` (columns of the weights).
+__device__ __forceinline__ i32x4 mfma(u32x4 a, u32x4 b, i32x4 c) {
+  return __builtin_amdgcn_mfma_i32_16x16x64_i8(__builtin_bit_cast(i32x4, a), __builtin_bit_cast(i32x4, b), c, 0, 0,
+                                              0);
+}
+
+template <bool Gated>
+__device__ __forceinline__ int packed_tiles(const ProductArgs& p) {
+  return (Gated ? 2 : 1) * ((p.n + 15) / 16);
+}
+
+__device__ __forceinline__ const uint8_t* packed_tile(const ProductArgs& p, int expert, int tiles, int tile) {
+  return static_cast<const uint8_t*>(p.packed) + ((int64_t)expert * tiles + tile) * p.blocks * kBlockBytes;
+}
+
+// The row of x that row `row` of y is made of.
+__device__ __forceinline__ int token_of(const ProductArgs& p, int row) {
+  return p.token != nullptr ? min(max(p.token[row], 0), p.tokens - 1) : row;
+}
+
+// C (4 or 8) consecutive columns of an expert's FP32 vector, `count` of them
+// inside it.
+template <int C>
+__device__ __forceinline__ void load_scales(const float* s, float (&v)[C], int count) {
+#pragma unroll
+  for (int t = 0; t < C; ++t) v[t] = t < count ? s[t] : 0.f;
+}
+
+// What the columns of an output need: scales and the bias.
+template <typename T, bool Gated, int C>
+struct Columns {
+  float scale[C], other[C];  // other: the up product's scale, or the bias
+  __device__ __forceinline__ Columns(const ProductArgs& p, int expert, int col) {
+    const int count = p.n - col;
+    const int64_t at = (int64_t)expert * p.n + col;
+    load_scales<C>(p.scale[0] + at, scale, count);
+    if constexpr (Gated) {
+      load_scales<C>(p.scale[1] + at, other, count);
+    } else {
+#pragma unroll
+      for (int t = 0; t < C; ++t) other[t] = 0.f;
+      if (p.bias != nullptr && count > 0)
+        block::load_cols<T, C>(static_cast<const typename T::raw*>(p.bias) + at, other, count);
+    }
+  }
+};
+
+// The end of a product: integer sums (for the gated product of both) of columns
+// col .. col + C - 1 of row `row`. The channel's scale comes first: the row's
+// may be as small or as large as FP32 goes.
+template <typename T, bool Gated, int Act, int C>
+__device__ __forceinline__ void finish(const ProductArgs& p, const Columns<T, Gated, C>& k, int row, int col,
+                                       float step, const float (&sum)[C], const float (&up)[C],
+                                       const float (&residual)[C]) {
+  float v[C];
+#pragma unroll
+  for (int t = 0; t < C; ++t) {
+    const float z = sum[t] * k.scale[t] * step;
+    if constexpr (Gated)
+      v[t] = block::activate<Act>(z).a * (up[t] * k.other[t] * step);
+    else
+      v[t] = block::activate<Act>(z + k.other[t]).a + residual[t];
+  }
+  block::store_cols<T, C>(static_cast<typename T::raw*>(p.y) + row * p.ldy + col, v, p.n - col);
+}
+
+template <bool Gated, typename F>
+__device__ __forceinline__ void with_ending(const ProductArgs& p, F f) {
+  block::with_activation(p.act, [&](auto act) __attribute__((always_inline)) {
+    if constexpr (!Gated || decltype(act)::value != BLOCK_ACT_NONE) f(act);
+  });
+}
+
+}  // namespace experts

@@ -57,14 +57,37 @@ constexpr int kBlockRed = 64, kBlockBytes = 1024;
 inline int red_blocks(int k) { return (k + kBlockRed - 1) / kBlockRed; }
 inline int column_tiles(int n) { return (n + 15) / 16; }
 
-// Up to kItemRows rows of one expert.
+// The rows of one expert in a product: up to kStreamRows of them (a short item,
+// for the kernel that streams weights), or its first-th and later row tiles (an
+// entry for each tile; `rows` is of all of them).
 struct Item {
-  int32_t expert, row, rows, unused;
+  int32_t expert, row, rows, first;
 };
-constexpr int kItemRows = 64;
-inline int64_t most_items(int64_t rows, int experts) {
-  return rows / kItemRows + (rows < experts ? rows : experts);
+constexpr int kStreamRows = 32, kTileRows = 256;
+struct Lists {
+  const int32_t* counts;  // short items, row tiles; NULL: one expert has every row
+  const Item* brief;
+  const Item* tiles;
+};
+inline int64_t most_brief(int64_t rows, int experts) { return rows < experts ? rows : experts; }
+inline int64_t most_tiles(int64_t rows, int experts) {
+  const int64_t long_ones = rows / (kStreamRows + 1);
+  return rows / kTileRows + (long_ones < experts ? long_ones : experts);
 }
+inline size_t list_bytes(int64_t rows, int experts) {
+  return sizeof(Item) * (size_t)(1 + most_brief(rows, experts) + most_tiles(rows, experts));
+}
+inline Lists lists_at(void* area, int64_t rows, int experts) {
+  const Item* items = static_cast<const Item*>(area);
+  return Lists{&items->expert, items + 1, items + 1 + most_brief(rows, experts)};
+}
+
+// What the streaming kernel uses of the workspace: counters of its column
+// groups, zero between calls, 64 bytes apart, and split sums, a unit of them
+// for each block.
+constexpr int kSplitUnits = 256, kUnitInts = kStreamRows * 64;
+static_assert(kSplitUnits * 64 <= EXPERTS_WORKSPACE_ZEROED, "what the caller clears");
+constexpr size_t kPartialBytes = (size_t)kSplitUnits * kUnitInts * 4;
 
 struct ProductArgs {
   const int8_t* q;          // rows of x as integers, stride 64 * blocks, zeros past the end
@@ -75,16 +98,18 @@ struct ProductArgs {
   const void* residual;
   void* y;
   const int32_t* token;     // NULL: the row itself
-  const Item* items;        // NULL: one expert, items of kItemRows rows in turn
-  const int32_t* count;     // of items
+  Lists lists;
+  uint32_t* counters;
+  int32_t* partial;
   int64_t ldr, ldy;
   int tokens, rows, n, blocks, act, gated;
 };
-// Also makes the list of items where there are offsets.
+// Also makes the lists (area: list_bytes) where there are offsets.
 hipError_t launch_quantise(int dtype, const void* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                           const int32_t* offsets, int experts, int rows, Item* items, int32_t* count,
-                           hipStream_t stream);
-hipError_t launch_product(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
+                           const int32_t* offsets, int experts, int rows, void* area, hipStream_t stream);
+// Experts of 1..kStreamRows rows, and those of more.
+hipError_t launch_stream(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
+hipError_t launch_tiles(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,
                        hipStream_t stream);

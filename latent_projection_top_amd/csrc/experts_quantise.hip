@@ -44,42 +44,58 @@ __device__ __forceinline__ float wider(float m, float x) {
   return v > m || v != v ? v : m;
 }
 
-// A block per row; the block after the last row makes the list of items.
+// The lists of short items and row tiles, by one block. An expert of more than
+// kStreamRows rows has as few tiles of at most kTileRows as it can, of equal
+// height.
+__device__ void make_lists(const int32_t* offsets, int experts, int rows, Item* area, int most_brief,
+                           int most_tiles) {
+  __shared__ uint2 part[kThreads / kWave];
+  const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
+  Item* brief = area + 1;
+  Item* tiles = brief + most_brief;
+  int briefs = 0, tile = 0;  // so far
+  for (int e0 = 0; e0 < experts; e0 += kThreads) {
+    const int e = e0 + t;
+    int first = 0, n = 0;
+    if (e < experts) {
+      first = min(max(offsets[e], 0), rows);
+      n = max(min(max(offsets[e + 1], 0), rows) - first, 0);
+    }
+    const int b = n > 0 && n <= kStreamRows ? 1 : 0;
+    const int m = n > kStreamRows ? (n + kTileRows - 1) / kTileRows : 0;
+    int rb = b, rm = m;
+    for (int d = 1; d < kWave; d *= 2) {
+      const int vb = __shfl_up(rb, d), vm = __shfl_up(rm, d);
+      rb += lane >= d ? vb : 0;
+      rm += lane >= d ? vm : 0;
+    }
+    if (lane == kWave - 1) part[wave] = uint2{(uint32_t)rb, (uint32_t)rm};
+    __syncthreads();
+    int ab = briefs + rb - b, am = tile + rm - m;
+    for (int w = 0; w < kThreads / kWave; ++w) {
+      ab += w < wave ? (int)part[w].x : 0;
+      am += w < wave ? (int)part[w].y : 0;
+      briefs += (int)part[w].x;
+      tile += (int)part[w].y;
+    }
+    // offsets that overlap would make more than there is room for
+    if (b != 0 && ab < most_brief) brief[ab] = Item{e, first, n, 0};
+    for (int i = 0; i < m && am + i < most_tiles; ++i) tiles[am + i] = Item{e, first, n, am};
+    __syncthreads();
+  }
+  if (t == 0) *area = Item{min(briefs, most_brief), min(tile, most_tiles), 0, 0};
+}
+
+// A block per row; the block after the last row makes the lists.
 template <typename T>
 __global__ __launch_bounds__(kThreads) void quantise_kernel(const uint16_t* x, int64_t ldx, int tokens, int k,
                                                             int stride, int8_t* q, float* step,
-                                                            const int32_t* offsets, int experts, int rows,
-                                                            Item* items, int32_t* count) {
+                                                            const int32_t* offsets, int experts, int rows, Item* area,
+                                                            int most_brief, int most_tiles) {
   __shared__ float part[kThreads / kWave];
-  __shared__ int scan[kThreads];
   const int t = threadIdx.x;
   if ((int)blockIdx.x == tokens) {
-    int base = 0;
-    for (int e0 = 0; e0 < experts; e0 += kThreads) {
-      const int e = e0 + t;
-      int first = 0, n = 0;
-      if (e < experts) {
-        first = min(max(offsets[e], 0), rows);
-        n = max(min(max(offsets[e + 1], 0), rows) - first, 0);
-      }
-      const int tiles = (n + kItemRows - 1) / kItemRows;
-      scan[t] = tiles;
-      __syncthreads();
-      for (int d = 1; d < kThreads; d *= 2) {
-        const int v = t >= d ? scan[t - d] : 0;
-        __syncthreads();
-        scan[t] += v;
-        __syncthreads();
-      }
-      const int most = rows / kItemRows + min(rows, experts);
-      for (int i = 0; i < tiles; ++i) {
-        const int at = base + scan[t] - tiles + i;
-        if (at < most) items[at] = Item{e, first + i * kItemRows, min(n - i * kItemRows, kItemRows), 0};
-      }
-      base += scan[kThreads - 1];
-      __syncthreads();
-    }
-    if (t == 0) *count = min(base, rows / kItemRows + min(rows, experts));
+    make_lists(offsets, experts, rows, area, most_brief, most_tiles);
     return;
   }
   const uint16_t* row = x + (int64_t)blockIdx.x * ldx;
@@ -97,12 +113,12 @@ __global__ __launch_bounds__(kThreads) void quantise_kernel(const uint16_t* x, i
 }
 
 hipError_t launch_quantise(int dtype, const void* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                           const int32_t* offsets, int experts, int rows, Item* items, int32_t* count,
-                           hipStream_t stream) {
+                           const int32_t* offsets, int experts, int rows, void* area, hipStream_t stream) {
   const unsigned blocks = (unsigned)tokens + (offsets != nullptr ? 1 : 0);
   return launch_kernel(dtype == BLOCK_BF16 ? quantise_kernel<BF16> : quantise_kernel<F16>, dim3(blocks),
                        dim3(kThreads), stream, static_cast<const uint16_t*>(x), ldx, tokens, k,
-                       red_blocks(k) * kBlockRed, q, step, offsets, experts, rows, items, count);
+                       red_blocks(k) * kBlockRed, q, step, offsets, experts, rows, static_cast<Item*>(area),
+                       (int)most_brief(rows, experts), (int)most_tiles(rows, experts));
 }
 
 // ---------------------------------------------------------------- weights --

@@ -1,0 +1,256 @@
+// 8-bit products of more rows: the tile kernel on v_mfma_i32_16x16x64_i8, for
+// experts of more than 32 rows and for dense products of as many.
+//
+// A tile is up to 256 rows of one expert by 256 columns of its packed weights
+// (for the gated product 128 output columns, gate and up alternating by 16).
+// Eight waves, two by four, have half of its rows and a quarter of its columns
+// each. The reduction runs in stages of 64, one MFMA deep, through a ring of
+// LDS buffers: one is read into registers while the one before is multiplied,
+// the others are on their way from memory. Rows lie in LDS as 64-byte lines
+// with a swizzle, weights as the packed form has them, so that neither read
+// meets a bank conflict. How many rows a tile has is known on the device only:
+// the kernel has a body for 64, 128, 192 and 256 of them and a block takes the
+// one that fits, and its CU's blocks go through the list of tiles by themselves.
+#include "experts_device.h"
+#include "lds_device.h"
+
+namespace experts {
+
+using block::dma16;
+using block::lds_b128;
+using block::wait_barrier;
+
+constexpr int kWaves = 8, kCols = 256, kLds = 160 * 1024;
+
+// 16-row fragments of a wave, of which there are two above each other.
+template <int MT>
+struct Shape {
+  static constexpr int BM = 32 * MT;
+  static constexpr int A_BYTES = BM * kBlockRed, B_BYTES = kCols * kBlockRed, STAGE = A_BYTES + B_BYTES;
+  static constexpr int kStages = kLds / STAGE < 8 ? kLds / STAGE : 8;
+  static constexpr int A_LOADS = BM / 16, A_PER = (A_LOADS + kWaves - 1) / kWaves;  // of 1 KB; of a wave
+  static constexpr int PER = A_PER + kCols / 16 / kWaves;
+  static constexpr int kReads = MT + 4;  // LDS reads of a wave and stage
+};
+
+template <typename T, bool Gated, int MT>
+__device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int expert, int row0, int rows, int tile0) {
+  typedef Shape<MT> S;
+  typedef typename T::raw raw;
+  constexpr int NT = 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, m = lane & 15;
+  const int wm = wave / 4, wn = wave % 4;
+  const int tiles = packed_tiles<Gated>(p), count = p.blocks;
+
+  // ---- global -> LDS: rows past the last repeat it, column tiles likewise ----
+  const char* src[S::PER];
+  uint32_t dst[S::PER];
+  constexpr int kStep[2] = {kBlockRed, kBlockBytes};  // from one stage to the next
+#pragma unroll
+  for (int i = 0; i < S::PER; ++i) {
+    if (i < S::A_PER) {
+      // fewer loads than waves: some are done twice, so that every wave counts alike
+      const int c = (wave + kWaves * i) % S::A_LOADS;
+      const int t = token_of(p, row0 + min(16 * c + (lane >> 2), rows - 1));
+      src[i] = reinterpret_cast<const char*>(p.q) + (int64_t)t * count * kBlockRed +
+               16 * ((lane & 3) ^ block::swizzle(lane >> 4));
+      dst[i] = c * 1024;
+    } else {
+      const int c = wave + kWaves * (i - S::A_PER);
+      src[i] = reinterpret_cast<const char*>(packed_tile(p, expert, tiles, min(tile0 + c, tiles - 1))) + 16 * lane;
+      dst[i] = S::A_BYTES + c * 1024;
+    }
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(block::lds_void*)smem;
+  auto issue = [&](int i, int s, uint32_t buf) __attribute__((always_inline)) {
+    dma16(src[i] + (int64_t)s * kStep[i < S::A_PER ? 0 : 1], buf + dst[i]);
+  };
+  // the row's scale, for the ending
+  const int mine = min((int)threadIdx.x, rows - 1);
+  const float step = p.step[token_of(p, row0 + mine)];
+
+  // ---- LDS -> registers ----
+  const uint32_t a_rd = (uint32_t)(wm * MT * 1024 + m * 64 + (g ^ block::swizzle(m >> 2)) * 16);
+  const uint32_t b_rd = (uint32_t)(S::A_BYTES + wn * NT * 1024 + 16 * lane);
+  auto read_a = [&](uint32_t buf, int i) { return lds_b128(buf + a_rd + i * 1024); };
+  auto read_b = [&](uint32_t buf, int j) { return lds_b128(buf + b_rd + j * 1024); };
+
+  i32x4 acc[MT][NT] = {};
+  u32x4 a[MT], b0[NT], b1[NT];
+  // Stage s's MFMAs, while stage s + 1 is read (a[i] as soon as its last MFMA is
+  // issued, b into the other registers) and the loads of stage s + kStages - 1 go
+  // out into the buffer that the last barrier freed.
+  auto step_of = [&](u32x4(&b)[NT], u32x4(&bn)[NT], uint32_t next, auto load) __attribute__((always_inline)) {
+    constexpr int kEvery = MT * NT / S::PER;
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int n = i * NT + j;
+        if (n % kEvery == kEvery / 2 && n / kEvery < S::PER) load(n / kEvery);
+        acc[i][j] = mfma(b[j], a[i], acc[i][j]);
+      }
+      if (MT >= NT ? i < NT : true)
+#pragma unroll
+        for (int j = i; j < NT; j += MT) bn[j] = read_b(next, j);
+      a[i] = read_a(next, i);
+    }
+  };
+  constexpr int kLgkm = S::kReads < 15 ? S::kReads : 15;
+  constexpr int kAhead = S::kStages - 1;
+
+#pragma unroll 1
+  for (int s = 0; s < min(count, kAhead); ++s)
+#pragma unroll
+    for (int i = 0; i < S::PER; ++i) issue(i, s, lds0 + s * S::STAGE);
+  if (count >= kAhead)
+    wait_barrier<(kAhead - 2) * S::PER, 0>();
+  else
+    wait_barrier<0, 0>();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) a[i] = read_a(lds0, i);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) b0[j] = read_b(lds0, j);
+  constexpr uint32_t kEnd = S::kStages * S::STAGE;
+  uint32_t next = lds0 + S::STAGE, fill = lds0 + kAhead * S::STAGE;
+  auto advance = [&]() __attribute__((always_inline)) {
+    next = next + S::STAGE == lds0 + kEnd ? lds0 : next + S::STAGE;
+    fill = fill + S::STAGE == lds0 + kEnd ? lds0 : fill + S::STAGE;
+  };
+  int s = 0;
+  auto steady = [&](u32x4(&b)[NT], u32x4(&bn)[NT], int at) __attribute__((always_inline)) {
+    step_of(b, bn, next, [&](int n) __attribute__((always_inline)) { issue(n, at + kAhead, fill); });
+    wait_barrier<(kAhead - 2) * S::PER, kLgkm>();
+    advance();
+  };
+#pragma unroll 1
+  for (; s + 1 + kAhead < count; s += 2) {
+    steady(b0, b1, s);
+    steady(b1, b0, s + 1);
+  }
+  auto other = [&](int at, u32x4(&b)[NT], u32x4(&bn)[NT]) __attribute__((always_inline)) {
+    if (at >= count) return;
+    const bool more = at + kAhead < count;
+    step_of(b, bn, next, [&](int n) __attribute__((always_inline)) {
+      if (more) issue(n, at + kAhead, fill);
+    });
+    // stage at + 2 has to be in LDS
+    if (at + 2 < count) {
+      const int behind = min(count - 1, at + kAhead) - (at + 2);  // stages that may be in flight
+      if (behind >= kAhead - 2)
+        wait_barrier<(kAhead - 2) * S::PER, kLgkm>();
+      else if (behind >= 1)
+        wait_barrier<S::PER, kLgkm>();
+      else
+        wait_barrier<0, kLgkm>();
+    }
+    advance();
+  };
+#pragma unroll 1
+  for (; s < count; s += 2) {
+    other(s, b0, b1);
+    other(s + 1, b1, b0);
+  }
+
+  // ---- ending: each wave turns its sums around in LDS, 16 kRows rows at a
+  // time, so that a lane ends eight columns of a row at once ----
+  constexpr int kPitch = 16 * NT + 4;
+  constexpr int kRows = MT % 4 == 0 ? 4 : 2;
+  constexpr int kTurn = kWaves * 16 * kRows * kPitch * 4;
+  constexpr int kWide = Gated ? 8 * NT : 16 * NT;  // output columns of a wave
+  constexpr int kLanes = kWide / 8, kStepRows = kWave / kLanes, kSteps = 16 * kRows / kStepRows;
+  static_assert(kTurn + S::BM * 4 <= kLds, "LDS");
+  int* turn = reinterpret_cast<int*>(smem) + wave * 16 * kRows * kPitch;
+  float* steps = reinterpret_cast<float*>(smem + kTurn);
+  const int wcol = 8 * (lane % kLanes), col = (Gated ? tile0 / 2 : tile0) * 16 + kWide * wn + wcol;
+  const int from = Gated ? wcol / 16 * 32 + wcol % 16 : wcol;
+  const Columns<T, Gated, 8> k(p, expert, col);
+  __syncthreads();
+  if ((int)threadIdx.x < S::BM) steps[threadIdx.x] = step;
+  __syncthreads();
+#pragma unroll 1
+  for (int c = 0; c < MT / kRows; ++c) {
+#pragma unroll
+    for (int cc = 0; cc < MT / kRows; ++cc)
+      if (c == cc)
+#pragma unroll
+        for (int i = 0; i < kRows; ++i)
+#pragma unroll
+          for (int j = 0; j < NT; ++j)
+            *reinterpret_cast<i32x4*>(turn + (16 * i + m) * kPitch + 16 * j + 4 * g) = acc[kRows * cc + i][j];
+    __builtin_amdgcn_wave_barrier();
+    with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll 1
+      for (int q = 0; q < kSteps; ++q) {
+        const int local = 16 * MT * wm + 16 * kRows * c + q * kStepRows + lane / kLanes;
+        const int row = row0 + local;
+        if (local < rows && col < p.n) {
+          const int* t = turn + (q * kStepRows + lane / kLanes) * kPitch + from;
+          float v[8], u[8], residual[8] = {};
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const i32x4 x = *reinterpret_cast<const i32x4*>(t + 4 * h);
+            const i32x4 y = *reinterpret_cast<const i32x4*>(t + 4 * h + (Gated ? 16 : 0));
+#pragma unroll
+            for (int f = 0; f < 4; ++f) {
+              v[4 * h + f] = (float)x[f];
+              u[4 * h + f] = (float)y[f];
+            }
+          }
+          if (!Gated && p.residual != nullptr)
+            block::load_cols<T, 8>(static_cast<const raw*>(p.residual) + row * p.ldr + col, residual, p.n - col);
+          finish<T, Gated, decltype(act)::value, 8>(p, k, row, col, steps[local], v, u, residual);
+        }
+      }
+    });
+    __builtin_amdgcn_wave_barrier();
+  }
+  __syncthreads();  // before the next tile's loads to LDS
+}
+
+template <typename T, bool Gated>
+__global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
+void tile_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(1024))) char smem[kLds];
+  const int ntiles = (packed_tiles<Gated>(p) + kCols / 16 - 1) / (kCols / 16);
+  const int mtiles = p.lists.counts != nullptr ? p.lists.counts[1] : (p.rows + kTileRows - 1) / kTileRows;
+  const int64_t total = (int64_t)mtiles * ntiles;
+  // Blocks are dealt round-robin over the 8 XCDs: each XCD has a contiguous
+  // range of tiles, which its blocks go through in turn.
+  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
+  const int64_t end = total * (xcd + 1) / 8;
+  for (int64_t at = total * xcd / 8 + (blockIdx.x >> 3); at < end; at += per) {
+    // row tiles of an expert in groups of 8, column by column
+    const int i = (int)(at / ntiles);
+    Item it = p.lists.counts != nullptr ? p.lists.tiles[i] : Item{0, 0, p.rows, 0};
+    const int high = (it.rows + kTileRows - 1) / kTileRows;  // its row tiles
+    const int64_t local = at - (int64_t)it.first * ntiles;
+    const int group = (int)(local / (8 * ntiles)), in = (int)(local - (int64_t)group * 8 * ntiles);
+    const int gm = min(high - 8 * group, 8);
+    const int height = min(((it.rows + high - 1) / high + 31) / 32 * 32, kTileRows);
+    const int mt = 8 * group + in % gm, nt = in / gm;
+    const int row0 = it.row + mt * height, rows = min(height, it.rows - mt * height);
+    if (rows <= 64)
+      tile<T, Gated, 2>(p, smem, it.expert, row0, rows, nt * (kCols / 16));
+    else if (rows <= 128)
+      tile<T, Gated, 4>(p, smem, it.expert, row0, rows, nt * (kCols / 16));
+    else if (rows <= 192)
+      tile<T, Gated, 6>(p, smem, it.expert, row0, rows, nt * (kCols / 16));
+    else
+      tile<T, Gated, 8>(p, smem, it.expert, row0, rows, nt * (kCols / 16));
+  }
+}
+
+template <typename T, bool Gated>
+static hipError_t launch_typed(const ProductArgs& p, int experts, hipStream_t stream) {
+  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p);
+}
+
+hipError_t launch_tiles(int dtype, const ProductArgs& p, int experts, hipStream_t stream) {
+  if (dtype == BLOCK_BF16)
+    return p.gated ? launch_typed<BF16, true>(p, experts, stream) : launch_typed<BF16, false>(p, experts, stream);
+  return p.gated ? launch_typed<F16, true>(p, experts, stream) : launch_typed<F16, false>(p, experts, stream);
+}
+
+}  // namespace experts
