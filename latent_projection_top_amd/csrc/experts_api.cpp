@@ -113,15 +113,29 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.blocks = experts::red_blocks(c.inputs);
   a.act = c.activation;
   a.gated = planes == 2;
-  int st = status_of(experts::launch_quantise(c.dtype, x, x_stride, tokens, c.inputs,
-                                              reinterpret_cast<int8_t*>(ws + c.off_q),
-                                              reinterpret_cast<float*>(ws + c.off_step), offsets, c.experts, rows,
-                                              ws + c.off_lists, s));
+  experts::QuantiseArgs z{};
+  z.x = static_cast<const uint16_t*>(x);
+  z.ldx = x_stride;
+  z.q = reinterpret_cast<int8_t*>(ws + c.off_q);
+  z.step = reinterpret_cast<float*>(ws + c.off_step);
+  z.offsets = offsets;
+  z.area = reinterpret_cast<experts::Item*>(ws + c.off_lists);
+  z.tokens = tokens;
+  z.k = c.inputs;
+  z.stride = a.blocks * experts::kBlockRed;
+  z.experts = c.experts;
+  z.rows = rows;
+  z.column_tiles = planes * experts::column_tiles(c.outputs);
+  z.blocks = a.blocks;
+  z.most_brief = (int)experts::most_brief(rows, c.experts);
+  z.most_mid = (int)experts::most_mid(rows, c.experts);
+  z.most_tiles = (int)experts::most_tiles(rows, c.experts);
+  int st = status_of(experts::launch_quantise(c.dtype, z, s));
   // which experts have few rows is known on the device only: both kernels go
   // through their lists
   if (st == ROUTE_OK && (offsets != nullptr || rows <= experts::kStreamRows))
     st = status_of(experts::launch_stream(c.dtype, a, c.experts, s));
-  if (st == ROUTE_OK && rows > experts::kStreamRows) st = status_of(experts::launch_tiles(c.dtype, a, c.experts, s));
+  if (st == ROUTE_OK && rows > experts::kStreamRows) st = status_of(experts::launch_tiles(c.dtype, a, s));
   return st;
 }
 

@@ -57,29 +57,46 @@ constexpr int kBlockRed = 64, kBlockBytes = 1024;
 inline int red_blocks(int k) { return (k + kBlockRed - 1) / kBlockRed; }
 inline int column_tiles(int n) { return (n + 15) / 16; }
 
-// The rows of one expert in a product: up to kStreamRows of them (a short item,
-// for the kernel that streams weights), or its first-th and later row tiles (an
-// entry for each tile; `rows` is of all of them).
+// The rows of one expert in a product: up to kStreamRows of them (`brief`, for
+// the kernel that streams weights), or one of its row tiles, of up to kMidRows
+// rows (`mid`) or the first-th and later of up to kTileRows (`tiles`, an entry
+// for each; `rows` is of all of them).
 struct Item {
   int32_t expert, row, rows, first;
 };
-constexpr int kStreamRows = 32, kTileRows = 256;
+constexpr int kStreamRows = 32, kMidRows = 64, kTileRows = 256;
+constexpr int kMidCols = 4, kTileCols = 16;  // packed column tiles of 16 each takes
 struct Lists {
-  const int32_t* counts;  // short items, row tiles; NULL: one expert has every row
+  const int32_t* counts;  // brief, mid, tiles; NULL: one expert has every row
   const Item* brief;
+  const Item* mid;
   const Item* tiles;
 };
 inline int64_t most_brief(int64_t rows, int experts) { return rows < experts ? rows : experts; }
-inline int64_t most_tiles(int64_t rows, int experts) {
-  const int64_t long_ones = rows / (kStreamRows + 1);
-  return rows / kTileRows + (long_ones < experts ? long_ones : experts);
+inline int64_t most_long(int64_t rows, int experts, int height) {
+  const int64_t n = rows / (kStreamRows + 1);
+  return rows / height + (n < experts ? n : experts);
 }
+inline int64_t most_mid(int64_t rows, int experts) { return most_long(rows, experts, kMidRows); }
+inline int64_t most_tiles(int64_t rows, int experts) { return most_long(rows, experts, kTileRows); }
 inline size_t list_bytes(int64_t rows, int experts) {
-  return sizeof(Item) * (size_t)(1 + most_brief(rows, experts) + most_tiles(rows, experts));
+  return sizeof(Item) *
+         (size_t)(1 + most_brief(rows, experts) + most_mid(rows, experts) + most_tiles(rows, experts));
 }
 inline Lists lists_at(void* area, int64_t rows, int experts) {
   const Item* items = static_cast<const Item*>(area);
-  return Lists{&items->expert, items + 1, items + 1 + most_brief(rows, experts)};
+  const Item* mid = items + 1 + most_brief(rows, experts);
+  return Lists{&items->expert, items + 1, mid, mid + most_mid(rows, experts)};
+}
+
+// Whether a product's long experts, `mids` row tiles by one height and `tiles`
+// by the other, go as row tiles of kMidRows altogether. Modelled times in us of
+// a tile of either kind by the reduction's blocks, and rounds of 256 of them.
+__host__ __device__ inline bool all_mid(int64_t mids, int64_t tiles, int column_tiles, int blocks) {
+  const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
+  const int64_t t = tiles * ((column_tiles + kTileCols - 1) / kTileCols);
+  return (float)((m + 255) / 256) * (5.f + 0.12f * (float)blocks) <
+         (float)((t + 255) / 256) * (6.f + 0.6f * (float)blocks);
 }
 
 // What the streaming kernel uses of the workspace: counters of its column
@@ -104,12 +121,22 @@ struct ProductArgs {
   int64_t ldr, ldy;
   int tokens, rows, n, blocks, act, gated;
 };
-// Also makes the lists (area: list_bytes) where there are offsets.
-hipError_t launch_quantise(int dtype, const void* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                           const int32_t* offsets, int experts, int rows, void* area, hipStream_t stream);
+// Rows as integers; where there are offsets also the lists of a product of
+// `rows` rows and `column_tiles` packed column tiles (area: list_bytes).
+struct QuantiseArgs {
+  const uint16_t* x;
+  int8_t* q;
+  float* step;
+  const int32_t* offsets;
+  Item* area;
+  int64_t ldx;
+  int tokens, k, stride, experts, rows, column_tiles, blocks;
+  int most_brief, most_mid, most_tiles;
+};
+hipError_t launch_quantise(int dtype, const QuantiseArgs& args, hipStream_t stream);
 // Experts of 1..kStreamRows rows, and those of more.
 hipError_t launch_stream(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
-hipError_t launch_tiles(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
+hipError_t launch_tiles(int dtype, const ProductArgs& args, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,
                        hipStream_t stream);

@@ -52,53 +52,79 @@ __device__ __forceinline__ float magnitude(uint32_t bits) {
   return T::load((uint16_t)bits);
 }
 
-// The lists of short items and row tiles, by the first four waves of a block.
-// An expert of more than kStreamRows rows has as few tiles of at most kTileRows
-// as it can, of equal height.
-__device__ __forceinline__ void make_lists(const int32_t* offsets, int experts, int rows, Item* area,
-                                           int most_brief, int most_tiles) {
-  __shared__ int2 part[kThreads / kWave];
+// The lists of a product's items, by the first four waves of a block. Up to
+// kStreamRows rows of an expert are one brief item. Of more, up to kMidRows are
+// one mid item and the others as few tiles of at most kTileRows as they can be,
+// of equal height; or all are mid items.
+__device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
+  __shared__ int4 part[kThreads / kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
-  Item* brief = area + 1;
-  Item* tiles = brief + most_brief;
-  int briefs = 0, tile = 0;  // so far
-  for (int e0 = 0; e0 < experts; e0 += kThreads) {
-    const int e = e0 + t;
-    int first = 0, n = 0;
-    if (t < kThreads && e < experts) {
-      first = min(max(offsets[e], 0), rows);
-      n = max(min(max(offsets[e + 1], 0), rows) - first, 0);
-    }
-    const int b = n > 0 && n <= kStreamRows ? 1 : 0;
-    const int m = n > kStreamRows ? (n + kTileRows - 1) / kTileRows : 0;
-    int rb = b, rm = m;
+  Item* lists[3] = {p.area + 1, p.area + 1 + p.most_brief, p.area + 1 + p.most_brief + p.most_mid};
+  const int most[3] = {p.most_brief, p.most_mid, p.most_tiles};
+  auto rows_of = [&](int e, int& first) __attribute__((always_inline)) {
+    first = 0;
+    if (t >= kThreads || e >= p.experts) return 0;
+    first = min(max(p.offsets[e], 0), p.rows);
+    return max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
+  };
+  // sums over the block, and before this thread
+  auto scan = [&](int4 v, int4& before) __attribute__((always_inline)) {
+    int4 r = v;
     for (int d = 1; d < kWave; d *= 2) {
-      const int vb = __shfl_up(rb, d), vm = __shfl_up(rm, d);
-      rb += lane >= d ? vb : 0;
-      rm += lane >= d ? vm : 0;
+      const int x = __shfl_up(r.x, d), y = __shfl_up(r.y, d), z = __shfl_up(r.z, d);
+      if (lane >= d) r = int4{r.x + x, r.y + y, r.z + z, 0};
     }
-    if (t < kThreads && lane == kWave - 1) part[wave] = int2{rb, rm};
+    if (t < kThreads && lane == kWave - 1) part[wave] = r;
     __syncthreads();
-    int ab = briefs + rb - b, am = tile + rm - m;
+    before = int4{r.x - v.x, r.y - v.y, r.z - v.z, 0};
+    int4 all = {0, 0, 0, 0};
     for (int w = 0; w < kThreads / kWave; ++w) {
-      ab += w < wave ? part[w].x : 0;
-      am += w < wave ? part[w].y : 0;
-      briefs += part[w].x;
-      tile += part[w].y;
+      const int4 s = part[w];
+      if (w < wave) before = int4{before.x + s.x, before.y + s.y, before.z + s.z, 0};
+      all = int4{all.x + s.x, all.y + s.y, all.z + s.z, 0};
     }
+    __syncthreads();
+    return all;
+  };
+  int64_t mids = 0, tiles = 0;
+  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+    int first;
+    const int n = rows_of(e0 + t, first);
+    int4 before;
+    const int4 all = scan(n > kStreamRows ? int4{0, (n + kMidRows - 1) / kMidRows,
+                                                 n > kMidRows ? (n + kTileRows - 1) / kTileRows : 0, 0}
+                                          : int4{0, 0, 0, 0}, before);
+    mids += all.y;
+    tiles += all.z;
+  }
+  const int mid_rows = all_mid(mids, tiles, p.column_tiles, p.blocks) ? p.rows : kMidRows;
+  int4 done = {0, 0, 0, 0};
+  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+    const int e = e0 + t;
+    int first;
+    const int n = rows_of(e, first);
+    // this thread's items: how many, of which list
+    const int kind = n <= kStreamRows ? 0 : n <= mid_rows ? 1 : 2;
+    const int m = n == 0 ? 0 : kind == 0 ? 1 : kind == 1 ? (n + kMidRows - 1) / kMidRows
+                                                        : (n + kTileRows - 1) / kTileRows;
+    int4 before;
+    const int4 all = scan(int4{kind == 0 ? m : 0, kind == 1 ? m : 0, kind == 2 ? m : 0, 0}, before);
+    const int start = kind == 0 ? done.x + before.x : kind == 1 ? done.y + before.y : done.z + before.z;
     // offsets that overlap would make more than there is room for
-    if (b != 0 && ab < most_brief) brief[ab] = Item{e, first, n, 0};
-    uint64_t todo = __ballot(m > 0);  // a wave writes an expert's tiles together
+    if (m == 1 && start < most[kind]) lists[kind][start] = Item{e, first, n, start};
+    uint64_t todo = __ballot(m > 1);  // a wave writes an expert's tiles together
     while (todo != 0) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
-      const int at = __shfl(am, l), end = min(at + __shfl(m, l), most_tiles);
-      const Item it{__shfl(e, l), __shfl(first, l), __shfl(n, l), at};
-      for (int i = at + lane; i < end; i += kWave) tiles[i] = it;
+      const int k = __shfl(kind, l), at = __shfl(start, l), count = __shfl(m, l);
+      const int of = __shfl(e, l), row = __shfl(first, l), rows = __shfl(n, l);
+      for (int i = lane; i < count && at + i < most[k]; i += kWave)
+        lists[k][at + i] = k == 1 ? Item{of, row + i * kMidRows, min(rows - i * kMidRows, kMidRows), at}
+                                  : Item{of, row, rows, at};
     }
-    __syncthreads();
+    done = int4{done.x + all.x, done.y + all.y, done.z + all.z, 0};
   }
-  if (t == 0) *area = Item{min(briefs, most_brief), min(tile, most_tiles), 0, 0};
+  if (t == 0) *p.area = Item{min(done.x, most[0]), min(done.y, most[1]), min(done.z, most[2]), 0};
 }
 
 typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
@@ -107,19 +133,17 @@ typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 // 16 values to a thread, which stay in registers from load to store. The block
 // after the last row makes the lists.
 template <typename T, int Threads, int Groups>
-__global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads)
-void quantise_kernel(const uint16_t* x, int64_t ldx, int tokens, int k, int stride, int8_t* q, float* step,
-                     const int32_t* offsets, int experts, int rows, Item* area, int most_brief, int most_tiles) {
+__global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quantise_kernel(QuantiseArgs p) {
   constexpr int kBlock = Threads < kThreads ? kThreads : Threads, kRowsPer = kBlock / Threads;
   __shared__ uint32_t part[kBlock / kWave];
-  const int blocks = (tokens + kRowsPer - 1) / kRowsPer;
+  const int blocks = (p.tokens + kRowsPer - 1) / kRowsPer, k = p.k;
   if ((int)blockIdx.x == blocks) {
-    make_lists(offsets, experts, rows, area, most_brief, most_tiles);
+    make_lists(p);
     return;
   }
   const int t = threadIdx.x % Threads, row = blockIdx.x * kRowsPer + threadIdx.x / Threads;
-  const bool live = row < tokens;
-  const uint16_t* in = x + (int64_t)(live ? row : tokens - 1) * ldx;
+  const bool live = row < p.tokens;
+  const uint16_t* in = p.x + (int64_t)(live ? row : p.tokens - 1) * p.ldx;
   u32x4 v[Groups][2];
 #pragma unroll
   for (int i = 0; i < Groups; ++i)
@@ -154,12 +178,12 @@ void quantise_kernel(const uint16_t* x, int64_t ldx, int tokens, int k, int stri
   }
   const Quantiser z(magnitude<T>(most));
   if (!live) return;
-  if (t == 0) step[row] = z.s;
-  int8_t* out = q + (int64_t)row * stride;
+  if (t == 0) p.step[row] = z.s;
+  int8_t* out = p.q + (int64_t)row * p.stride;
 #pragma unroll
   for (int i = 0; i < Groups; ++i) {
     const int c = 16 * (t + Threads * i);
-    if (c >= stride) break;
+    if (c >= p.stride) break;
     u32x4 b;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -172,33 +196,22 @@ void quantise_kernel(const uint16_t* x, int64_t ldx, int tokens, int k, int stri
 }
 
 template <typename T, int Threads, int Groups>
-static hipError_t launch_rows(const uint16_t* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                              const int32_t* offsets, int experts, int rows, Item* area, hipStream_t stream) {
+static hipError_t launch_rows(const QuantiseArgs& p, hipStream_t stream) {
   constexpr int kBlock = Threads < kThreads ? kThreads : Threads, kRowsPer = kBlock / Threads;
-  const unsigned blocks = (unsigned)((tokens + kRowsPer - 1) / kRowsPer) + (offsets != nullptr ? 1 : 0);
-  return launch_kernel(quantise_kernel<T, Threads, Groups>, dim3(blocks), dim3(kBlock), stream, x, ldx, tokens, k,
-                       red_blocks(k) * kBlockRed, q, step, offsets, experts, rows, area,
-                       (int)most_brief(rows, experts), (int)most_tiles(rows, experts));
+  const unsigned blocks = (unsigned)((p.tokens + kRowsPer - 1) / kRowsPer) + (p.offsets != nullptr ? 1 : 0);
+  return launch_kernel(quantise_kernel<T, Threads, Groups>, dim3(blocks), dim3(kBlock), stream, p);
 }
 
 // A wave to a row where there are enough of them to fill the CUs, else a block.
 template <typename T>
-static hipError_t launch_typed(const uint16_t* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                               const int32_t* offsets, int experts, int rows, Item* area, hipStream_t stream) {
-  if (k > 8192)
-    return launch_rows<T, 1024, 8>(x, ldx, tokens, k, q, step, offsets, experts, rows, area, stream);
-  if (k > 4096 || tokens < 1024)
-    return launch_rows<T, 256, 2>(x, ldx, tokens, k, q, step, offsets, experts, rows, area, stream);
-  return launch_rows<T, 64, 4>(x, ldx, tokens, k, q, step, offsets, experts, rows, area, stream);
+static hipError_t launch_typed(const QuantiseArgs& p, hipStream_t stream) {
+  if (p.k > 8192) return launch_rows<T, 1024, 8>(p, stream);
+  if (p.k > 4096 || p.tokens < 1024) return launch_rows<T, 256, 2>(p, stream);
+  return launch_rows<T, 64, 4>(p, stream);
 }
 
-hipError_t launch_quantise(int dtype, const void* x, int64_t ldx, int tokens, int k, int8_t* q, float* step,
-                           const int32_t* offsets, int experts, int rows, void* area, hipStream_t stream) {
-  const uint16_t* in = static_cast<const uint16_t*>(x);
-  Item* items = static_cast<Item*>(area);
-  return dtype == BLOCK_BF16
-             ? launch_typed<BF16>(in, ldx, tokens, k, q, step, offsets, experts, rows, items, stream)
-             : launch_typed<F16>(in, ldx, tokens, k, q, step, offsets, experts, rows, items, stream);
+hipError_t launch_quantise(int dtype, const QuantiseArgs& p, hipStream_t stream) {
+  return dtype == BLOCK_BF16 ? launch_typed<BF16>(p, stream) : launch_typed<F16>(p, stream);
 }
 
 // ---------------------------------------------------------------- weights --
