@@ -24,7 +24,7 @@ SOURCES = ["route_api.cpp", "topk16.hip", "topk16_sharded.hip", "decode_route.hi
            "experts_api.cpp", "experts_sort.hip", "experts_rows.hip", "experts_quantise.hip",
            "experts_stream.hip", "experts_tile.hip"]
 HEADERS = ["route_device.h", "route_launch.h", "block_device.h", "block_launch.h", "lds_device.h",
-           "experts_launch.h", "experts_device.h"]
+           "experts_launch.h", "experts_device.h", "experts_quantiser.h"]
 
 COMMON_FLAGS = [
     "-O3", "-std=c++17", f"--offload-arch={ARCH}", "-fPIC",

@@ -113,8 +113,15 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.blocks = experts::red_blocks(c.inputs);
   a.act = c.activation;
   a.gated = planes == 2;
+  a.x = static_cast<const uint16_t*>(x);
+  a.ldx = x_stride;
+  a.k = c.inputs;
+  a.experts = c.experts;
+  a.offsets = offsets;
+  if (experts::is_fused(rows, c.experts, offsets != nullptr))
+    return status_of(experts::launch_stream(c.dtype, a, true, 0, s));
   experts::QuantiseArgs z{};
-  z.x = static_cast<const uint16_t*>(x);
+  z.x = a.x;
   z.ldx = x_stride;
   z.q = reinterpret_cast<int8_t*>(ws + c.off_q);
   z.step = reinterpret_cast<float*>(ws + c.off_step);
@@ -130,13 +137,19 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);
   z.most_tiles = (int)experts::most_tiles(rows, c.experts);
-  int st = status_of(experts::launch_quantise(c.dtype, z, s));
-  // which experts have few rows is known on the device only: both kernels go
+  if (int st = status_of(experts::launch_quantise(c.dtype, z, s))) return st;
+  if (offsets == nullptr) {
+    if (rows <= experts::kStreamRows)
+      return status_of(experts::launch_stream(c.dtype, a, false, experts::kStreamRows, s));
+    if (experts::all_mid((rows + experts::kMidRows - 1) / experts::kMidRows,
+                         (rows + experts::kTileRows - 1) / experts::kTileRows, z.column_tiles, a.blocks))
+      return status_of(experts::launch_stream(c.dtype, a, false, experts::kMidRows, s));
+    return status_of(experts::launch_tiles(c.dtype, a, s));
+  }
+  // how many rows an expert has is known on the device only: both kernels go
   // through their lists
-  if (st == ROUTE_OK && (offsets != nullptr || rows <= experts::kStreamRows))
-    st = status_of(experts::launch_stream(c.dtype, a, c.experts, s));
-  if (st == ROUTE_OK && rows > experts::kStreamRows) st = status_of(experts::launch_tiles(c.dtype, a, s));
-  return st;
+  if (int st = status_of(experts::launch_stream(c.dtype, a, false, 0, s))) return st;
+  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, s)) : ROUTE_OK;
 }
 
 int run_quantize(const Product8& c, const void* w, int8_t* w8, float* scale, void* stream) {

@@ -57,10 +57,10 @@ constexpr int kBlockRed = 64, kBlockBytes = 1024;
 inline int red_blocks(int k) { return (k + kBlockRed - 1) / kBlockRed; }
 inline int column_tiles(int n) { return (n + 15) / 16; }
 
-// The rows of one expert in a product: up to kStreamRows of them (`brief`, for
-// the kernel that streams weights), or one of its row tiles, of up to kMidRows
-// rows (`mid`) or the first-th and later of up to kTileRows (`tiles`, an entry
-// for each; `rows` is of all of them).
+// The rows of one expert in a product: up to kStreamRows of them (`brief`), or
+// one of its row tiles, all of a product of up to kMidRows rows (`mid`) or the
+// first-th and later of up to kTileRows (`tiles`, an entry for each; `rows` is
+// of all of them).
 struct Item {
   int32_t expert, row, rows, first;
 };
@@ -90,24 +90,33 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
 }
 
 // Whether a product's long experts, `mids` row tiles by one height and `tiles`
-// by the other, go as row tiles of kMidRows altogether. Modelled times in us of
-// a tile of either kind by the reduction's blocks, and rounds of 256 of them.
+// by the other, go as row tiles of kMidRows altogether. Modelled times in us:
+// a mid item's is mostly latency, until their operands, 8 KB for each block of
+// the reduction, keep the L2s busy (8 TB/s); tiles come in rounds of 256.
 __host__ __device__ inline bool all_mid(int64_t mids, int64_t tiles, int column_tiles, int blocks) {
   const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
   const int64_t t = tiles * ((column_tiles + kTileCols - 1) / kTileCols);
-  return (float)((m + 255) / 256) * (5.f + 0.12f * (float)blocks) <
-         (float)((t + 255) / 256) * (6.f + 0.6f * (float)blocks);
+  const float latency = 6.f + 0.1f * (float)blocks, busy = (float)m * (float)blocks * 0.001f;
+  return (latency > busy ? latency : busy) < (float)((t + 255) / 256) * (6.f + 0.6f * (float)blocks);
+}
+
+// The most rows of a product that makes the integers by itself: of an item, and
+// of all of them by expert, where most experts have to have few.
+constexpr int kFusedItem = 16, kFusedRows = 512;
+inline bool is_fused(int64_t rows, int experts, bool offsets) {
+  return rows <= kFusedItem || (offsets && rows <= kFusedRows && rows <= 8 * (int64_t)experts);
 }
 
 // What the streaming kernel uses of the workspace: counters of its column
 // groups, zero between calls, 64 bytes apart, and split sums, a unit of them
 // for each block.
-constexpr int kSplitUnits = 256, kUnitInts = kStreamRows * 64;
+constexpr int kSplitUnits = 256, kUnitInts = kMidRows * 16 * kMidCols;
 static_assert(kSplitUnits * 64 <= EXPERTS_WORKSPACE_ZEROED, "what the caller clears");
 constexpr size_t kPartialBytes = (size_t)kSplitUnits * kUnitInts * 4;
 
 struct ProductArgs {
-  const int8_t* q;          // rows of x as integers, stride 64 * blocks, zeros past the end
+  const uint16_t* x;        // rows as they are
+  const int8_t* q;          // as integers, stride 64 * blocks, zeros past the end
   const float* step;        // their scales
   const void* packed;
   const float* scale[2];    // [experts][n]; [1] for the gated product
@@ -115,11 +124,12 @@ struct ProductArgs {
   const void* residual;
   void* y;
   const int32_t* token;     // NULL: the row itself
+  const int32_t* offsets;   // NULL: one expert has every row
   Lists lists;
   uint32_t* counters;
   int32_t* partial;
-  int64_t ldr, ldy;
-  int tokens, rows, n, blocks, act, gated;
+  int64_t ldx, ldr, ldy;
+  int tokens, rows, experts, k, n, blocks, act, gated;
 };
 // Rows as integers; where there are offsets also the lists of a product of
 // `rows` rows and `column_tiles` packed column tiles (area: list_bytes).
@@ -134,8 +144,9 @@ struct QuantiseArgs {
   int most_brief, most_mid, most_tiles;
 };
 hipError_t launch_quantise(int dtype, const QuantiseArgs& args, hipStream_t stream);
-// Experts of 1..kStreamRows rows, and those of more.
-hipError_t launch_stream(int dtype, const ProductArgs& args, int experts, hipStream_t stream);
+// Brief and mid items; without offsets, items of `dense` rows (0: none).
+hipError_t launch_stream(int dtype, const ProductArgs& args, bool fused, int dense, hipStream_t stream);
+// Tiles; without offsets, of every row.
 hipError_t launch_tiles(int dtype, const ProductArgs& args, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,

@@ -1,7 +1,7 @@
 // Rows and weights as 8-bit integers, the packed form of the weights, and the
 // list of row tiles that the products work through.
 #include "block_device.h"
-#include "experts_launch.h"
+#include "experts_quantiser.h"
 
 namespace experts {
 
@@ -12,50 +12,10 @@ using block::u32x4;
 
 constexpr int kThreads = 256;
 
-// The integers of values whose largest magnitude is `most`: q = rne(127 x / a),
-// s = a / 127. The quotient is decided without a division: with x and a of at
-// most 11 significant bits it is a border n + 1/2 exactly or at least 2^-19 of
-// its size from one, and t below, a product corrected by its exact residual
-// (fma), is within an ulp of it and equal where it is representable, as every
-// border is. Values so small that 1 / a overflows, or so large that 127 x does,
-// are scaled first, exactly.
-struct Quantiser {
-  float up, inv, a, s;
-  __device__ __forceinline__ explicit Quantiser(float most) {
-    const float shift = most < 0x1p-60f ? 0x1p+100f : most > 0x1p+60f ? 0x1p-100f : 1.f;
-    a = most * shift;
-    up = 127.f * shift;
-    inv = a > 0.f ? 1.f / a : 0.f;
-    s = most / 127.f;
-    if (!(most < INFINITY)) {  // infinite or NaN: the whole row is NaN
-      a = inv = up = 0.f;
-      s = NAN;
-    }
-  }
-  // the integer in the low byte; adding 1.5 x 2^23 rounds to nearest-even
-  __device__ __forceinline__ uint32_t byte(float x) const {
-    const float n = up > 0.f ? up * x : 0.f;
-    const float t = n * inv;
-    return __float_as_uint(fmaf(fmaf(-t, a, n), inv, t) + 12582912.f);
-  }
-  __device__ __forceinline__ uint32_t bytes(float x, float y, float z, float w) const {
-    const uint32_t lo = __builtin_amdgcn_perm(byte(y), byte(x), 0x0c0c0400);
-    const uint32_t hi = __builtin_amdgcn_perm(byte(w), byte(z), 0x0c0c0400);
-    return lo | hi << 16;
-  }
-};
-
-// Largest magnitude of a type's values as the bits of one of them, which are in
-// order for what has no sign: infinity and NaN come last.
-template <typename T>
-__device__ __forceinline__ float magnitude(uint32_t bits) {
-  return T::load((uint16_t)bits);
-}
-
 // The lists of a product's items, by the first four waves of a block. Up to
-// kStreamRows rows of an expert are one brief item. Of more, up to kMidRows are
-// one mid item and the others as few tiles of at most kTileRows as they can be,
-// of equal height; or all are mid items.
+// kStreamRows rows of an expert are one brief item. More are row tiles: in all
+// of the product mid items, or as few tiles of at most kTileRows as there can be,
+// of equal height.
 __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
   __shared__ int4 part[kThreads / kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
@@ -91,20 +51,19 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
     int first;
     const int n = rows_of(e0 + t, first);
     int4 before;
-    const int4 all = scan(n > kStreamRows ? int4{0, (n + kMidRows - 1) / kMidRows,
-                                                 n > kMidRows ? (n + kTileRows - 1) / kTileRows : 0, 0}
+    const int4 all = scan(n > kStreamRows ? int4{0, (n + kMidRows - 1) / kMidRows, (n + kTileRows - 1) / kTileRows, 0}
                                           : int4{0, 0, 0, 0}, before);
     mids += all.y;
     tiles += all.z;
   }
-  const int mid_rows = all_mid(mids, tiles, p.column_tiles, p.blocks) ? p.rows : kMidRows;
+  const int long_kind = all_mid(mids, tiles, p.column_tiles, p.blocks) ? 1 : 2;
   int4 done = {0, 0, 0, 0};
   for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
     const int e = e0 + t;
     int first;
     const int n = rows_of(e, first);
     // this thread's items: how many, of which list
-    const int kind = n <= kStreamRows ? 0 : n <= mid_rows ? 1 : 2;
+    const int kind = n <= kStreamRows ? 0 : long_kind;
     const int m = n == 0 ? 0 : kind == 0 ? 1 : kind == 1 ? (n + kMidRows - 1) / kMidRows
                                                         : (n + kTileRows - 1) / kTileRows;
     int4 before;
@@ -126,8 +85,6 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
   }
   if (t == 0) *p.area = Item{min(done.x, most[0]), min(done.y, most[1]), min(done.z, most[2]), 0};
 }
-
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
 
 // Rows as integers, bound by HBM: Threads threads to a row, up to Groups times
 // 16 values to a thread, which stay in registers from load to store. The block
@@ -163,10 +120,7 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
 #pragma unroll
   for (int i = 0; i < Groups; ++i)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        m = __builtin_elementwise_max(m, __builtin_bit_cast(u16x2, v[i][h][e] & 0x7fff7fffu));
+    for (int h = 0; h < 2; ++h) m = larger(m, v[i][h]);
   uint32_t most = max((uint32_t)m[0], (uint32_t)m[1]);
 #pragma unroll
   for (int d = kWave / 2; d > 0; d /= 2) most = max(most, (uint32_t)__shfl_xor((int)most, d));
@@ -184,14 +138,7 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
   for (int i = 0; i < Groups; ++i) {
     const int c = 16 * (t + Threads * i);
     if (c >= p.stride) break;
-    u32x4 b;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const uint32_t lo = v[i][e >> 1][2 * (e & 1)], hi = v[i][e >> 1][2 * (e & 1) + 1];
-      b[e] = z.bytes(T::load((uint16_t)lo), T::load((uint16_t)(lo >> 16)), T::load((uint16_t)hi),
-                     T::load((uint16_t)(hi >> 16)));
-    }
-    *reinterpret_cast<u32x4*>(out + c) = b;
+    *reinterpret_cast<u32x4*>(out + c) = z.template sixteen<T>(v[i][0], v[i][1]);
   }
 }
 

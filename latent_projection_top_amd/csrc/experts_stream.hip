@@ -1,19 +1,27 @@
-// 8-bit products of few rows (up to 32 of an expert): the time is the weights'
-// way from HBM.
+// 8-bit products of few rows of an expert: the time is the weights' way from
+// HBM, or, where there are few weights, the steps one after another.
 //
-// A block has one expert's rows and up to four column tiles of its packed
-// weights. Its eight waves take the reduction's blocks of 64 in turn, 1 KB of a
-// column tile per load, straight into the registers that the matrix cores read;
-// the next blocks' loads are under way while one is multiplied. The waves'
-// integer sums meet in LDS. Blocks go through the list of (expert, columns) by
-// themselves, since only the device knows how long it is. Where that is too
-// short to fill the CUs the reduction is also split over blocks, whose sums are
-// added by the last of them to arrive: integers, so in any order the same.
+// A block has up to 32 rows of one expert and four column tiles of its packed
+// weights, or up to 64 rows and two. Its eight waves take the reduction's blocks
+// of 64 in turn, 1 KB of a column tile per load, straight into the registers
+// that the matrix cores read; the next blocks' loads are under way while one is
+// multiplied. The waves' integer sums meet in LDS. 512 blocks, two to a CU, so
+// that one's sums meet while the other's weights arrive, go through the lists of
+// items by themselves, since only the device knows how long they are. Where
+// that is too little to fill the CUs and the reduction is long, it is also split
+// over blocks, whose sums are added by the last of them to arrive: integers, so
+// in any order the same.
+//
+// For few rows in all (Fused) the kernel reads the rows as they are and makes
+// the integers itself: each wave those of its own blocks of the reduction, after
+// the row's largest magnitude has gone around through LDS. That is done again
+// for every item, but saves a launch. It makes its own list of items as well.
 #include "experts_device.h"
+#include "experts_quantiser.h"
 
 namespace experts {
 
-constexpr int kWaves = 8;
+constexpr int kWaves = 8, kThreads = kWave * kWaves;
 
 // Sums between blocks of one launch: relaxed device-scope atomics, which go
 // past the XCDs' L2s both ways.
@@ -24,177 +32,382 @@ __device__ __forceinline__ int get(const int32_t* p) {
   return __hip_atomic_load(const_cast<int32_t*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
-template <int C>
-using Parts = int32_t[kWaves][kStreamRows][16 * C + 4];
+struct Shared {
+  int32_t part[kWaves * kStreamRows * (16 * 4 + 4)];
+  uint32_t most[kWaves][kFusedItem];
+  uint32_t arrived;
+};
 
-// One item's columns from tile0 on, its split-th of `splits` parts of the
-// reduction, with RT tiles of 16 rows.
-template <typename T, bool Gated, int C, int RT>
+// 16 values of a row, `count` of them inside it.
+__device__ __forceinline__ void load16(const uint16_t* p, u32x4 (&v)[2], int count) {
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    v[h] = u32x4{0, 0, 0, 0};
+    if (count >= 8 * h + 8) {
+      v[h] = reinterpret_cast<const block::Any16*>(p + 8 * h)->v;
+    } else {
+#pragma unroll
+      for (int t = 0; t < 7; ++t)
+        if (8 * h + t < count) v[h][t >> 1] |= (uint32_t)p[8 * h + t] << (16 * (t & 1));
+    }
+  }
+}
+
+// One item's columns from tile0 on, C column tiles of them, its split-th of
+// `splits` parts of the reduction, with RT tiles of 16 rows.
+// Whole: the reduction is whole blocks (the loads of rows that end inside one
+// are many instructions, which no other product should have to fetch).
+template <typename T, bool Gated, int C, int RT, bool Fused, bool Whole>
 __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it, int tile0, int unit, int split,
-                                            int splits, Parts<C>& part, uint32_t& arrived) {
+                                            int splits, Shared& shared) {
   typedef typename T::raw raw;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, m = lane & 15;
+  constexpr int kPitch = 16 * C + 4;
+  typedef int32_t Part[16 * (RT < 2 ? RT : 2)][kPitch];
+  Part* part = reinterpret_cast<Part*>(shared.part);
+  static_assert(sizeof(Part) * kWaves <= sizeof(Shared::part), "LDS");
+  // (not the same register as in the item before: what is made of it would
+  // otherwise be kept from item to item, in more registers than there are)
+  int tid = threadIdx.x;
+  asm volatile("" : "+v"(tid));
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int lane = tid & (kWave - 1), g = lane >> 4, m = lane & 15;
   const int tiles = packed_tiles<Gated>(p);
   const int b0 = (int)((int64_t)p.blocks * split / splits) + wave;
   const int b1 = (int)((int64_t)p.blocks * (split + 1) / splits);
   const int count = b1 > b0 ? (b1 - b0 + kWaves - 1) / kWaves : 0;
 
-  const uint8_t* w[C];
-  const int8_t* q[RT];
+  const uint8_t* w[C];  // uniform; lanes are 16 bytes apart
 #pragma unroll
   for (int c = 0; c < C; ++c)
-    w[c] = packed_tile(p, it.expert, tiles, min(tile0 + c, tiles - 1)) + (int64_t)b0 * kBlockBytes + 16 * lane;
+    w[c] = packed_tile(p, it.expert, tiles, min(tile0 + c, tiles - 1)) + (int64_t)b0 * kBlockBytes;
+  int token[RT];
+  const char* q[RT];
 #pragma unroll
-  for (int r = 0; r < RT; ++r)
-    q[r] = p.q + ((int64_t)token_of(p, it.row + min(16 * r + m, it.rows - 1)) * p.blocks + b0) * kBlockRed + 16 * g;
-
+  for (int r = 0; r < RT; ++r) {
+    token[r] = token_of(p, it.row + min(16 * r + m, it.rows - 1));
+    if constexpr (Fused)
+      q[r] = reinterpret_cast<const char*>(p.x + token[r] * p.ldx + b0 * kBlockRed + 16 * g);
+    else
+      q[r] = reinterpret_cast<const char*>(p.q) + ((int64_t)token[r] * p.blocks + b0) * kBlockRed + 16 * g;
+  }
+  constexpr int kX = Fused ? 2 : 1;
   struct Step {
-    u32x4 w[C], x[RT];
+    u32x4 w[C], x[RT][kX];
+  };
+  auto fetch_w = [&](Step& d, int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane));
+  };
+  auto fetch_x = [&](Step& d, int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if constexpr (Fused) {
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(q[r]) + (int64_t)i * kWaves * kBlockRed;
+        const int b = b0 + i * kWaves;
+        if (Whole || (b + 1) * kBlockRed <= p.k) {
+          d.x[r][0] = reinterpret_cast<const block::Any16*>(from)->v;
+          d.x[r][kX - 1] = reinterpret_cast<const block::Any16*>(from + 8)->v;
+        } else {
+          load16(from, reinterpret_cast<u32x4(&)[2]>(d.x[r]), p.k - b * kBlockRed - 16 * g);
+        }
+      } else {
+        d.x[r][0] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
+      }
+    }
   };
   auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
+    fetch_w(d, i);
+    fetch_x(d, i);
   };
+
+  Quantiser z[Fused ? RT : 1];
   i32x4 acc[C][RT] = {};
   auto multiply = [&](const Step& d) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)
+    for (int r = 0; r < RT; ++r) {
+      u32x4 x;
+      if constexpr (Fused)
+        x = z[r].template sixteen<T>(d.x[r][0], d.x[r][kX - 1]);
+      else
+        x = d.x[r][0];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) acc[c][r] = mfma(d.w[c], d.x[r], acc[c][r]);
+      for (int c = 0; c < C; ++c) acc[c][r] = mfma(d.w[c], x, acc[c][r]);
+    }
   };
-  if (count > 0) {
-    Step d0, d1;
-    fetch(d0, 0);
-    int i = 0;
+  // Depth steps are on their way at once, as many as there are registers for.
+  constexpr int kDepth = RT > 2 ? 1 : C == 2 ? 4 : RT == 1 ? 3 : 2;
+  Step d[kDepth];
+  if constexpr (Fused) {
+    // The rows' largest magnitudes: of this wave's blocks (of all of them, also
+    // where the reduction is split), then of all. The first blocks' loads go out
+    // before the weights', behind which they would have to wait.
+    constexpr int kFirst = 4;
+    u32x4 v[kFirst][RT][2];
+    auto look = [&](u32x4(&d)[RT][2], int b) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+        load16(reinterpret_cast<const uint16_t*>(q[r]) + (int64_t)(b - b0) * kBlockRed, d[r],
+               Whole ? 16 : p.k - b * kBlockRed - 16 * g);
+    };
+#pragma unroll
+    for (int i = 0; i < kFirst; ++i) look(v[i], min(wave + i * kWaves, p.blocks - 1));
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s)
+      if (s < count) fetch_w(d[s], s);
+    __builtin_amdgcn_sched_barrier(0);
+    u16x2 most[RT];
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      most[r] = u16x2{0, 0};
+#pragma unroll
+      for (int i = 0; i < kFirst; ++i) most[r] = larger(larger(most[r], v[i][r][0]), v[i][r][1]);
+    }
 #pragma unroll 1
-    for (; i + 2 < count; i += 2) {
-      fetch(d1, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d0);
-      fetch(d0, i + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d1);
+    for (int b = wave + kFirst * kWaves; b < p.blocks; b += kWaves) {
+      look(v[0], b);
+#pragma unroll
+      for (int r = 0; r < RT; ++r) most[r] = larger(larger(most[r], v[0][r][0]), v[0][r][1]);
     }
-    if (i + 1 < count) {
-      fetch(d1, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d0);
-      multiply(d1);
-    } else {
-      multiply(d0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      uint32_t a = max((uint32_t)most[r][0], (uint32_t)most[r][1]);
+      a = max(a, (uint32_t)__shfl_xor((int)a, 16));
+      a = max(a, (uint32_t)__shfl_xor((int)a, 32));
+      if (g == 0) shared.most[wave][16 * r + m] = a;
     }
+    __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS only: the weights are still on their way
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) a = max(a, shared.most[k][16 * r + m]);
+      z[r] = Quantiser(magnitude<T>(a));
+    }
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s)
+      if (s < count) fetch_x(d[s], s);
+  } else {
+#pragma unroll
+    for (int s = 0; s < kDepth; ++s)
+      if (s < count) fetch(d[s], s);
   }
-
-  // lane (g, m) holds row 16 r + m, columns 16 c + 4 g .. + 3
+#pragma unroll 1
+  for (int i = 0; i < count; i += kDepth)
 #pragma unroll
-  for (int c = 0; c < C; ++c)
-#pragma unroll
-    for (int r = 0; r < RT; ++r) *reinterpret_cast<i32x4*>(&part[wave][16 * r + m][16 * c + 4 * g]) = acc[c][r];
-  __syncthreads();
-
-  constexpr int kQuads = 4 * C;  // groups of 4 packed columns
-  auto sums = [&](int row, int quad) __attribute__((always_inline)) {
-    i32x4 v = {};
-#pragma unroll
-    for (int k = 0; k < kWaves; ++k) v += *reinterpret_cast<const i32x4*>(&part[k][row][4 * quad]);
-    return v;
-  };
-  bool last = true;
-  int32_t* units = p.partial + (int64_t)unit * splits * kUnitInts;
-  if (splits > 1) {
-    for (int id = threadIdx.x; id < it.rows * kQuads; id += kWave * kWaves) {
-      const i32x4 v = sums(id / kQuads, id % kQuads);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) put(units + (int64_t)split * kUnitInts + 4 * id + t, v[t]);
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      uint32_t* c = p.counters + 16 * unit;
-      arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (arrived == (uint32_t)splits - 1) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    last = arrived == (uint32_t)splits - 1;
-  }
-  if (last) {
-    constexpr int kOut = Gated ? kQuads / 2 : kQuads;  // groups of 4 output columns
-    const int out0 = (Gated ? tile0 / 2 : tile0) * 16;
-    with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
-      for (int id = threadIdx.x; id < it.rows * kOut; id += kWave * kWaves) {
-        const int row = id / kOut, o = id % kOut, col = out0 + 4 * o;
-        if (col >= p.n) continue;
-        const int quad = Gated ? o / 4 * 8 + o % 4 : o;
-        i32x4 v = {}, u = {};
-        if (splits > 1) {
-          for (int s = 0; s < splits; ++s)
-#pragma unroll
-            for (int t = 0; t < 4; ++t) {
-              const int32_t* e = units + (int64_t)s * kUnitInts + 4 * (row * kQuads + quad) + t;
-              v[t] += get(e);
-              if constexpr (Gated) u[t] += get(e + 16);
-            }
-        } else {
-          v = sums(row, quad);
-          if constexpr (Gated) u = sums(row, quad + 4);
-        }
-        const int64_t r = it.row + row;
-        const Columns<T, Gated, 4> k(p, it.expert, col);
-        float sum[4], up[4], residual[4] = {};
-        if (!Gated && p.residual != nullptr)
-          block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + r * p.ldr + col, residual, p.n - col);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          sum[t] = (float)v[t];
-          up[t] = (float)u[t];
-        }
-        finish<T, Gated, decltype(act)::value, 4>(p, k, (int)r, col, p.step[token_of(p, (int)r)], sum, up, residual);
+    for (int s = 0; s < kDepth; ++s)
+      if (i + s < count) {
+        multiply(d[s]);
+        if (i + s + kDepth < count) fetch(d[s], i + s + kDepth);
       }
-    });
+
+  // lane (g, m) holds row 16 r + m, columns 16 c + 4 g .. + 3. The waves' sums
+  // meet in LDS, at most 32 rows at a time; a thread ends four columns of a row.
+  // Where the reduction is split they go to memory instead, and the last block
+  // to arrive ends all rows, in one more turn.
+  constexpr int kAtOnce = RT < 2 ? RT : 2, kTurns = RT / kAtOnce;
+  constexpr int kQuads = 4 * C, kOut = Gated ? 2 * C : 4 * C;  // groups of 4 packed and output columns
+  int32_t* units = p.partial + (int64_t)unit * splits * kUnitInts;
+#pragma unroll 1
+  for (int h = 0; h < (splits > 1 ? kTurns + 1 : kTurns); ++h) {
+    int row0 = 16 * kAtOnce * h, row1 = min(row0 + 16 * kAtOnce, it.rows);
+    if (h < kTurns) {
+#pragma unroll
+      for (int x = 0; x < kTurns; ++x)
+        if (h == x)
+#pragma unroll
+          for (int c = 0; c < C; ++c)
+#pragma unroll
+            for (int r = 0; r < kAtOnce; ++r)
+              *reinterpret_cast<i32x4*>(&part[wave][16 * r + m][16 * c + 4 * g]) = acc[c][kAtOnce * x + r];
+      __syncthreads();
+    } else {
+      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
+      __syncthreads();
+      if (tid == 0) {
+        uint32_t* c = p.counters + 16 * unit;
+        shared.arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if (shared.arrived == (uint32_t)splits - 1)
+          __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      __syncthreads();
+      row0 = 0;
+      row1 = shared.arrived == (uint32_t)splits - 1 ? it.rows : 0;
+    }
+    auto sums = [&](int row, int quad) __attribute__((always_inline)) {
+      i32x4 v = {};
+#pragma unroll
+      for (int k = 0; k < kWaves; ++k) v += *reinterpret_cast<const i32x4*>(&part[k][row - row0][4 * quad]);
+      return v;
+    };
+    if (h < kTurns && splits > 1) {
+      for (int id = kQuads * row0 + tid; id < kQuads * row1; id += kThreads) {
+        const i32x4 v = sums(id / kQuads, id % kQuads);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) put(units + (int64_t)split * kUnitInts + 4 * id + t, v[t]);
+      }
+      row1 = row0;
+    }
+    auto sum_of = [&](int row, int quad) __attribute__((always_inline)) {
+      if (splits == 1) return sums(row, quad);
+      i32x4 v = {};
+      for (int s = 0; s < splits; ++s)
+#pragma unroll
+        for (int t = 0; t < 4; ++t) v[t] += get(units + (int64_t)s * kUnitInts + 4 * (row * kQuads + quad) + t);
+      return v;
+    };
+    const int out0 = (Gated ? tile0 / 2 : tile0) * 16;
+#pragma unroll 1
+    for (int id = tid; id < (row1 - row0) * kOut; id += kThreads) {
+      const int row = row0 + id / kOut, o = id % kOut, col = out0 + 4 * o;
+      if (col >= p.n) continue;
+      const int quad = Gated ? o / 4 * 8 + o % 4 : o;
+      const int64_t r = it.row + row;
+      const Columns<T, Gated, 4> k(p, it.expert, col);
+      float step;
+      if constexpr (Fused) {
+        uint32_t a = 0;
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) a = max(a, shared.most[x][row]);
+        step = Quantiser(magnitude<T>(a)).s;
+      } else {
+        step = p.step[token_of(p, (int)r)];
+      }
+      float sum[4], up[4] = {}, residual[4] = {};
+      if (!Gated && p.residual != nullptr)
+        block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + r * p.ldr + col, residual, p.n - col);
+      const i32x4 v = sum_of(row, quad);
+#pragma unroll
+      for (int t = 0; t < 4; ++t) sum[t] = (float)v[t];
+      if constexpr (Gated) {
+        const i32x4 u = sum_of(row, quad + 4);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) up[t] = (float)u[t];
+      }
+      with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
+        finish<T, Gated, decltype(act)::value, 4>(p, k, (int)r, col, step, sum, up, residual);
+      });
+    }
+    __syncthreads();  // before the next sums
   }
-  __syncthreads();  // before the next item's sums
 }
 
+// How many blocks share a unit of work: parts of at least four steps of a wave,
+// since a join costs 2 to 3 us, and a step some 0.4.
+__device__ __forceinline__ int splits_of(int64_t units, int blocks) {
+  return units == 0 || units >= kSplitUnits / 2 ? 1 : max(1, min(kSplitUnits / (int)units, blocks / (4 * kWaves)));
+}
+
+// Items of up to 32 rows by C column tiles, and of up to 64 rows by two.
+// (dense: one expert has every row, in items of this many)
 template <typename T, bool Gated, int C>
-__global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(4, 4)))
-void stream_kernel(ProductArgs p) {
-  __shared__ __attribute__((aligned(16))) Parts<C> part;
-  __shared__ uint32_t arrived;
-  const int groups = (packed_tiles<Gated>(p) + C - 1) / C;
-  const int items = p.lists.counts != nullptr ? p.lists.counts[0] : 1;
-  const int64_t total = (int64_t)items * groups;
-  if (total == 0) return;
-  int splits = 1;
-  if (total < kSplitUnits * 3 / 4)
-    splits = min(kSplitUnits / (int)total, max(p.blocks / kWaves, 1));
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void stream_kernel(ProductArgs p, int dense) {
+  __shared__ __attribute__((aligned(16))) Shared shared;
+  const int tiles = packed_tiles<Gated>(p), wide = (tiles + C - 1) / C, narrow = (tiles + kMidCols - 1) / kMidCols;
+  const bool listed = p.lists.counts != nullptr;
+  const int dense_items = dense > 0 ? (p.rows + dense - 1) / dense : 0;
+  const int briefs = listed ? p.lists.counts[0] : dense <= kStreamRows ? dense_items : 0;
+  const int mids = listed ? p.lists.counts[1] : dense_items - briefs;
+  const int64_t first = (int64_t)briefs * wide, total = first + (int64_t)mids * narrow;
+  const int splits = splits_of(total, p.blocks);
   for (int64_t at = blockIdx.x; at < total * splits; at += gridDim.x) {
-    const int unit = (int)(at / splits), split = (int)(at % splits);  // (more than one: at < kSplitUnits)
-    const int i = (int)(at / splits / groups), group = (int)(at / splits % groups);
-    const Item it = p.lists.counts != nullptr ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
-    if (it.rows <= 16)
-      stream_item<T, Gated, C, 1>(p, it, group * C, unit, split, splits, part, arrived);
-    else
-      stream_item<T, Gated, C, 2>(p, it, group * C, unit, split, splits, part, arrived);
+    const int64_t u = at / splits;
+    const int split = (int)(at - u * splits);  // (more than one: u < kSplitUnits / 2)
+    if (u < first) {
+      const int i = (int)(u / wide), tile0 = (int)(u - (int64_t)i * wide) * C;
+      const Item it = listed ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
+      if (it.rows <= 16)
+        stream_item<T, Gated, C, 1, false, true>(p, it, tile0, (int)u, split, splits, shared);
+      else
+        stream_item<T, Gated, C, 2, false, true>(p, it, tile0, (int)u, split, splits, shared);
+    } else {
+      const int64_t v = u - first;
+      // row tiles of the same columns next to each other
+      const int i = (int)(listed ? v / narrow : v % mids), tile0 = (int)(listed ? v % narrow : v / mids) * kMidCols;
+      const Item it = listed ? p.lists.mid[i] : Item{0, i * dense, min(p.rows - i * dense, dense), 0};
+      stream_item<T, Gated, kMidCols, 4, false, true>(p, it, tile0, (int)u, split, splits, shared);
+    }
   }
 }
 
-template <typename T, bool Gated>
-static hipError_t launch_typed(const ProductArgs& p, int experts, hipStream_t stream) {
-  const int64_t tiles = (Gated ? 2 : 1) * column_tiles(p.n);
-  const int64_t items = p.lists.counts != nullptr ? most_brief(p.rows, experts) : 1;
-  // two blocks to a CU
-  const dim3 grid(512), block(kWave * kWaves);
-  if (items * tiles <= 512 * 2) return launch_kernel(stream_kernel<T, Gated, 2>, grid, block, stream, p);
-  return launch_kernel(stream_kernel<T, Gated, 4>, grid, block, stream, p);
+// The same from the rows as they are, in items of up to kFusedItem of them.
+template <typename T, bool Gated, int C, bool Whole>
+__global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
+void fused_kernel(ProductArgs p) {
+  __shared__ __attribute__((aligned(16))) Shared shared;
+  __shared__ Item list[kFusedRows];
+  __shared__ int part[kWaves];
+  const int t = threadIdx.x;
+  int items = 1;
+  if (p.offsets != nullptr) {
+    items = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+      const int e = e0 + t;
+      int first = 0, n = 0;
+      if (e < p.experts) {
+        first = min(max(p.offsets[e], 0), p.rows);
+        n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
+      }
+      const int m = (n + kFusedItem - 1) / kFusedItem;
+      int run = m;
+      for (int d = 1; d < kWave; d *= 2) {
+        const int v = __shfl_up(run, d);
+        run += (t & (kWave - 1)) >= d ? v : 0;
+      }
+      if ((t & (kWave - 1)) == kWave - 1) part[t / kWave] = run;
+      __syncthreads();
+      int at = items + run - m;
+      for (int w = 0; w < kWaves; ++w) {
+        at += w < t / kWave ? part[w] : 0;
+        items += part[w];
+      }
+      for (int i = 0; i < m && at + i < kFusedRows; ++i)
+        list[at + i] = Item{e, first + i * kFusedItem, min(n - i * kFusedItem, kFusedItem), 0};
+      __syncthreads();
+    }
+    items = min(items, kFusedRows);
+  }
+  const int tiles = packed_tiles<Gated>(p), wide = (tiles + C - 1) / C;
+  const int64_t total = (int64_t)items * wide;
+  const int splits = splits_of(total, p.blocks);
+  for (int64_t at = blockIdx.x; at < total * splits; at += gridDim.x) {
+    const int64_t u = at / splits;
+    const int i = (int)(u / wide), tile0 = (int)(u - (int64_t)i * wide) * C, split = (int)(at - u * splits);
+    Item it{0, 0, p.rows, 0};
+    if (p.offsets != nullptr)
+      it = Item{__builtin_amdgcn_readfirstlane(list[i].expert), __builtin_amdgcn_readfirstlane(list[i].row),
+                __builtin_amdgcn_readfirstlane(list[i].rows), 0};
+    stream_item<T, Gated, C, 1, true, Whole>(p, it, tile0, (int)u, split, splits, shared);
+  }
 }
 
-hipError_t launch_stream(int dtype, const ProductArgs& p, int experts, hipStream_t stream) {
+// Two blocks to a CU; four column tiles to each unless that leaves CUs idle.
+template <typename T, bool Gated>
+static hipError_t launch_typed(const ProductArgs& p, bool fused, int dense, hipStream_t stream) {
+  const int64_t tiles = (Gated ? 2 : 1) * column_tiles(p.n);
+  const int64_t items = p.offsets != nullptr ? most_brief(p.rows, p.experts) : 1;
+  const dim3 grid(512), block(kThreads);
+  const bool narrow = items * tiles <= 512 * 2;
+  if (fused && p.k % kBlockRed == 0)
+    return launch_kernel(narrow ? fused_kernel<T, Gated, 2, true> : fused_kernel<T, Gated, 4, true>, grid, block,
+                         stream, p);
+  if (fused)
+    return launch_kernel(narrow ? fused_kernel<T, Gated, 2, false> : fused_kernel<T, Gated, 4, false>, grid, block,
+                         stream, p);
+  return launch_kernel(narrow ? stream_kernel<T, Gated, 2> : stream_kernel<T, Gated, 4>, grid, block, stream, p,
+                       dense);
+}
+
+hipError_t launch_stream(int dtype, const ProductArgs& p, bool fused, int dense, hipStream_t stream) {
   if (dtype == BLOCK_BF16)
-    return p.gated ? launch_typed<BF16, true>(p, experts, stream) : launch_typed<BF16, false>(p, experts, stream);
-  return p.gated ? launch_typed<F16, true>(p, experts, stream) : launch_typed<F16, false>(p, experts, stream);
+    return p.gated ? launch_typed<BF16, true>(p, fused, dense, stream)
+                   : launch_typed<BF16, false>(p, fused, dense, stream);
+  return p.gated ? launch_typed<F16, true>(p, fused, dense, stream)
+                 : launch_typed<F16, false>(p, fused, dense, stream);
 }
 
 }  // namespace experts

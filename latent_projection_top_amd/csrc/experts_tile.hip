@@ -1,20 +1,15 @@
-// 8-bit products of more than 32 rows of an expert, on
-// v_mfma_i32_16x16x64_i8. How many rows an expert has is known on the device
-// only: 256 blocks, one to a CU, go through the lists of items by themselves.
+// 8-bit products of more than 64 rows of an expert, on
+// v_mfma_i32_16x16x64_i8: up to 256 rows by 256 columns of the packed weights
+// (for the gated product 128 output columns, gate and up alternating by 16).
 //
-// tiles: up to 256 rows by 256 columns of the packed weights (for the gated
-// product 128 output columns, gate and up alternating by 16). Eight waves, two
-// by four, have half of the rows and a quarter of the columns each. The
-// reduction runs in stages of 64, one MFMA deep, through a ring of LDS buffers:
-// one is read into registers while the one before is multiplied, the others are
-// on their way from memory. Rows lie in LDS as 64-byte lines with a swizzle,
-// weights as the packed form has them, so that neither read meets a bank
-// conflict. There is a body for 128, 192 and 256 rows.
-//
-// mid items: up to 64 rows by 64 columns, the reduction dealt to the eight waves,
-// whose operands come straight from memory and whose sums meet in LDS: a
-// quarter of the matrix cores' rate at best, but an eighth of the steps one
-// after another, which is what the time of few rows or few tiles is made of.
+// Eight waves, two by four, have half of the rows and a quarter of the columns
+// each. The reduction runs in stages of 64, one MFMA deep, through a ring of
+// LDS buffers: one is read into registers while the one before is multiplied,
+// the others are on their way from memory. Rows lie in LDS as 64-byte lines
+// with a swizzle, weights as the packed form has them, so that neither read
+// meets a bank conflict. How many rows a tile has is known on the device only:
+// there is a body for 128, 192 and 256, and 256 blocks, one to a CU, go through
+// the list of tiles by themselves.
 #include "experts_device.h"
 #include "lds_device.h"
 
@@ -237,123 +232,19 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
   __syncthreads();  // before the next tile's loads to LDS
 }
 
-// Up to 64 rows by four column tiles.
-template <typename T, bool Gated>
-__device__ __forceinline__ void mid(const ProductArgs& p, char* smem, const Item& it, int tile0) {
-  typedef typename T::raw raw;
-  constexpr int C = kMidCols, RT = kMidRows / 16, kPitch = 16 * C + 4;
-  typedef int32_t Slab[kWaves][16][kPitch];
-  Slab* slabs = reinterpret_cast<Slab*>(smem);  // one of 16 rows for each turn
-  static_assert(RT * sizeof(Slab) <= kLds, "LDS");
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, m = lane & 15;
-  const int tiles = packed_tiles<Gated>(p);
-  const int count = p.blocks > wave ? (p.blocks - wave + kWaves - 1) / kWaves : 0;
-
-  const uint8_t* w[C];
-  const int8_t* q[RT];
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-    q[r] = p.q + ((int64_t)token_of(p, it.row + min(16 * r + m, it.rows - 1)) * p.blocks + wave) * kBlockRed + 16 * g;
-#pragma unroll
-  for (int c = 0; c < C; ++c)
-    w[c] = packed_tile(p, it.expert, tiles, min(tile0 + c, tiles - 1)) + (int64_t)wave * kBlockBytes + 16 * lane;
-  // a thread ends four columns of one row of every slab that it has a part in
-  constexpr int kOut = Gated ? 2 * C : 4 * C;           // groups of 4 output columns
-  constexpr int kSlabs = kWave * kWaves / (16 * kOut);  // at once
-  const int o = threadIdx.x % kOut, sr = threadIdx.x / kOut % 16, s0 = threadIdx.x / (16 * kOut);
-  float step[RT / kSlabs];
-#pragma unroll
-  for (int i = 0; i < RT / kSlabs; ++i)
-    step[i] = p.step[token_of(p, it.row + min(16 * (s0 + kSlabs * i) + sr, it.rows - 1))];
-  struct Step {
-    u32x4 w[C], x[RT];
-  };
-  auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
-#pragma unroll
-    for (int c = 0; c < C; ++c) d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes);
-#pragma unroll
-    for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
-  };
-  static_assert(RT / kSlabs <= 2, "");
-  i32x4 acc[RT][C] = {};
-  auto multiply = [&](const Step& d) __attribute__((always_inline)) {
-#pragma unroll
-    for (int r = 0; r < RT; ++r)
-#pragma unroll
-      for (int c = 0; c < C; ++c) acc[r][c] = mfma(d.w[c], d.x[r], acc[r][c]);
-  };
-  if (count > 0) {
-    Step d0, d1;
-    fetch(d0, 0);
-    int i = 0;
-#pragma unroll 1
-    for (; i + 2 < count; i += 2) {
-      fetch(d1, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d0);
-      fetch(d0, i + 2);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d1);
-    }
-    if (i + 1 < count) {
-      fetch(d1, i + 1);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(d0);
-      multiply(d1);
-    } else {
-      multiply(d0);
-    }
-  }
-  const int col = (Gated ? tile0 / 2 : tile0) * 16 + 4 * o, from = 4 * (Gated ? o / 4 * 8 + o % 4 : o);
-  const Columns<T, Gated, 4> k(p, it.expert, col);
-#pragma unroll
-  for (int r = 0; r < RT; ++r)
-#pragma unroll
-    for (int c = 0; c < C; ++c) *reinterpret_cast<i32x4*>(&slabs[r][wave][m][16 * c + 4 * g]) = acc[r][c];
-  __syncthreads();
-  with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
-#pragma unroll 1
-    for (int i = 0; i < RT / kSlabs; ++i) {
-      const int r = s0 + kSlabs * i, local = 16 * r + sr;
-      if (local >= it.rows || col >= p.n) continue;
-      const int64_t row = it.row + local;
-      float residual[4] = {};
-      if (!Gated && p.residual != nullptr)
-        block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + row * p.ldr + col, residual, p.n - col);
-      i32x4 v = {}, u = {};
-#pragma unroll
-      for (int x = 0; x < kWaves; ++x) {
-        v += *reinterpret_cast<const i32x4*>(&slabs[r][x][sr][from]);
-        if constexpr (Gated) u += *reinterpret_cast<const i32x4*>(&slabs[r][x][sr][from + 16]);
-      }
-      float sum[4], up[4];
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        sum[t] = (float)v[t];
-        up[t] = (float)u[t];
-      }
-      finish<T, Gated, decltype(act)::value, 4>(p, k, (int)row, col, i == 0 ? step[0] : step[RT / kSlabs - 1], sum,
-                                                up, residual);
-    }
-  });
-  __syncthreads();  // before the next item's sums or loads
-}
-
 template <typename T, bool Gated>
 __global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void tile_kernel(ProductArgs p, int dense_mid) {
+void tile_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const bool listed = p.lists.counts != nullptr;
-  const int tiles = packed_tiles<Gated>(p);
-  const int ntiles = (tiles + kTileCols - 1) / kTileCols, groups = (tiles + kMidCols - 1) / kMidCols;
-  const int mids = listed ? p.lists.counts[1] : dense_mid ? (p.rows + kMidRows - 1) / kMidRows : 0;
-  const int mtiles = listed ? p.lists.counts[2] : dense_mid ? 0 : (p.rows + kTileRows - 1) / kTileRows;
+  const int ntiles = (packed_tiles<Gated>(p) + kTileCols - 1) / kTileCols;
+  const int mtiles = listed ? p.lists.counts[2] : (p.rows + kTileRows - 1) / kTileRows;
+  const int64_t total = (int64_t)mtiles * ntiles;
   // Blocks are dealt round-robin over the 8 XCDs: each XCD has a contiguous
-  // range of either kind, which its blocks go through in turn.
-  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3, slot = blockIdx.x >> 3;
-  const int64_t total = (int64_t)mtiles * ntiles, begin = total * xcd / 8, end = total * (xcd + 1) / 8;
-  for (int64_t at = begin + slot; at < end; at += per) {
+  // range of tiles, which its blocks go through in turn.
+  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
+  const int64_t end = total * (xcd + 1) / 8;
+  for (int64_t at = total * xcd / 8 + (blockIdx.x >> 3); at < end; at += per) {
     // row tiles of an expert in groups of 8, column by column
     const Item it = listed ? p.lists.tiles[at / ntiles] : Item{0, 0, p.rows, 0};
     const int high = (it.rows + kTileRows - 1) / kTileRows;  // its row tiles
@@ -363,48 +254,20 @@ void tile_kernel(ProductArgs p, int dense_mid) {
     const int height = min(((it.rows + high - 1) / high + 31) / 32 * 32, kTileRows);
     const int mt = 8 * group + in % gm, nt = in / gm;
     const int row0 = it.row + mt * height, rows = min(height, it.rows - mt * height);
-    if (rows <= 128)
+    if (rows <= 64)
+      tile<T, Gated, 2>(p, smem, it.expert, row0, rows, nt * kTileCols);
+    else if (rows <= 128)
       tile<T, Gated, 4>(p, smem, it.expert, row0, rows, nt * kTileCols);
     else if (rows <= 192)
       tile<T, Gated, 6>(p, smem, it.expert, row0, rows, nt * kTileCols);
     else
       tile<T, Gated, 8>(p, smem, it.expert, row0, rows, nt * kTileCols);
   }
-  // Blocks that had a tile less first take the four mid items it is worth.
-  const int64_t all = (int64_t)mids * groups, first = all * xcd / 8, last = all * (xcd + 1) / 8;
-  const int more = (int)((end - begin) % per), less = per - more;
-  const int64_t extra = more != 0 ? 4 * less : 0;
-  const int64_t count = last - first;
-  const bool light = more != 0 && slot >= more;
-  for (int64_t j = light ? slot - more : extra + slot; j < count;) {
-    const int64_t at = first + j;
-    // row tiles of a column group next to each other share its weights
-    Item it;
-    int group;
-    if (listed) {
-      it = p.lists.mid[at / groups];
-      group = (int)(at % groups);
-    } else {
-      const int r = (int)(at % mids);
-      group = (int)(at / mids);
-      it = Item{0, r * kMidRows, min(p.rows - r * kMidRows, kMidRows), 0};
-    }
-    mid<T, Gated>(p, smem, it, group * kMidCols);
-    if (j < extra) {
-      j += less;
-      if (j >= extra) j = extra + slot;
-    } else {
-      j += per;
-    }
-  }
 }
 
 template <typename T, bool Gated>
 static hipError_t launch_typed(const ProductArgs& p, hipStream_t stream) {
-  const bool dense_mid = p.rows <= kMidRows || all_mid((p.rows + kMidRows - 1) / kMidRows,
-                                                       (p.rows + kTileRows - 1) / kTileRows,
-                                                       (Gated ? 2 : 1) * column_tiles(p.n), p.blocks);
-  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p, (int)dense_mid);
+  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p);
 }
 
 hipError_t launch_tiles(int dtype, const ProductArgs& p, hipStream_t stream) {
