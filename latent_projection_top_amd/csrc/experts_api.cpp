@@ -119,7 +119,7 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.experts = c.experts;
   a.offsets = offsets;
   if (experts::is_fused(rows, c.experts, offsets != nullptr))
-    return status_of(experts::launch_stream(c.dtype, a, true, 0, s));
+    return status_of(experts::launch_stream(c.dtype, a, true, s));
   experts::QuantiseArgs z{};
   z.x = a.x;
   z.ldx = x_stride;
@@ -134,22 +134,21 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.rows = rows;
   z.column_tiles = planes * experts::column_tiles(c.outputs);
   z.blocks = a.blocks;
+  // (by expert: mid items as many, and tiles as few, as there can be)
+  z.few = rows > experts::kStreamRows &&
+          experts::is_few(offsets != nullptr ? experts::most_mid(rows, c.experts)
+                                             : (rows + experts::kMidRows - 1) / experts::kMidRows,
+                          (rows + experts::kTileRows - 1) / experts::kTileRows, z.column_tiles, a.blocks,
+                          offsets != nullptr);
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);
   z.most_tiles = (int)experts::most_tiles(rows, c.experts);
   if (int st = status_of(experts::launch_quantise(c.dtype, z, s))) return st;
-  if (offsets == nullptr) {
-    if (rows <= experts::kStreamRows)
-      return status_of(experts::launch_stream(c.dtype, a, false, experts::kStreamRows, s));
-    if (experts::all_mid((rows + experts::kMidRows - 1) / experts::kMidRows,
-                         (rows + experts::kTileRows - 1) / experts::kTileRows, z.column_tiles, a.blocks))
-      return status_of(experts::launch_stream(c.dtype, a, false, experts::kMidRows, s));
-    return status_of(experts::launch_tiles(c.dtype, a, s));
-  }
   // how many rows an expert has is known on the device only: both kernels go
-  // through their lists
-  if (int st = status_of(experts::launch_stream(c.dtype, a, false, 0, s))) return st;
-  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, s)) : ROUTE_OK;
+  // through their lists, unless there can be nothing on one of them
+  if (!z.few && (offsets != nullptr || rows <= experts::kStreamRows))
+    if (int st = status_of(experts::launch_stream(c.dtype, a, false, s))) return st;
+  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, z.few != 0, s)) : ROUTE_OK;
 }
 
 int run_quantize(const Product8& c, const void* w, int8_t* w8, float* scale, void* stream) {

@@ -46,6 +46,7 @@ __device__ __forceinline__ void load_scales(const float* s, float (&v)[C], int c
 template <typename T, bool Gated, int C>
 struct Columns {
   float scale[C], other[C];  // other: the up product's scale, or the bias
+  Columns() = default;
   __device__ __forceinline__ Columns(const ProductArgs& p, int expert, int col) {
     const int count = p.n - col;
     const int64_t at = (int64_t)expert * p.n + col;

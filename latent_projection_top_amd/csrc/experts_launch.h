@@ -57,15 +57,15 @@ constexpr int kBlockRed = 64, kBlockBytes = 1024;
 inline int red_blocks(int k) { return (k + kBlockRed - 1) / kBlockRed; }
 inline int column_tiles(int n) { return (n + 15) / 16; }
 
-// The rows of one expert in a product: up to kStreamRows of them (`brief`), or
-// one of its row tiles, all of a product of up to kMidRows rows (`mid`) or the
-// first-th and later of up to kTileRows (`tiles`, an entry for each; `rows` is
-// of all of them).
+// The rows of one expert in a product. Where there are many in all: up to
+// kStreamRows of them (`brief`), or its first-th and later row tiles of up to
+// kTileRows (`tiles`, an entry for each; `rows` is of all of them). Where there
+// are few: row tiles of up to kMidRows (`mid`).
 struct Item {
   int32_t expert, row, rows, first;
 };
 constexpr int kStreamRows = 32, kMidRows = 64, kTileRows = 256;
-constexpr int kMidCols = 4, kTileCols = 16;  // packed column tiles of 16 each takes
+constexpr int kMidCols = 4, kTileCols = 16;  // packed column tiles of 16 that each takes
 struct Lists {
   const int32_t* counts;  // brief, mid, tiles; NULL: one expert has every row
   const Item* brief;
@@ -73,12 +73,11 @@ struct Lists {
   const Item* tiles;
 };
 inline int64_t most_brief(int64_t rows, int experts) { return rows < experts ? rows : experts; }
-inline int64_t most_long(int64_t rows, int experts, int height) {
+inline int64_t most_mid(int64_t rows, int experts) { return rows / kMidRows + most_brief(rows, experts); }
+inline int64_t most_tiles(int64_t rows, int experts) {
   const int64_t n = rows / (kStreamRows + 1);
-  return rows / height + (n < experts ? n : experts);
+  return rows / kTileRows + (n < experts ? n : experts);
 }
-inline int64_t most_mid(int64_t rows, int experts) { return most_long(rows, experts, kMidRows); }
-inline int64_t most_tiles(int64_t rows, int experts) { return most_long(rows, experts, kTileRows); }
 inline size_t list_bytes(int64_t rows, int experts) {
   return sizeof(Item) *
          (size_t)(1 + most_brief(rows, experts) + most_mid(rows, experts) + most_tiles(rows, experts));
@@ -89,15 +88,19 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
   return Lists{&items->expert, items + 1, mid, mid + most_mid(rows, experts)};
 }
 
-// Whether a product's long experts, `mids` row tiles by one height and `tiles`
-// by the other, go as row tiles of kMidRows altogether. Modelled times in us:
-// a mid item's is mostly latency, until their operands, 8 KB for each block of
-// the reduction, keep the L2s busy (8 TB/s); tiles come in rounds of 256.
-__host__ __device__ inline bool all_mid(int64_t mids, int64_t tiles, int column_tiles, int blocks) {
+// Whether a product of more than kStreamRows rows goes as mid items: `mids` of
+// them at most, or `tiles` row tiles at least. Modelled times in us. A mid item's
+// is mostly latency; many wait for each other, 256 at a time, or for their
+// operands, 8 KB for each block of the reduction, which the L2s deliver at 8
+// TB/s. Tiles come in rounds of 256; by expert they are a second launch after
+// the brief items'.
+inline bool is_few(int64_t mids, int64_t tiles, int column_tiles, int blocks, bool offsets) {
   const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
   const int64_t t = tiles * ((column_tiles + kTileCols - 1) / kTileCols);
-  const float latency = 6.f + 0.1f * (float)blocks, busy = (float)m * (float)blocks * 0.001f;
-  return (latency > busy ? latency : busy) < (float)((t + 255) / 256) * (6.f + 0.6f * (float)blocks);
+  const double step = (double)blocks;
+  const double busy = (double)m * step * 0.001, rounds = (double)((m + 255) / 256) * (3.0 + 0.1 * step);
+  return 3.0 + (busy > rounds ? busy : rounds) <
+         (double)((t + 255) / 256) * (6.0 + 0.6 * step) + (offsets ? 8.0 + 0.1 * step : 0.0);
 }
 
 // The most rows of a product that makes the integers by itself: of an item, and
@@ -110,7 +113,7 @@ inline bool is_fused(int64_t rows, int experts, bool offsets) {
 // What the streaming kernel uses of the workspace: counters of its column
 // groups, zero between calls, 64 bytes apart, and split sums, a unit of them
 // for each block.
-constexpr int kSplitUnits = 256, kUnitInts = kMidRows * 16 * kMidCols;
+constexpr int kSplitUnits = 256, kUnitInts = kStreamRows * 64;
 static_assert(kSplitUnits * 64 <= EXPERTS_WORKSPACE_ZEROED, "what the caller clears");
 constexpr size_t kPartialBytes = (size_t)kSplitUnits * kUnitInts * 4;
 
@@ -141,13 +144,14 @@ struct QuantiseArgs {
   Item* area;
   int64_t ldx;
   int tokens, k, stride, experts, rows, column_tiles, blocks;
+  int few;  // the list is of mid items alone
   int most_brief, most_mid, most_tiles;
 };
 hipError_t launch_quantise(int dtype, const QuantiseArgs& args, hipStream_t stream);
-// Brief and mid items; without offsets, items of `dense` rows (0: none).
-hipError_t launch_stream(int dtype, const ProductArgs& args, bool fused, int dense, hipStream_t stream);
-// Tiles; without offsets, of every row.
-hipError_t launch_tiles(int dtype, const ProductArgs& args, hipStream_t stream);
+// Brief items (without offsets every row, of kStreamRows at most).
+hipError_t launch_stream(int dtype, const ProductArgs& args, bool fused, hipStream_t stream);
+// Tiles and mid items (without offsets every row, as either).
+hipError_t launch_tiles(int dtype, const ProductArgs& args, bool few, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,
                        hipStream_t stream);

@@ -12,62 +12,41 @@ using block::u32x4;
 
 constexpr int kThreads = 256;
 
-// The lists of a product's items, by the first four waves of a block. Up to
-// kStreamRows rows of an expert are one brief item. More are row tiles: in all
-// of the product mid items, or as few tiles of at most kTileRows as there can be,
-// of equal height.
+// The lists of a product's items, by the first four waves of a block. An
+// expert's rows are as few tiles of at most kTileRows as there can be, of equal
+// height.
 __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
   __shared__ int4 part[kThreads / kWave];
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
   Item* lists[3] = {p.area + 1, p.area + 1 + p.most_brief, p.area + 1 + p.most_brief + p.most_mid};
   const int most[3] = {p.most_brief, p.most_mid, p.most_tiles};
-  auto rows_of = [&](int e, int& first) __attribute__((always_inline)) {
-    first = 0;
-    if (t >= kThreads || e >= p.experts) return 0;
-    first = min(max(p.offsets[e], 0), p.rows);
-    return max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
-  };
-  // sums over the block, and before this thread
-  auto scan = [&](int4 v, int4& before) __attribute__((always_inline)) {
-    int4 r = v;
+  int4 done = {0, 0, 0, 0};
+  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
+    const int e = e0 + t;
+    int first = 0, n = 0;
+    if (t < kThreads && e < p.experts) {
+      first = min(max(p.offsets[e], 0), p.rows);
+      n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
+    }
+    // this thread's items: how many, of which list
+    const int kind = p.few ? 1 : n <= kStreamRows ? 0 : 2;
+    const int height = kind == 0 ? kStreamRows : kind == 1 ? kMidRows : kTileRows;
+    const int m = (n + height - 1) / height;
+    // sums over the block, and before this thread
+    int4 r = {kind == 0 ? m : 0, kind == 1 ? m : 0, kind == 2 ? m : 0, 0}, before = r, all = {0, 0, 0, 0};
     for (int d = 1; d < kWave; d *= 2) {
       const int x = __shfl_up(r.x, d), y = __shfl_up(r.y, d), z = __shfl_up(r.z, d);
       if (lane >= d) r = int4{r.x + x, r.y + y, r.z + z, 0};
     }
     if (t < kThreads && lane == kWave - 1) part[wave] = r;
     __syncthreads();
-    before = int4{r.x - v.x, r.y - v.y, r.z - v.z, 0};
-    int4 all = {0, 0, 0, 0};
+    before = int4{r.x - before.x, r.y - before.y, r.z - before.z, 0};
     for (int w = 0; w < kThreads / kWave; ++w) {
       const int4 s = part[w];
       if (w < wave) before = int4{before.x + s.x, before.y + s.y, before.z + s.z, 0};
       all = int4{all.x + s.x, all.y + s.y, all.z + s.z, 0};
     }
     __syncthreads();
-    return all;
-  };
-  int64_t mids = 0, tiles = 0;
-  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
-    int first;
-    const int n = rows_of(e0 + t, first);
-    int4 before;
-    const int4 all = scan(n > kStreamRows ? int4{0, (n + kMidRows - 1) / kMidRows, (n + kTileRows - 1) / kTileRows, 0}
-                                          : int4{0, 0, 0, 0}, before);
-    mids += all.y;
-    tiles += all.z;
-  }
-  const int long_kind = all_mid(mids, tiles, p.column_tiles, p.blocks) ? 1 : 2;
-  int4 done = {0, 0, 0, 0};
-  for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
-    const int e = e0 + t;
-    int first;
-    const int n = rows_of(e, first);
-    // this thread's items: how many, of which list
-    const int kind = n <= kStreamRows ? 0 : long_kind;
-    const int m = n == 0 ? 0 : kind == 0 ? 1 : kind == 1 ? (n + kMidRows - 1) / kMidRows
-                                                        : (n + kTileRows - 1) / kTileRows;
-    int4 before;
-    const int4 all = scan(int4{kind == 0 ? m : 0, kind == 1 ? m : 0, kind == 2 ? m : 0, 0}, before);
     const int start = kind == 0 ? done.x + before.x : kind == 1 ? done.y + before.y : done.z + before.z;
     // offsets that overlap would make more than there is room for
     if (m == 1 && start < most[kind]) lists[kind][start] = Item{e, first, n, start};

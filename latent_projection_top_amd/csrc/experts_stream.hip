@@ -1,16 +1,15 @@
-// 8-bit products of few rows of an expert: the time is the weights' way from
-// HBM, or, where there are few weights, the steps one after another.
+// 8-bit products of few rows (up to 32 of an expert): the time is the weights'
+// way from HBM.
 //
-// A block has up to 32 rows of one expert and four column tiles of its packed
-// weights, or up to 64 rows and two. Its eight waves take the reduction's blocks
-// of 64 in turn, 1 KB of a column tile per load, straight into the registers
-// that the matrix cores read; the next blocks' loads are under way while one is
-// multiplied. The waves' integer sums meet in LDS. 512 blocks, two to a CU, so
-// that one's sums meet while the other's weights arrive, go through the lists of
-// items by themselves, since only the device knows how long they are. Where
-// that is too little to fill the CUs and the reduction is long, it is also split
-// over blocks, whose sums are added by the last of them to arrive: integers, so
-// in any order the same.
+// A block has one expert's rows and four column tiles of its packed weights.
+// Its eight waves take the reduction's blocks of 64 in turn, 1 KB of a column
+// tile per load, straight into the registers that the matrix cores read; the
+// next blocks' loads are under way while one is multiplied. The waves' integer
+// sums meet in LDS. 512 blocks, two to a CU, so that one's sums meet while the
+// other's weights arrive, go through the list of items by themselves, since only
+// the device knows how long it is. Where that is too little to fill the CUs and
+// the reduction is long, it is also split over blocks, whose sums are added by
+// the last of them to arrive: integers, so in any order the same.
 //
 // For few rows in all (Fused) the kernel reads the rows as they are and makes
 // the integers itself: each wave those of its own blocks of the reduction, after
@@ -62,7 +61,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
                                             int splits, Shared& shared) {
   typedef typename T::raw raw;
   constexpr int kPitch = 16 * C + 4;
-  typedef int32_t Part[16 * (RT < 2 ? RT : 2)][kPitch];
+  typedef int32_t Part[16 * RT][kPitch];
   Part* part = reinterpret_cast<Part*>(shared.part);
   static_assert(sizeof(Part) * kWaves <= sizeof(Shared::part), "LDS");
   // (not the same register as in the item before: what is made of it would
@@ -121,6 +120,25 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     fetch_x(d, i);
   };
 
+  // A thread ends four columns of one row. What it needs for that is on its way
+  // with the first operands, or after the last, where registers are short.
+  constexpr int kQuads = 4 * C, kOut = Gated ? 2 * C : 4 * C;  // groups of 4 packed and output columns
+  static_assert(16 * RT * kQuads <= kThreads, "");
+  int row, col, quad;
+  Columns<T, Gated, 4> k;
+  float step = 0.f;
+  auto fetch_ends = [&]() __attribute__((always_inline)) {
+    asm volatile("" : "+v"(tid));
+    const int o = tid % kOut;
+    row = tid / kOut;
+    col = (Gated ? tile0 / 2 : tile0) * 16 + 4 * o;
+    quad = Gated ? o / 4 * 8 + o % 4 : o;
+    k = Columns<T, Gated, 4>(p, it.expert, col);
+    if constexpr (!Fused) step = p.step[token_of(p, it.row + min(row, it.rows - 1))];
+  };
+  constexpr bool kRoom = C == 2;  // registers for them meanwhile
+  if (kRoom) fetch_ends();
+
   Quantiser z[Fused ? RT : 1];
   i32x4 acc[C][RT] = {};
   auto multiply = [&](const Step& d) __attribute__((always_inline)) {
@@ -136,7 +154,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     }
   };
   // Depth steps are on their way at once, as many as there are registers for.
-  constexpr int kDepth = RT > 2 ? 1 : C == 2 ? 4 : RT == 1 ? 3 : 2;
+  constexpr int kDepth = C == 2 ? 4 : RT == 1 ? 3 : 2;
   Step d[kDepth];
   if constexpr (Fused) {
     // The rows' largest magnitudes: of this wave's blocks (of all of them, also
@@ -201,98 +219,77 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     for (int s = 0; s < kDepth; ++s)
       if (i + s < count) {
         multiply(d[s]);
+        __builtin_amdgcn_sched_barrier(0);
         if (i + s + kDepth < count) fetch(d[s], i + s + kDepth);
       }
 
-  // lane (g, m) holds row 16 r + m, columns 16 c + 4 g .. + 3. The waves' sums
-  // meet in LDS, at most 32 rows at a time; a thread ends four columns of a row.
-  // Where the reduction is split they go to memory instead, and the last block
-  // to arrive ends all rows, in one more turn.
-  constexpr int kAtOnce = RT < 2 ? RT : 2, kTurns = RT / kAtOnce;
-  constexpr int kQuads = 4 * C, kOut = Gated ? 2 * C : 4 * C;  // groups of 4 packed and output columns
+  if (!kRoom) fetch_ends();
+  // lane (g, m) holds row 16 r + m, columns 16 c + 4 g .. + 3
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int r = 0; r < RT; ++r) *reinterpret_cast<i32x4*>(&part[wave][16 * r + m][16 * c + 4 * g]) = acc[c][r];
+  __syncthreads();
+  auto sums = [&](int row, int quad) __attribute__((always_inline)) {
+    i32x4 v = {};
+#pragma unroll
+    for (int x = 0; x < kWaves; ++x) v += *reinterpret_cast<const i32x4*>(&part[x][row][4 * quad]);
+    return v;
+  };
+  bool mine = row < it.rows && col < p.n;
   int32_t* units = p.partial + (int64_t)unit * splits * kUnitInts;
-#pragma unroll 1
-  for (int h = 0; h < (splits > 1 ? kTurns + 1 : kTurns); ++h) {
-    int row0 = 16 * kAtOnce * h, row1 = min(row0 + 16 * kAtOnce, it.rows);
-    if (h < kTurns) {
+  if (splits > 1) {
+    if (tid < it.rows * kQuads) {
+      const i32x4 v = sums(tid / kQuads, tid % kQuads);
 #pragma unroll
-      for (int x = 0; x < kTurns; ++x)
-        if (h == x)
-#pragma unroll
-          for (int c = 0; c < C; ++c)
-#pragma unroll
-            for (int r = 0; r < kAtOnce; ++r)
-              *reinterpret_cast<i32x4*>(&part[wave][16 * r + m][16 * c + 4 * g]) = acc[c][kAtOnce * x + r];
-      __syncthreads();
-    } else {
-      asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
-      __syncthreads();
-      if (tid == 0) {
-        uint32_t* c = p.counters + 16 * unit;
-        shared.arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        if (shared.arrived == (uint32_t)splits - 1)
-          __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      }
-      __syncthreads();
-      row0 = 0;
-      row1 = shared.arrived == (uint32_t)splits - 1 ? it.rows : 0;
+      for (int t = 0; t < 4; ++t) put(units + (int64_t)split * kUnitInts + 4 * tid + t, v[t]);
     }
-    auto sums = [&](int row, int quad) __attribute__((always_inline)) {
-      i32x4 v = {};
-#pragma unroll
-      for (int k = 0; k < kWaves; ++k) v += *reinterpret_cast<const i32x4*>(&part[k][row - row0][4 * quad]);
-      return v;
-    };
-    if (h < kTurns && splits > 1) {
-      for (int id = kQuads * row0 + tid; id < kQuads * row1; id += kThreads) {
-        const i32x4 v = sums(id / kQuads, id % kQuads);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) put(units + (int64_t)split * kUnitInts + 4 * id + t, v[t]);
-      }
-      row1 = row0;
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's sums are out
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t* c = p.counters + 16 * unit;
+      shared.arrived = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (shared.arrived == (uint32_t)splits - 1)
+        __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
-    auto sum_of = [&](int row, int quad) __attribute__((always_inline)) {
-      if (splits == 1) return sums(row, quad);
-      i32x4 v = {};
+    __syncthreads();
+    mine = mine && shared.arrived == (uint32_t)splits - 1;
+  }
+  if (mine) {
+    const int64_t r = it.row + row;
+    if constexpr (Fused) {
+      uint32_t a = 0;
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) a = max(a, shared.most[x][row]);
+      step = Quantiser(magnitude<T>(a)).s;
+    }
+    float residual[4] = {};
+    if (!Gated && p.residual != nullptr)
+      block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + r * p.ldr + col, residual, p.n - col);
+    i32x4 v = {}, u = {};
+    if (splits > 1) {
+      const int32_t* from = units + 4 * (row * kQuads + quad);
       for (int s = 0; s < splits; ++s)
 #pragma unroll
-        for (int t = 0; t < 4; ++t) v[t] += get(units + (int64_t)s * kUnitInts + 4 * (row * kQuads + quad) + t);
-      return v;
-    };
-    const int out0 = (Gated ? tile0 / 2 : tile0) * 16;
-#pragma unroll 1
-    for (int id = tid; id < (row1 - row0) * kOut; id += kThreads) {
-      const int row = row0 + id / kOut, o = id % kOut, col = out0 + 4 * o;
-      if (col >= p.n) continue;
-      const int quad = Gated ? o / 4 * 8 + o % 4 : o;
-      const int64_t r = it.row + row;
-      const Columns<T, Gated, 4> k(p, it.expert, col);
-      float step;
-      if constexpr (Fused) {
-        uint32_t a = 0;
-#pragma unroll
-        for (int x = 0; x < kWaves; ++x) a = max(a, shared.most[x][row]);
-        step = Quantiser(magnitude<T>(a)).s;
-      } else {
-        step = p.step[token_of(p, (int)r)];
-      }
-      float sum[4], up[4] = {}, residual[4] = {};
-      if (!Gated && p.residual != nullptr)
-        block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + r * p.ldr + col, residual, p.n - col);
-      const i32x4 v = sum_of(row, quad);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) sum[t] = (float)v[t];
-      if constexpr (Gated) {
-        const i32x4 u = sum_of(row, quad + 4);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) up[t] = (float)u[t];
-      }
-      with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
-        finish<T, Gated, decltype(act)::value, 4>(p, k, (int)r, col, step, sum, up, residual);
-      });
+        for (int t = 0; t < 4; ++t) {
+          v[t] += get(from + (int64_t)s * kUnitInts + t);
+          if constexpr (Gated) u[t] += get(from + (int64_t)s * kUnitInts + 16 + t);
+        }
+    } else {
+      v = sums(row, quad);
+      if constexpr (Gated) u = sums(row, quad + 4);
     }
-    __syncthreads();  // before the next sums
+    float sum[4], up[4];
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      sum[t] = (float)v[t];
+      up[t] = (float)u[t];
+    }
+    with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
+      finish<T, Gated, decltype(act)::value, 4>(p, k, (int)r, col, step, sum, up, residual);
+    });
   }
+  __syncthreads();  // before the next item's sums
 }
 
 // How many blocks share a unit of work: parts of at least four steps of a wave,
@@ -301,36 +298,23 @@ __device__ __forceinline__ int splits_of(int64_t units, int blocks) {
   return units == 0 || units >= kSplitUnits / 2 ? 1 : max(1, min(kSplitUnits / (int)units, blocks / (4 * kWaves)));
 }
 
-// Items of up to 32 rows by C column tiles, and of up to 64 rows by two.
-// (dense: one expert has every row, in items of this many)
 template <typename T, bool Gated, int C>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
-void stream_kernel(ProductArgs p, int dense) {
+void stream_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(16))) Shared shared;
-  const int tiles = packed_tiles<Gated>(p), wide = (tiles + C - 1) / C, narrow = (tiles + kMidCols - 1) / kMidCols;
+  const int groups = (packed_tiles<Gated>(p) + C - 1) / C;
   const bool listed = p.lists.counts != nullptr;
-  const int dense_items = dense > 0 ? (p.rows + dense - 1) / dense : 0;
-  const int briefs = listed ? p.lists.counts[0] : dense <= kStreamRows ? dense_items : 0;
-  const int mids = listed ? p.lists.counts[1] : dense_items - briefs;
-  const int64_t first = (int64_t)briefs * wide, total = first + (int64_t)mids * narrow;
+  const int64_t total = (int64_t)(listed ? p.lists.counts[0] : 1) * groups;
   const int splits = splits_of(total, p.blocks);
   for (int64_t at = blockIdx.x; at < total * splits; at += gridDim.x) {
     const int64_t u = at / splits;
     const int split = (int)(at - u * splits);  // (more than one: u < kSplitUnits / 2)
-    if (u < first) {
-      const int i = (int)(u / wide), tile0 = (int)(u - (int64_t)i * wide) * C;
-      const Item it = listed ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
-      if (it.rows <= 16)
-        stream_item<T, Gated, C, 1, false, true>(p, it, tile0, (int)u, split, splits, shared);
-      else
-        stream_item<T, Gated, C, 2, false, true>(p, it, tile0, (int)u, split, splits, shared);
-    } else {
-      const int64_t v = u - first;
-      // row tiles of the same columns next to each other
-      const int i = (int)(listed ? v / narrow : v % mids), tile0 = (int)(listed ? v % narrow : v / mids) * kMidCols;
-      const Item it = listed ? p.lists.mid[i] : Item{0, i * dense, min(p.rows - i * dense, dense), 0};
-      stream_item<T, Gated, kMidCols, 4, false, true>(p, it, tile0, (int)u, split, splits, shared);
-    }
+    const int i = (int)(u / groups), tile0 = (int)(u - (int64_t)i * groups) * C;
+    const Item it = listed ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
+    if (it.rows <= 16)
+      stream_item<T, Gated, C, 1, false, true>(p, it, tile0, (int)u, split, splits, shared);
+    else
+      stream_item<T, Gated, C, 2, false, true>(p, it, tile0, (int)u, split, splits, shared);
   }
 }
 
@@ -387,7 +371,7 @@ void fused_kernel(ProductArgs p) {
 
 // Two blocks to a CU; four column tiles to each unless that leaves CUs idle.
 template <typename T, bool Gated>
-static hipError_t launch_typed(const ProductArgs& p, bool fused, int dense, hipStream_t stream) {
+static hipError_t launch_typed(const ProductArgs& p, bool fused, hipStream_t stream) {
   const int64_t tiles = (Gated ? 2 : 1) * column_tiles(p.n);
   const int64_t items = p.offsets != nullptr ? most_brief(p.rows, p.experts) : 1;
   const dim3 grid(512), block(kThreads);
@@ -398,16 +382,15 @@ static hipError_t launch_typed(const ProductArgs& p, bool fused, int dense, hipS
   if (fused)
     return launch_kernel(narrow ? fused_kernel<T, Gated, 2, false> : fused_kernel<T, Gated, 4, false>, grid, block,
                          stream, p);
-  return launch_kernel(narrow ? stream_kernel<T, Gated, 2> : stream_kernel<T, Gated, 4>, grid, block, stream, p,
-                       dense);
+  return launch_kernel(narrow ? stream_kernel<T, Gated, 2> : stream_kernel<T, Gated, 4>, grid, block, stream, p);
 }
 
-hipError_t launch_stream(int dtype, const ProductArgs& p, bool fused, int dense, hipStream_t stream) {
+hipError_t launch_stream(int dtype, const ProductArgs& p, bool fused, hipStream_t stream) {
   if (dtype == BLOCK_BF16)
-    return p.gated ? launch_typed<BF16, true>(p, fused, dense, stream)
-                   : launch_typed<BF16, false>(p, fused, dense, stream);
-  return p.gated ? launch_typed<F16, true>(p, fused, dense, stream)
-                 : launch_typed<F16, false>(p, fused, dense, stream);
+    return p.gated ? launch_typed<BF16, true>(p, fused, stream)
+                   : launch_typed<BF16, false>(p, fused, stream);
+  return p.gated ? launch_typed<F16, true>(p, fused, stream)
+                 : launch_typed<F16, false>(p, fused, stream);
 }
 
 }  // namespace experts

@@ -1,15 +1,21 @@
-// 8-bit products of more than 64 rows of an expert, on
-// v_mfma_i32_16x16x64_i8: up to 256 rows by 256 columns of the packed weights
-// (for the gated product 128 output columns, gate and up alternating by 16).
+// 8-bit products of more than 32 rows of an expert, or of many experts with few,
+// on v_mfma_i32_16x16x64_i8. How many rows an expert has is known on the device
+// only: 256 blocks, one to a CU, go through the lists of items by themselves.
 //
-// Eight waves, two by four, have half of the rows and a quarter of the columns
-// each. The reduction runs in stages of 64, one MFMA deep, through a ring of
-// LDS buffers: one is read into registers while the one before is multiplied,
-// the others are on their way from memory. Rows lie in LDS as 64-byte lines
-// with a swizzle, weights as the packed form has them, so that neither read
-// meets a bank conflict. How many rows a tile has is known on the device only:
-// there is a body for 128, 192 and 256, and 256 blocks, one to a CU, go through
-// the list of tiles by themselves.
+// tiles: up to 256 rows by 256 columns of the packed weights (for the gated
+// product 128 output columns, gate and up alternating by 16). Eight waves, two
+// by four, have half of the rows and a quarter of the columns each. The
+// reduction runs in stages of 64, one MFMA deep, through a ring of LDS buffers:
+// one is read into registers while the one before is multiplied, the others are
+// on their way from memory. Rows lie in LDS as 64-byte lines with a swizzle,
+// weights as the packed form has them, so that neither read meets a bank
+// conflict. There is a body for 64, 128, 192 and 256 rows.
+//
+// mid items, where there are few tiles: up to 64 rows by 64 columns, the
+// reduction dealt to the eight waves, whose operands come straight from memory
+// and whose sums meet in LDS: half of the matrix cores' rate at best, but an
+// eighth of the steps one after another, which is what the time is made of
+// there. The next item's first operands are on their way while one ends.
 #include "experts_device.h"
 #include "lds_device.h"
 
@@ -232,17 +238,145 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
   __syncthreads();  // before the next tile's loads to LDS
 }
 
+// A block's mid items, `at(j)` the j-th, which ends where there are no more.
+template <typename T, bool Gated, typename At>
+__device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int64_t j, int64_t end, int64_t stride,
+                                          At at) {
+  typedef typename T::raw raw;
+  constexpr int C = kMidCols, RT = kMidRows / 16, kPitch = 16 * C + 4;
+  typedef int32_t Slab[kWaves][16][kPitch];
+  Slab* slabs = reinterpret_cast<Slab*>(smem);  // one for 16 rows
+  static_assert(RT * sizeof(Slab) <= kLds, "LDS");
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1), g = lane >> 4, m = lane & 15;
+  const int tiles = packed_tiles<Gated>(p);
+  const int count = p.blocks > wave ? (p.blocks - wave + kWaves - 1) / kWaves : 0;
+  // a thread ends four columns of one row of every slab that it has a part in
+  constexpr int kOut = Gated ? 2 * C : 4 * C;           // groups of 4 output columns
+  constexpr int kSlabs = kWave * kWaves / (16 * kOut);  // at once
+  constexpr int kTurns = RT / kSlabs;
+  const int o = threadIdx.x % kOut, sr = threadIdx.x / kOut % 16, s0 = threadIdx.x / (16 * kOut);
+  const int from = 4 * (Gated ? o / 4 * 8 + o % 4 : o);
+
+  struct Step {
+    u32x4 w[C], x[RT];
+  };
+  Item it;
+  int tile0;
+  const uint8_t* w[C];  // uniform; lanes are 16 bytes apart
+  const int8_t* q[RT];
+  Step d0, d1;
+  auto point = [&](int64_t j) __attribute__((always_inline)) {
+    it = at(j, tile0);
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      w[c] = packed_tile(p, it.expert, tiles, min(tile0 + c, tiles - 1)) + (int64_t)wave * kBlockBytes;
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+      q[r] = p.q + ((int64_t)token_of(p, it.row + min(16 * r + m, it.rows - 1)) * p.blocks + wave) * kBlockRed + 16 * g;
+  };
+  auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
+#pragma unroll
+    for (int c = 0; c < C; ++c)
+      d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane));
+#pragma unroll
+    for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
+  };
+  auto start = [&](int64_t j) __attribute__((always_inline)) {
+    point(j);
+    if (count > 0) fetch(d0, 0);
+    if (count > 1) fetch(d1, 1);
+  };
+  if (j < end) start(j);
+#pragma unroll 1
+  for (; j < end; j += stride) {
+    const Item now = it;
+    const int col = (Gated ? tile0 / 2 : tile0) * 16 + 4 * o;
+    const Columns<T, Gated, 4> k(p, now.expert, col);
+    float step[kTurns], residual[kTurns][4];
+#pragma unroll
+    for (int i = 0; i < kTurns; ++i) {
+      const int64_t row = now.row + min(16 * (s0 + kSlabs * i) + sr, now.rows - 1);
+      step[i] = p.step[token_of(p, (int)row)];
+#pragma unroll
+      for (int t = 0; t < 4; ++t) residual[i][t] = 0.f;
+      if (!Gated && p.residual != nullptr && col < p.n)
+        block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + row * p.ldr + col, residual[i], p.n - col);
+    }
+    i32x4 acc[RT][C] = {};
+    auto multiply = [&](const Step& d) __attribute__((always_inline)) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[r][c] = mfma(d.w[c], d.x[r], acc[r][c]);
+    };
+#pragma unroll 1
+    for (int i = 0; i < count; i += 2) {
+      multiply(d0);
+      __builtin_amdgcn_sched_barrier(0);
+      if (i + 2 < count) fetch(d0, i + 2);
+      if (i + 1 < count) {
+        multiply(d1);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + 3 < count) fetch(d1, i + 3);
+      }
+    }
+    if (j + stride < end) start(j + stride);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int r = 0; r < RT; ++r)
+#pragma unroll
+      for (int c = 0; c < C; ++c) *reinterpret_cast<i32x4*>(&slabs[r][wave][m][16 * c + 4 * g]) = acc[r][c];
+    wait_barrier<63, 0>();
+    with_ending<Gated>(p, [&](auto act) __attribute__((always_inline)) {
+#pragma unroll
+      for (int i = 0; i < kTurns; ++i) {
+        const int r = s0 + kSlabs * i, local = 16 * r + sr;
+        if (local >= now.rows || col >= p.n) continue;
+        i32x4 v = {}, u = {};
+#pragma unroll
+        for (int x = 0; x < kWaves; ++x) {
+          v += *reinterpret_cast<const i32x4*>(&slabs[r][x][sr][from]);
+          if constexpr (Gated) u += *reinterpret_cast<const i32x4*>(&slabs[r][x][sr][from + 16]);
+        }
+        float sum[4], up[4];
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          sum[t] = (float)v[t];
+          up[t] = (float)u[t];
+        }
+        finish<T, Gated, decltype(act)::value, 4>(p, k, now.row + local, col, step[i], sum, up, residual[i]);
+      }
+    });
+    wait_barrier<63, 0>();  // before the next item's sums
+  }
+}
+
 template <typename T, bool Gated>
 __global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void tile_kernel(ProductArgs p) {
+void tile_kernel(ProductArgs p, int few) {
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const bool listed = p.lists.counts != nullptr;
+  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
+  if (few) {
+    const int groups = (packed_tiles<Gated>(p) + kMidCols - 1) / kMidCols;
+    const int mids = listed ? p.lists.counts[1] : (p.rows + kMidRows - 1) / kMidRows;
+    const int64_t total = (int64_t)mids * groups;
+    mid_items<T, Gated>(p, smem, total * xcd / 8 + (blockIdx.x >> 3), total * (xcd + 1) / 8, per,
+                        [&](int64_t j, int& tile0) __attribute__((always_inline)) {
+                          // row tiles of the same columns next to each other, where one expert has all
+                          const int i = (int)(listed ? j / groups : j % mids);
+                          tile0 = (int)(listed ? j % groups : j / mids) * kMidCols;
+                          return listed ? p.lists.mid[i]
+                                        : Item{0, i * kMidRows, min(p.rows - i * kMidRows, kMidRows), 0};
+                        });
+    return;
+  }
   const int ntiles = (packed_tiles<Gated>(p) + kTileCols - 1) / kTileCols;
   const int mtiles = listed ? p.lists.counts[2] : (p.rows + kTileRows - 1) / kTileRows;
   const int64_t total = (int64_t)mtiles * ntiles;
   // Blocks are dealt round-robin over the 8 XCDs: each XCD has a contiguous
   // range of tiles, which its blocks go through in turn.
-  const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
   const int64_t end = total * (xcd + 1) / 8;
   for (int64_t at = total * xcd / 8 + (blockIdx.x >> 3); at < end; at += per) {
     // row tiles of an expert in groups of 8, column by column
@@ -266,13 +400,14 @@ void tile_kernel(ProductArgs p) {
 }
 
 template <typename T, bool Gated>
-static hipError_t launch_typed(const ProductArgs& p, hipStream_t stream) {
-  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p);
+static hipError_t launch_typed(const ProductArgs& p, bool few, hipStream_t stream) {
+  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p, (int)few);
 }
 
-hipError_t launch_tiles(int dtype, const ProductArgs& p, hipStream_t stream) {
-  if (dtype == BLOCK_BF16) return p.gated ? launch_typed<BF16, true>(p, stream) : launch_typed<BF16, false>(p, stream);
-  return p.gated ? launch_typed<F16, true>(p, stream) : launch_typed<F16, false>(p, stream);
+hipError_t launch_tiles(int dtype, const ProductArgs& p, bool few, hipStream_t stream) {
+  if (dtype == BLOCK_BF16)
+    return p.gated ? launch_typed<BF16, true>(p, few, stream) : launch_typed<BF16, false>(p, few, stream);
+  return p.gated ? launch_typed<F16, true>(p, few, stream) : launch_typed<F16, false>(p, few, stream);
 }
 
 }  // namespace experts
