@@ -8,10 +8,12 @@
 // it, and its rank among those lanes. That needs each wave's count of each
 // expert, which LDS holds in 16 bits. Nothing depends on the order of atomics.
 //
-// Up to kOne choices are one block's work in one launch. More are dealt to up
-// to kBlocks blocks: a first launch counts each block's choices by expert, in
-// the second every block adds up what the others have (64 x 896 counts, read
-// from L2 by all of them) instead of a launch of its own for that.
+// Up to kOne choices are one block's work. More are dealt to up to kBlocks
+// blocks, each of which has to know how many choices of each expert are in the
+// blocks before it and in all. Up to kRead choices every block counts them all
+// for itself, in the same launch (32752 choices of 112 of 896 experts: 7.2 us,
+// with a launch for the counts 9.8); of more, a first launch counts each block's,
+// and in the second every block adds up what the others have.
 #include "block_device.h"
 #include "experts_launch.h"
 
@@ -20,15 +22,14 @@ namespace experts {
 using block::kWave;
 
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
-constexpr int kOne = 4 * kThreads;
+constexpr int kOne = 4 * kThreads, kRead = 64 * kThreads;
 constexpr int kBlocks = 64;
+enum Counts { kOwn, kAll, kListed };  // of a block's own choices, of all, by the launch before
 
-// The expert of choice c counted from `first`, or -1.
-__device__ __forceinline__ int local(const SortArgs& p, int c) {
-  const int id = p.ids[c];
-  const uint32_t e = (uint32_t)id - (uint32_t)p.first;
-  return id >= p.first && e < (uint32_t)p.experts ? (int)e : -1;
-}
+// An id counted from `first`, in unsigned arithmetic: below `experts` if it is one
+// of them. (Negative ids are all one: -1 - first is never small.)
+__device__ __forceinline__ uint32_t local(const SortArgs& p, int id) { return (uint32_t)max(id, -1) - (uint32_t)p.first; }
+struct __attribute__((packed, aligned(4))) Four { block::u32x4 v; };  // of ids, at any of them
 
 // The choices of block b: whole rounds of kThreads.
 __device__ __forceinline__ int64_t chunk_of(const SortArgs& p, int blocks) {
@@ -43,21 +44,22 @@ __global__ __launch_bounds__(kThreads) void count_kernel(SortArgs p, int* hist) 
   const int64_t chunk = chunk_of(p, gridDim.x), c0 = blockIdx.x * chunk;
   const int c1 = (int)min((int64_t)p.choices, c0 + chunk);
   for (int64_t c = c0 + threadIdx.x; c < c1; c += kThreads) {
-    const int e = local(p, (int)c);
-    if (e >= 0) atomicAdd(&count[e], 1);
+    const uint32_t e = local(p, p.ids[c]);
+    if (e < (uint32_t)p.experts) atomicAdd(&count[e], 1);
   }
   __syncthreads();
-  for (int e = threadIdx.x; e < p.experts; e += kThreads) hist[(int64_t)blockIdx.x * p.experts + e] = count[e];
+  for (int e = threadIdx.x; e < p.experts; e += kThreads) hist[blockIdx.x * p.experts + e] = count[e];
 }
 
-// Most: the experts there is room for. Per: choices of a lane in a round.
-// Alone: one block, one round, no counts from a launch before.
-template <int Most, int Per, bool Alone>
+// Most: the experts there is room for. Per: choices of a lane in a round. (kOwn:
+// one block, one round.)
+template <int Most, int Per, Counts From>
 __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* hist) {
   constexpr int kMine = Most / kThreads;  // experts of a thread: kMine t ..
-  __shared__ uint16_t seen[kWaves][Most];  // by wave, then the sum of earlier waves'
+  __shared__ __attribute__((aligned(16))) uint16_t seen[kWaves][Most];  // by wave, then the sum of earlier waves'
   __shared__ int start[Most];
   __shared__ int part[kWaves];
+  constexpr bool Alone = From == kOwn;
   const int t = threadIdx.x, wave = t / kWave, lane = t & (kWave - 1);
   const int64_t chunk = Alone ? Per * kThreads : chunk_of(p, gridDim.x), c0 = blockIdx.x * chunk;
   const int64_t c1 = min((int64_t)p.choices, c0 + chunk);
@@ -65,7 +67,6 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
   // waves that have any choice
   const int waves = Alone ? (p.choices + Per * kWave - 1) / (Per * kWave) : kWaves;
 
-  for (int i = t; i < waves * Most / 2; i += kThreads) reinterpret_cast<uint32_t*>(seen)[i] = 0;
   int mine[kMine], before[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) mine[i] = before[i] = 0;
@@ -94,25 +95,63 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
     }
     if (blockIdx.x == 0 && t == kThreads - 1) p.offsets[p.experts] = base;
   };
-  if constexpr (!Alone) {
+  if constexpr (From == kAll) {
+    // `start` counts what is before this block, `after` the rest
+    int* after = reinterpret_cast<int*>(seen);
+    for (int e = t; e < p.experts; e += kThreads) start[e] = after[e] = 0;
+    __syncthreads();
+    // (c0 is a multiple of four; a thread has four groups of four at once)
+    constexpr int kAtOnce = 4;
+    const int groups = p.choices / 4;
+    auto count = [&](int* to, int id) __attribute__((always_inline)) {
+      const uint32_t e = local(p, id);
+      if (e < (uint32_t)p.experts) atomicAdd(to + e, 1);
+    };
+#pragma unroll 1
+    for (int g = t; g < groups; g += kAtOnce * kThreads) {
+      block::u32x4 ids[kAtOnce];
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        ids[q] = reinterpret_cast<const Four*>(p.ids + 4 * min(g + q * kThreads, groups - 1))->v;
+#pragma unroll
+      for (int q = 0; q < kAtOnce; ++q)
+        if (g + q * kThreads < groups) {
+          int* to = 4 * (g + q * kThreads) < c0 ? start : after;
+#pragma unroll
+          for (int f = 0; f < 4; ++f) count(to, (int)ids[q][f]);
+        }
+    }
+    if (4 * groups + t < p.choices) count(4 * groups + t < c0 ? start : after, p.ids[4 * groups + t]);
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int e = kMine * t + i;
+      before[i] = e < p.experts ? start[e] : 0;
+      mine[i] = e < p.experts ? before[i] + after[e] : 0;
+    }
+    scan();
+  } else if constexpr (From == kListed) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int e = min(kMine * t + i, p.experts - 1);
-      const bool in = kMine * t + i < p.experts;
-      for (int b0 = 0; b0 < (int)gridDim.x; b0 += 32) {
-        int n[32];
+      int n[kBlocks];
 #pragma unroll
-        for (int q = 0; q < 32; ++q) n[q] = hist[(int64_t)min(b0 + q, (int)gridDim.x - 1) * p.experts + e];
+      for (int b = 0; b < kBlocks; ++b) n[b] = hist[min(b, (int)gridDim.x - 1) * p.experts + e];
+      // (which blocks there are, and come before, is the same for all lanes)
+      if (kMine * t + i < p.experts) {
 #pragma unroll
-        for (int q = 0; q < 32; ++q) {
-          const int v = in && b0 + q < (int)gridDim.x ? n[q] : 0;
-          mine[i] += v;
-          before[i] += b0 + q < (int)blockIdx.x ? v : 0;
-        }
+        for (int b = 0; b < kBlocks; ++b)
+          if (b < (int)blockIdx.x)
+            before[i] += n[b];
+          else if (b < (int)gridDim.x)
+            mine[i] += n[b];
+        mine[i] += before[i];
       }
     }
     scan();
   }
+  if constexpr (From == kAll) __syncthreads();  // `after` is read
+  for (int i = t; i < waves * Most / 2; i += kThreads) reinterpret_cast<uint32_t*>(seen)[i] = 0;
   __syncthreads();
 #pragma unroll 1
   for (int64_t r = c0; r < c1; r += Per * kThreads) {
@@ -120,22 +159,23 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
 #pragma unroll
     for (int i = 0; i < Per; ++i) {
       const int64_t c = r + (wave * Per + i) * kWave + lane;
-      e[i] = c < c1 ? local(p, (int)c) : -1;
+      e[i] = c < c1 ? (int)min(local(p, p.ids[c]), (uint32_t)p.experts) : p.experts;
     }
 #pragma unroll
     for (int i = 0; i < Per; ++i) {
-      const int key = e[i] < 0 ? p.experts : e[i];
-      uint64_t same = ~0ull;
+      uint64_t other = 0;  // lanes whose number has another bit somewhere
       for (int b = 0; b < bits; ++b) {
-        const uint64_t set = __ballot((key >> b) & 1);
-        same &= (key >> b) & 1 ? set : ~set;
+        const uint64_t set = __ballot((e[i] >> b) & 1);
+        const uint32_t mine = (uint32_t)-((e[i] >> b) & 1);
+        other |= set ^ (uint64_t)mine << 32 ^ mine;
       }
+      const uint64_t same = ~other;
       const int below = __popcll(same & ((1ull << lane) - 1));
-      rank[i] = e[i] >= 0 ? seen[wave][e[i]] + below : 0;
+      rank[i] = e[i] < p.experts ? seen[wave][e[i]] + below : 0;
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
       // the last of them counts for all
-      if (e[i] >= 0 && (same >> lane) == 1) seen[wave][e[i]] = (uint16_t)(rank[i] + 1);
+      if (e[i] < p.experts && (same >> lane) == 1) seen[wave][e[i]] = (uint16_t)(rank[i] + 1);
       __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
       __builtin_amdgcn_wave_barrier();
     }
@@ -145,13 +185,16 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int x = kMine * t + i;
-      int sum = 0;
-      if (x < p.experts)
-        for (int w = 0; w < waves; ++w) {
-          const int v = seen[w][x];
-          seen[w][x] = (uint16_t)sum;
-          sum += v;
+      int sum = 0, v[kWaves];
+      if (x < p.experts) {
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) v[w] = w < waves ? seen[w][x] : 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          if (w < waves) seen[w][x] = (uint16_t)sum;
+          sum += v[w];
         }
+      }
       total[i] = sum;
     }
     if constexpr (Alone) {
@@ -164,7 +207,7 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
     for (int i = 0; i < Per; ++i) {
       const int64_t c = r + (wave * Per + i) * kWave + lane;
       if (c >= c1) continue;
-      const int at = e[i] >= 0 ? start[e[i]] + seen[wave][e[i]] + rank[i] : -1;
+      const int at = e[i] < p.experts ? start[e[i]] + seen[wave][e[i]] + rank[i] : -1;
       p.place[c] = at;
       if (at >= 0 && at < p.capacity) p.token[at] = (int)((uint32_t)c / (uint32_t)p.topk);
     }
@@ -192,22 +235,22 @@ static int blocks_for(int64_t choices) {
 }
 
 size_t sort_workspace_bytes(int64_t choices, int experts) {
-  return choices <= kOne ? 0 : (size_t)kBlocks * experts * sizeof(int);
+  return choices <= kRead ? 0 : (size_t)kBlocks * experts * sizeof(int);
 }
 
 template <int Most>
 static hipError_t launch_most(const SortArgs& p, hipStream_t stream) {
   int* hist = static_cast<int*>(p.workspace);
-  const dim3 one(1), threads(kThreads);
+  const dim3 blocks(p.choices <= kOne ? 1 : blocks_for(p.choices)), threads(kThreads);
   if (p.choices <= kOne)
-    return launch_kernel(p.choices <= kThreads ? place_kernel<Most, 1, true> : place_kernel<Most, 4, true>, one,
+    return launch_kernel(p.choices <= kThreads ? place_kernel<Most, 1, kOwn> : place_kernel<Most, 4, kOwn>, blocks,
                          threads, stream, p, nullptr);
-  const dim3 blocks(blocks_for(p.choices));
+  if (p.choices <= kRead) return launch_kernel(place_kernel<Most, 1, kAll>, blocks, threads, stream, p, nullptr);
   const hipError_t e = launch_kernel(count_kernel<Most>, blocks, threads, stream, p, hist);
   if (e != hipSuccess) return e;
   const bool many = p.choices > (int64_t)kBlocks * 2 * kThreads;
-  return launch_kernel(many ? place_kernel<Most, 4, false> : place_kernel<Most, 1, false>, blocks, threads, stream, p,
-                       hist);
+  return launch_kernel(many ? place_kernel<Most, 4, kListed> : place_kernel<Most, 1, kListed>, blocks, threads, stream,
+                       p, hist);
 }
 
 hipError_t launch_sort(const SortArgs& p, hipStream_t stream) {

@@ -192,11 +192,29 @@ class Gated8Plan(_ProductPlan):
 _I32, _F32, _I8 = torch.int32, torch.float32, torch.int8
 
 
+# The checks run on every call, in front of kernels of a few microseconds: what
+# is as it should be passes here, the rest goes to the checks that name the fault.
+
+
+def _per_token(t, dtype, plan: _ExpertsPlan, rows: int, name: str) -> int | None:
+    """Pointer of a contiguous [rows][topk] tensor; spare rows at the end are allowed."""
+    if t is not None and t.dtype is dtype and t.get_device() == plan.device:
+        shape = t.shape
+        if len(shape) == 2 and shape[1] == plan.topk and shape[0] >= rows and t.is_contiguous():
+            return t.data_ptr()
+    return _per_row(t, dtype, plan, (rows, plan.topk), name)
+
+
 def _sorted_rows(t, plan: CombinePlan, name: str) -> tuple[int | None, int, int]:
     """Pointer, row stride and rows of a matrix in sorted order; None has no rows."""
     if t is None:
         return None, plan.width, 0
-    rows = min(t.shape[0], MAX_CHOICES) if t.dim() == 2 else 0
+    shape = t.shape
+    if t.dtype is plan.dtype and t.get_device() == plan.device and len(shape) == 2 and shape[1] == plan.width:
+        stride = t.stride()
+        if stride[1] == 1 and stride[0] >= plan.width and 1 < shape[0] <= MAX_CHOICES:
+            return t.data_ptr(), stride[0], shape[0]
+    rows = min(shape[0], MAX_CHOICES) if len(shape) == 2 else 0
     return *_rows_of(t, plan.dtype, plan, rows, plan.width, name), rows
 
 
@@ -204,12 +222,12 @@ def sort(plan: SortPlan, ids, offsets, place, token, workspace, rows: int | None
     """offsets [experts + 1], place [rows][topk] and token [capacity] of the
     choices ids [rows][topk], all int32."""
     rows = ids.shape[0] if rows is None else rows
-    shape = (rows, plan.topk)
-    if token.dim() != 1:
-        raise ValueError(f"token: expected one dimension, got {tuple(token.shape)}")
-    capacity = min(token.shape[0], MAX_CHOICES)
-    _run(LIB.experts_sort, "experts_sort", plan, _per_row(ids, _I32, plan, shape, "ids"),
-         _dense(offsets, _I32, plan, (plan.experts + 1,), "offsets"), _per_row(place, _I32, plan, shape, "place"),
+    shape = token.shape
+    if len(shape) != 1:
+        raise ValueError(f"token: expected one dimension, got {tuple(shape)}")
+    capacity = min(shape[0], MAX_CHOICES)
+    _run(LIB.experts_sort, "experts_sort", plan, _per_token(ids, _I32, plan, rows, "ids"),
+         _dense(offsets, _I32, plan, (plan.experts + 1,), "offsets"), _per_token(place, _I32, plan, rows, "place"),
          _per_row(token, _I32, plan, (capacity,), "token"), _workspace(plan, workspace), capacity, rows,
          _stream(plan, stream))
 
@@ -219,7 +237,7 @@ def gather(plan: CombinePlan, x, place, xs, rows: int | None = None, stream=None
     rows = x.shape[0] if rows is None else rows
     to, ld, capacity = _sorted_rows(xs, plan, "xs")
     _run(LIB.experts_gather, "experts_gather", plan, *_rows_of(x, plan.dtype, plan, rows, plan.width, "x"),
-         _per_row(place, _I32, plan, (rows, plan.topk), "place"), to, ld, capacity, rows, _stream(plan, stream))
+         _per_token(place, _I32, plan, rows, "place"), to, ld, capacity, rows, _stream(plan, stream))
 
 
 def gather_backward(plan: CombinePlan, dxs, place, dx, rows: int | None = None, stream=None) -> None:
@@ -227,7 +245,7 @@ def gather_backward(plan: CombinePlan, dxs, place, dx, rows: int | None = None, 
     rows = dx.shape[0] if rows is None else rows
     src, ld, capacity = _sorted_rows(dxs, plan, "dxs")
     _run(LIB.experts_gather_backward, "experts_gather_backward", plan, src, ld,
-         _per_row(place, _I32, plan, (rows, plan.topk), "place"),
+         _per_token(place, _I32, plan, rows, "place"),
          *_rows_of(dx, plan.dtype, plan, rows, plan.width, "dx"), capacity, rows, _stream(plan, stream))
 
 
@@ -235,10 +253,10 @@ def combine(plan: CombinePlan, ys, place, weights, y, residual=None, rows: int |
     """y[r] = sum_j weights[r, j] ys[place[r, j]] + residual[r]; `residual` may
     be `y` itself; weights are FP32 [rows][topk]."""
     rows = y.shape[0] if rows is None else rows
-    shape, dt, w = (rows, plan.topk), plan.dtype, plan.width
+    dt, w = plan.dtype, plan.width
     src, ld, capacity = _sorted_rows(ys, plan, "ys")
-    _run(LIB.experts_combine, "experts_combine", plan, src, ld, _per_row(place, _I32, plan, shape, "place"),
-         _per_row(weights, _F32, plan, shape, "weights"), *_rows_of(residual, dt, plan, rows, w, "residual"),
+    _run(LIB.experts_combine, "experts_combine", plan, src, ld, _per_token(place, _I32, plan, rows, "place"),
+         _per_token(weights, _F32, plan, rows, "weights"), *_rows_of(residual, dt, plan, rows, w, "residual"),
          *_rows_of(y, dt, plan, rows, w, "y"), capacity, rows, _stream(plan, stream))
 
 
@@ -248,7 +266,6 @@ def combine_backward(plan: CombinePlan, dy, ys, place, weights, dys, dweights, r
     weights[r, j] dy[r], other rows left as they are, and dweights [rows][topk]
     FP32. Either may be None (not computed), ys with dweights, weights with dys."""
     rows = dy.shape[0] if rows is None else rows
-    shape = (rows, plan.topk)
     if dweights is None:
         ys = None
     src, src_ld, have = _sorted_rows(ys, plan, "ys")
@@ -257,8 +274,8 @@ def combine_backward(plan: CombinePlan, dy, ys, place, weights, dys, dweights, r
         raise ValueError(f"dys: expected as many rows as ys ({have}), has {room}")
     _run(LIB.experts_combine_backward, "experts_combine_backward", plan,
          *_rows_of(dy, plan.dtype, plan, rows, plan.width, "dy"), src, src_ld,
-         _per_row(place, _I32, plan, shape, "place"), _per_row(weights, _F32, plan, shape, "weights"), to, to_ld,
-         _per_row(dweights, _F32, plan, shape, "dweights"), max(have, room), rows, _stream(plan, stream))
+         _per_token(place, _I32, plan, rows, "place"), _per_token(weights, _F32, plan, rows, "weights"), to, to_ld,
+         _per_token(dweights, _F32, plan, rows, "dweights"), max(have, room), rows, _stream(plan, stream))
 
 
 def quantize(plan: _ProductPlan, w, stream=None) -> tuple[torch.Tensor, torch.Tensor]:
