@@ -28,11 +28,14 @@ struct Cols {
   static constexpr int kWords = 2 * (int)sizeof(typename T::raw);
   uint32_t w[kWords];
 
-  // `count` of them inside the row
+  // `count` of them inside the row. Once: the row is not read again (rows in
+  // sorted order, which together are larger than the caches), written likewise.
+  template <bool Once = false>
   __device__ __forceinline__ void load(const typename T::raw* p, int count) {
+    auto get = [](const u32x4* q) { return Once ? __builtin_nontemporal_load(q) : *q; };
     if constexpr (sizeof(typename T::raw) == 2) {
       if (count >= 8) {
-        const u32x4 x = reinterpret_cast<const block::Any16*>(p)->v;
+        const u32x4 x = get(&reinterpret_cast<const block::Any16*>(p)->v);
 #pragma unroll
         for (int t = 0; t < 4; ++t) w[t] = x[t];
       } else {
@@ -43,7 +46,8 @@ struct Cols {
           if (t < count) w[t >> 1] |= (uint32_t)p[t] << (16 * (t & 1));
       }
     } else if (count >= 8) {
-      const u32x4 x = reinterpret_cast<const Any16of4*>(p)->v, y = reinterpret_cast<const Any16of4*>(p + 4)->v;
+      const u32x4 x = get(&reinterpret_cast<const Any16of4*>(p)->v);
+      const u32x4 y = get(&reinterpret_cast<const Any16of4*>(p + 4)->v);
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         w[t] = x[t];
@@ -54,18 +58,25 @@ struct Cols {
       for (int t = 0; t < 8; ++t) w[t] = t < count ? __float_as_uint(p[t]) : 0;
     }
   }
+  template <bool Once = false>
   __device__ __forceinline__ void store(typename T::raw* p, int count) const {
+    auto put = [](u32x4* q, u32x4 v) {
+      if (Once)
+        __builtin_nontemporal_store(v, q);
+      else
+        *q = v;
+    };
     if constexpr (sizeof(typename T::raw) == 2) {
       if (count >= 8) {
-        reinterpret_cast<block::Any16*>(p)->v = u32x4{w[0], w[1], w[2], w[3]};
+        put(&reinterpret_cast<block::Any16*>(p)->v, u32x4{w[0], w[1], w[2], w[3]});
       } else {
 #pragma unroll
         for (int t = 0; t < 7; ++t)
           if (t < count) p[t] = (uint16_t)(w[t >> 1] >> (16 * (t & 1)));
       }
     } else if (count >= 8) {
-      reinterpret_cast<Any16of4*>(p)->v = u32x4{w[0], w[1], w[2], w[3]};
-      reinterpret_cast<Any16of4*>(p + 4)->v = u32x4{w[4], w[5], w[6], w[7]};
+      put(&reinterpret_cast<Any16of4*>(p)->v, u32x4{w[0], w[1], w[2], w[3]});
+      put(&reinterpret_cast<Any16of4*>(p + 4)->v, u32x4{w[4], w[5], w[6], w[7]});
     } else {
 #pragma unroll
       for (int t = 0; t < 8; ++t)
@@ -135,7 +146,7 @@ __global__ __launch_bounds__(256) void gather_kernel(RowsArgs p, int chunks) {
     const int j = __builtin_ctzll(k.live);
     k.live &= k.live - 1;
     const int64_t at = __builtin_amdgcn_readlane(k.place, j);
-    if (c < p.width) v.store(static_cast<raw*>(p.to_sorted) + at * p.ld_to_sorted + c, p.width - c);
+    if (c < p.width) v.template store<true>(static_cast<raw*>(p.to_sorted) + at * p.ld_to_sorted + c, p.width - c);
   }
 }
 
@@ -158,7 +169,7 @@ __global__ __launch_bounds__(1024) void collect_kernel(RowsArgs p, int chunks) {
     const int n = k.next(at, w, which);
 #pragma unroll
     for (int q = 0; q < kGroup; ++q)
-      v[q].load(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
+      v[q].template load<true>(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
 #pragma unroll
     for (int q = 0; q < kGroup; ++q)
       if (q < n)
@@ -225,7 +236,7 @@ __global__ __launch_bounds__(1024) void backward_kernel(RowsArgs p) {
       if (dots)
 #pragma unroll
         for (int q = 0; q < kGroup; ++q)
-          s[q].load(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
+          s[q].template load<true>(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
       if (!one) v.load(x + c, count);
       if (p.to_sorted != nullptr)
 #pragma unroll
@@ -236,7 +247,7 @@ __global__ __launch_bounds__(1024) void backward_kernel(RowsArgs p) {
 #pragma unroll
             for (int t = 0; t < 8; ++t) y[t] = w[q] * v.get(t);
             out.set(y);
-            out.store(static_cast<raw*>(p.to_sorted) + at[q] * p.ld_to_sorted + c, count);
+            out.template store<true>(static_cast<raw*>(p.to_sorted) + at[q] * p.ld_to_sorted + c, count);
           }
       if (dots)
 #pragma unroll
