@@ -29,10 +29,10 @@ struct Quantiser {
       s = NAN;
     }
   }
-  // the integer in the low byte; adding 1.5 x 2^23 rounds to nearest-even
+  // The integer in the low byte; adding 1.5 x 2^23 rounds to nearest-even. (Any
+  // byte will do where the scale is NaN.)
   __device__ __forceinline__ uint32_t byte(float x) const {
-    const float n = up > 0.f ? up * x : 0.f;
-    const float t = n * inv;
+    const float n = up * x, t = n * inv;
     return __float_as_uint(fmaf(fmaf(-t, a, n), inv, t) + 12582912.f);
   }
   __device__ __forceinline__ uint32_t bytes(float x, float y, float z, float w) const {

@@ -9,7 +9,9 @@
 // one is read into registers while the one before is multiplied, the others are
 // on their way from memory. Rows lie in LDS as 64-byte lines with a swizzle,
 // weights as the packed form has them, so that neither read meets a bank
-// conflict. There is a body for 64, 128, 192 and 256 rows.
+// conflict. There is a body for 64, 128, 192 and 256 rows. The weights of an
+// expert with one row tile pass by the caches (64 rows of 3584 x 65536: 53 us,
+// like this 46; 256 rows: 74 and 70; where row tiles share them it costs 4 %).
 //
 // mid items, where there are few tiles: up to 64 rows by 64 columns, the
 // reduction dealt to the eight waves, whose operands come straight from memory
@@ -38,7 +40,8 @@ struct Shape {
   static constexpr int kReads = MT + 4;  // LDS reads of a wave and stage
 };
 
-template <typename T, bool Gated, int MT>
+// Once: no other row tile reads these weights.
+template <typename T, bool Gated, int MT, bool Once>
 __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int expert, int row0, int rows, int tile0) {
   typedef Shape<MT> S;
   typedef typename T::raw raw;
@@ -69,7 +72,11 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
   }
   const uint32_t lds0 = (uint32_t)(uintptr_t)(block::lds_void*)smem;
   auto issue = [&](int i, int s, uint32_t buf) __attribute__((always_inline)) {
-    dma16(src[i] + (int64_t)s * kStep[i < S::A_PER ? 0 : 1], buf + dst[i]);
+    const char* from = src[i] + (int64_t)s * kStep[i < S::A_PER ? 0 : 1];
+    if (i >= S::A_PER && Once)
+      block::dma16_once(from, buf + dst[i]);
+    else
+      dma16(from, buf + dst[i]);
   };
   // the row's scale, for the ending
   const int mine = min((int)threadIdx.x, rows - 1);
@@ -388,14 +395,21 @@ void tile_kernel(ProductArgs p, int few) {
     const int height = min(((it.rows + high - 1) / high + 31) / 32 * 32, kTileRows);
     const int mt = 8 * group + in % gm, nt = in / gm;
     const int row0 = it.row + mt * height, rows = min(height, it.rows - mt * height);
-    if (rows <= 64)
-      tile<T, Gated, 2>(p, smem, it.expert, row0, rows, nt * kTileCols);
-    else if (rows <= 128)
-      tile<T, Gated, 4>(p, smem, it.expert, row0, rows, nt * kTileCols);
-    else if (rows <= 192)
-      tile<T, Gated, 6>(p, smem, it.expert, row0, rows, nt * kTileCols);
-    else
-      tile<T, Gated, 8>(p, smem, it.expert, row0, rows, nt * kTileCols);
+    const int tile0 = nt * kTileCols;
+    if (high == 1) {
+      if (rows <= 64)
+        tile<T, Gated, 2, true>(p, smem, it.expert, row0, rows, tile0);
+      else if (rows <= 128)
+        tile<T, Gated, 4, true>(p, smem, it.expert, row0, rows, tile0);
+      else if (rows <= 192)
+        tile<T, Gated, 6, true>(p, smem, it.expert, row0, rows, tile0);
+      else
+        tile<T, Gated, 8, true>(p, smem, it.expert, row0, rows, tile0);
+    } else if (rows <= 192) {
+      tile<T, Gated, 6, false>(p, smem, it.expert, row0, rows, tile0);
+    } else {
+      tile<T, Gated, 8, false>(p, smem, it.expert, row0, rows, tile0);
+    }
   }
 }
 

@@ -20,6 +20,11 @@ __device__ __forceinline__ void dma16(const char* addr, uint32_t lds) {
   asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off" : : "v"(addr), "{m0}"(lds));
 }
 
+// The same for what no other block reads: past the caches.
+__device__ __forceinline__ void dma16_once(const char* addr, uint32_t lds) {
+  asm volatile("s_nop 0\n\tglobal_load_lds_dwordx4 %0, off nt" : : "v"(addr), "{m0}"(lds));
+}
+
 __device__ __forceinline__ u32x4 lds_b128(uint32_t addr) {
   return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)addr;
 }
