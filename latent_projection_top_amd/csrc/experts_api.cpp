@@ -134,21 +134,14 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.rows = rows;
   z.column_tiles = planes * experts::column_tiles(c.outputs);
   z.blocks = a.blocks;
-  // (by expert: mid items as many, and tiles as few, as there can be)
-  z.few = rows > experts::kStreamRows &&
-          experts::is_few(offsets != nullptr ? experts::most_mid(rows, c.experts)
-                                             : (rows + experts::kMidRows - 1) / experts::kMidRows,
-                          (rows + experts::kTileRows - 1) / experts::kTileRows, z.column_tiles, a.blocks,
-                          offsets != nullptr);
+  z.way = experts::way_of(rows, c.experts, z.column_tiles, a.blocks, offsets != nullptr);
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);
   z.most_tiles = (int)experts::most_tiles(rows, c.experts);
   if (int st = status_of(experts::launch_quantise(c.dtype, z, s))) return st;
-  // how many rows an expert has is known on the device only: both kernels go
-  // through their lists, unless there can be nothing on one of them
-  if (!z.few && (offsets != nullptr || rows <= experts::kStreamRows))
+  if (z.way == experts::kApart)
     if (int st = status_of(experts::launch_stream(c.dtype, a, false, s))) return st;
-  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, z.few != 0, s)) : ROUTE_OK;
+  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, z.way, s)) : ROUTE_OK;
 }
 
 int run_quantize(const Product8& c, const void* w, int8_t* w8, float* scale, void* stream) {

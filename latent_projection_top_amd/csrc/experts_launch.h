@@ -57,10 +57,16 @@ constexpr int kBlockRed = 64, kBlockBytes = 1024;
 inline int red_blocks(int k) { return (k + kBlockRed - 1) / kBlockRed; }
 inline int column_tiles(int n) { return (n + 15) / 16; }
 
-// The rows of one expert in a product. Where there are many in all: up to
-// kStreamRows of them (`brief`), or its first-th and later row tiles of up to
-// kTileRows (`tiles`, an entry for each; `rows` is of all of them). Where there
-// are few: row tiles of up to kMidRows (`mid`).
+// How a product's rows are dealt out. How many rows an expert has is known on
+// the device only, which makes lists of items:
+//   kApart     up to kStreamRows rows of an expert are a brief item, for a kernel
+//              that streams weights; of more, row tiles of up to kTileRows, for
+//              another
+//   kTogether  short experts are row tiles of up to kMidRows (mid items), which
+//              the second kernel takes after its tiles: one launch less
+//   kFew       all are mid items
+enum Way { kApart = 0, kTogether = 1, kFew = 2 };
+// (of a tile, `rows` is of all of its expert's, which are at `first` and after)
 struct Item {
   int32_t expert, row, rows, first;
 };
@@ -88,19 +94,28 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
   return Lists{&items->expert, items + 1, mid, mid + most_mid(rows, experts)};
 }
 
-// Whether a product of more than kStreamRows rows goes as mid items: `mids` of
-// them at most, or `tiles` row tiles at least. Modelled times in us. A mid item's
-// is mostly latency; many wait for each other, 256 at a time, or for their
-// operands, 8 KB for each block of the reduction, which the L2s deliver at 8
-// TB/s. Tiles come in rounds of 256; by expert they are a second launch after
-// the brief items'.
-inline bool is_few(int64_t mids, int64_t tiles, int column_tiles, int blocks, bool offsets) {
+// The way of a product of `rows` rows. kFew where its modelled time in us is less
+// than the tiles': a mid item's is mostly latency; many wait for each other, 256
+// at a time, or for their operands, 8 KB for each block of the reduction, which
+// the L2s deliver at 8 TB/s; tiles come in rounds of 256, and by expert with
+// another launch before them. (By expert mid items as many, and tiles as few, as
+// there can be.) Where the weights are more than the last-level cache holds,
+// streaming the short experts' in a kernel of its own is worth a launch (112
+// experts of 3584 x 4096, 1.6 GB: 260 us, together 302; 33 of 253 x 320, 3 MB:
+// 26 and 22).
+inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
+  if (rows <= kStreamRows) return kApart;
+  const int64_t mids = (rows + kMidRows - 1) / kMidRows + (offsets ? most_brief(rows, experts) : 0);
+  const int64_t tiles = (rows + kTileRows - 1) / kTileRows;
   const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
   const int64_t t = tiles * ((column_tiles + kTileCols - 1) / kTileCols);
   const double step = (double)blocks;
   const double busy = (double)m * step * 0.001, rounds = (double)((m + 255) / 256) * (3.0 + 0.1 * step);
-  return 3.0 + (busy > rounds ? busy : rounds) <
-         (double)((t + 255) / 256) * (6.0 + 0.6 * step) + (offsets ? 8.0 + 0.1 * step : 0.0);
+  if (3.0 + (busy > rounds ? busy : rounds) <
+      (double)((t + 255) / 256) * (12.0 + 0.65 * step) + (offsets ? 8.0 + 0.1 * step : 0.0))
+    return kFew;
+  const double bytes = (double)experts * column_tiles * blocks * kBlockBytes;
+  return offsets && bytes > 256e6 ? kApart : kTogether;
 }
 
 // The most rows of a product that makes the integers by itself: of an item, and
@@ -144,14 +159,14 @@ struct QuantiseArgs {
   Item* area;
   int64_t ldx;
   int tokens, k, stride, experts, rows, column_tiles, blocks;
-  int few;  // the list is of mid items alone
+  int way;
   int most_brief, most_mid, most_tiles;
 };
 hipError_t launch_quantise(int dtype, const QuantiseArgs& args, hipStream_t stream);
 // Brief items (without offsets every row, of kStreamRows at most).
 hipError_t launch_stream(int dtype, const ProductArgs& args, bool fused, hipStream_t stream);
 // Tiles and mid items (without offsets every row, as either).
-hipError_t launch_tiles(int dtype, const ProductArgs& args, bool few, hipStream_t stream);
+hipError_t launch_tiles(int dtype, const ProductArgs& args, int way, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,
                        hipStream_t stream);

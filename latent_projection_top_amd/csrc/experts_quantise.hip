@@ -29,7 +29,7 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
       n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
     }
     // this thread's items: how many, of which list
-    const int kind = p.few ? 1 : n <= kStreamRows ? 0 : 2;
+    const int kind = p.way == kFew ? 1 : n > kStreamRows ? 2 : p.way == kTogether ? 1 : 0;
     const int height = kind == 0 ? kStreamRows : kind == 1 ? kMidRows : kTileRows;
     const int m = (n + height - 1) / height;
     // sums over the block, and before this thread

@@ -28,7 +28,9 @@ enum Counts { kOwn, kAll, kListed };  // of a block's own choices, of all, by th
 
 // An id counted from `first`, in unsigned arithmetic: below `experts` if it is one
 // of them. (Negative ids are all one: -1 - first is never small.)
-__device__ __forceinline__ uint32_t local(const SortArgs& p, int id) { return (uint32_t)max(id, -1) - (uint32_t)p.first; }
+__device__ __forceinline__ uint32_t local(const SortArgs& p, int id) {
+  return (uint32_t)max(id, -1) - (uint32_t)p.first;
+}
 struct __attribute__((packed, aligned(4))) Four { block::u32x4 v; };  // of ids, at any of them
 
 // The choices of block b: whole rounds of kThreads.

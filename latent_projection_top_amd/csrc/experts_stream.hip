@@ -95,7 +95,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
   };
   auto fetch_w = [&](Step& d, int i) __attribute__((always_inline)) {
 #pragma unroll
-    for (int c = 0; c < C; ++c)  // past the caches: a block's weights are no other's (16 rows of 3584 x 65536: 56 us, like this 51)
+    for (int c = 0; c < C; ++c)  // past the caches: no other block reads them (16 x 3584 x 65536: 56 us, like this 51)
       d.w[c] = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane)));
   };
@@ -162,6 +162,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     // where the reduction is split), then of all. The first blocks' loads go out
     // before the weights', behind which they would have to wait.
     constexpr int kFirst = 4;
+    static_assert(kDepth <= kFirst, "");
     u32x4 v[kFirst][RT][2];
     auto look = [&](u32x4(&d)[RT][2], int b) __attribute__((always_inline)) {
 #pragma unroll
@@ -183,11 +184,23 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
 #pragma unroll
       for (int i = 0; i < kFirst; ++i) most[r] = larger(larger(most[r], v[i][r][0]), v[i][r][1]);
     }
-#pragma unroll 1
-    for (int b = wave + kFirst * kWaves; b < p.blocks; b += kWaves) {
-      look(v[0], b);
+    if (splits == 1)  // they are the first steps' as well
 #pragma unroll
-      for (int r = 0; r < RT; ++r) most[r] = larger(larger(most[r], v[0][r][0]), v[0][r][1]);
+      for (int s = 0; s < kDepth; ++s)
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          d[s].x[r][0] = v[s][r][0];
+          d[s].x[r][kX - 1] = v[s][r][1];
+        }
+    constexpr int kMore = Whole ? kFirst : 1;  // (see Whole)
+#pragma unroll 1
+    for (int b = wave + kFirst * kWaves; b < p.blocks; b += kMore * kWaves) {
+#pragma unroll
+      for (int i = 0; i < kMore; ++i) look(v[i], min(b + i * kWaves, p.blocks - 1));
+#pragma unroll
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int i = 0; i < kMore; ++i) most[r] = larger(larger(most[r], v[i][r][0]), v[i][r][1]);
     }
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
@@ -208,7 +221,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     }
 #pragma unroll
     for (int s = 0; s < kDepth; ++s)
-      if (s < count) fetch_x(d[s], s);
+      if (s < count && splits > 1) fetch_x(d[s], s);
   } else {
 #pragma unroll
     for (int s = 0; s < kDepth; ++s)

@@ -13,11 +13,11 @@
 // expert with one row tile pass by the caches (64 rows of 3584 x 65536: 53 us,
 // like this 46; 256 rows: 74 and 70; where row tiles share them it costs 4 %).
 //
-// mid items, where there are few tiles: up to 64 rows by 64 columns, the
-// reduction dealt to the eight waves, whose operands come straight from memory
-// and whose sums meet in LDS: half of the matrix cores' rate at best, but an
-// eighth of the steps one after another, which is what the time is made of
-// there. The next item's first operands are on their way while one ends.
+// mid items, where there are few tiles, or after them: up to 64 rows by 64
+// columns, the reduction dealt to the eight waves, whose operands come straight
+// from memory and whose sums meet in LDS: half of the matrix cores' rate at
+// best, but an eighth of the steps one after another, which is what the time is
+// made of there. The next item's first operands are on their way while one ends.
 #include "experts_device.h"
 #include "lds_device.h"
 
@@ -245,10 +245,9 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
   __syncthreads();  // before the next tile's loads to LDS
 }
 
-// A block's mid items, `at(j)` the j-th, which ends where there are no more.
-template <typename T, bool Gated, typename At>
-__device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int64_t j, int64_t end, int64_t stride,
-                                          At at) {
+// A block's mid items of `end`: next_of(-1) is the first, at(j) the j-th.
+template <typename T, bool Gated, typename Next, typename At>
+__device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int64_t end, Next next_of, At at) {
   typedef typename T::raw raw;
   constexpr int C = kMidCols, RT = kMidRows / 16, kPitch = 16 * C + 4;
   typedef int32_t Slab[kWaves][16][kPitch];
@@ -287,16 +286,18 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
     for (int c = 0; c < C; ++c)
       d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane));
 #pragma unroll
-    for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
+    for (int r = 0; r < RT; ++r)
+      if (16 * r < it.rows) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
   };
   auto start = [&](int64_t j) __attribute__((always_inline)) {
     point(j);
     if (count > 0) fetch(d0, 0);
     if (count > 1) fetch(d1, 1);
   };
-  if (j < end) start(j);
+  int64_t next = next_of(-1);
+  if (next < end) start(next);
 #pragma unroll 1
-  for (; j < end; j += stride) {
+  while (next < end) {
     const Item now = it;
     const int col = (Gated ? tile0 / 2 : tile0) * 16 + 4 * o;
     const Columns<T, Gated, 4> k(p, now.expert, col);
@@ -314,8 +315,9 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
     auto multiply = [&](const Step& d) __attribute__((always_inline)) {
 #pragma unroll
       for (int r = 0; r < RT; ++r)
+        if (16 * r < now.rows)
 #pragma unroll
-        for (int c = 0; c < C; ++c) acc[r][c] = mfma(d.w[c], d.x[r], acc[r][c]);
+          for (int c = 0; c < C; ++c) acc[r][c] = mfma(d.w[c], d.x[r], acc[r][c]);
     };
 #pragma unroll 1
     for (int i = 0; i < count; i += 2) {
@@ -328,7 +330,8 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
         if (i + 3 < count) fetch(d1, i + 3);
       }
     }
-    if (j + stride < end) start(j + stride);
+    next = next_of(next);
+    if (next < end) start(next);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -361,26 +364,13 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
 
 template <typename T, bool Gated>
 __global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void tile_kernel(ProductArgs p, int few) {
+void tile_kernel(ProductArgs p, int way) {
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const bool listed = p.lists.counts != nullptr;
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
-  if (few) {
-    const int groups = (packed_tiles<Gated>(p) + kMidCols - 1) / kMidCols;
-    const int mids = listed ? p.lists.counts[1] : (p.rows + kMidRows - 1) / kMidRows;
-    const int64_t total = (int64_t)mids * groups;
-    mid_items<T, Gated>(p, smem, total * xcd / 8 + (blockIdx.x >> 3), total * (xcd + 1) / 8, per,
-                        [&](int64_t j, int& tile0) __attribute__((always_inline)) {
-                          // row tiles of the same columns next to each other, where one expert has all
-                          const int i = (int)(listed ? j / groups : j % mids);
-                          tile0 = (int)(listed ? j % groups : j / mids) * kMidCols;
-                          return listed ? p.lists.mid[i]
-                                        : Item{0, i * kMidRows, min(p.rows - i * kMidRows, kMidRows), 0};
-                        });
-    return;
-  }
+  const int slot = blockIdx.x >> 3;
   const int ntiles = (packed_tiles<Gated>(p) + kTileCols - 1) / kTileCols;
-  const int mtiles = listed ? p.lists.counts[2] : (p.rows + kTileRows - 1) / kTileRows;
+  const int mtiles = listed ? p.lists.counts[2] : way == kFew ? 0 : (p.rows + kTileRows - 1) / kTileRows;
   const int64_t total = (int64_t)mtiles * ntiles;
   // Blocks are dealt round-robin over the 8 XCDs: each XCD has a contiguous
   // range of tiles, which its blocks go through in turn.
@@ -411,17 +401,35 @@ void tile_kernel(ProductArgs p, int few) {
       tile<T, Gated, 8, false>(p, smem, it.expert, row0, rows, tile0);
     }
   }
+  // Blocks that had a tile less take the four mid items that it is worth first.
+  const int groups = (packed_tiles<Gated>(p) + kMidCols - 1) / kMidCols;
+  const int mids = listed ? p.lists.counts[1] : way == kFew ? (p.rows + kMidRows - 1) / kMidRows : 0;
+  const int64_t all = (int64_t)mids * groups, first = all * xcd / 8, count = all * (xcd + 1) / 8 - first;
+  const int more = (int)((end - total * xcd / 8) % per), less = per - more;
+  const int64_t extra = more != 0 ? 4 * less : 0;
+  auto next_of = [&](int64_t j) __attribute__((always_inline)) {
+    if (j < 0) return more != 0 && slot >= more ? (int64_t)(slot - more) : extra + slot;
+    if (j >= extra) return j + per;
+    return j + less < extra ? j + less : extra + slot;
+  };
+  mid_items<T, Gated>(p, smem, count, next_of, [&](int64_t j, int& tile0) __attribute__((always_inline)) {
+    // row tiles of the same columns next to each other, where one expert has all
+    const int64_t at = first + j;
+    const int i = (int)(listed ? at / groups : at % mids);
+    tile0 = (int)(listed ? at % groups : at / mids) * kMidCols;
+    return listed ? p.lists.mid[i] : Item{0, i * kMidRows, min(p.rows - i * kMidRows, kMidRows), 0};
+  });
 }
 
 template <typename T, bool Gated>
-static hipError_t launch_typed(const ProductArgs& p, bool few, hipStream_t stream) {
-  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p, (int)few);
+static hipError_t launch_typed(const ProductArgs& p, int way, hipStream_t stream) {
+  return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p, way);
 }
 
-hipError_t launch_tiles(int dtype, const ProductArgs& p, bool few, hipStream_t stream) {
+hipError_t launch_tiles(int dtype, const ProductArgs& p, int way, hipStream_t stream) {
   if (dtype == BLOCK_BF16)
-    return p.gated ? launch_typed<BF16, true>(p, few, stream) : launch_typed<BF16, false>(p, few, stream);
-  return p.gated ? launch_typed<F16, true>(p, few, stream) : launch_typed<F16, false>(p, few, stream);
+    return p.gated ? launch_typed<BF16, true>(p, way, stream) : launch_typed<BF16, false>(p, way, stream);
+  return p.gated ? launch_typed<F16, true>(p, way, stream) : launch_typed<F16, false>(p, way, stream);
 }
 
 }  // namespace experts
