@@ -34,18 +34,60 @@ __device__ __forceinline__ int token_of(const ProductArgs& p, int row) {
   return p.token != nullptr ? min(max(p.token[row], 0), p.tokens - 1) : row;
 }
 
-// C (4 or 8) consecutive columns of an expert's FP32 vector, `count` of them
-// inside it.
+// `count` (less than eight) consecutive 16-bit values, zeros after them. Every
+// load is of a value that is there, so that they go out together: one by one
+// where the row's end says so, each would be waited for (7 us a row's end).
+__device__ __forceinline__ u32x4 edge8(const uint16_t* p, int count) {
+  u32x4 v = {0, 0, 0, 0};
+  if (count > 0) {
+    uint32_t e[8];
+#pragma unroll
+    for (int t = 0; t < 7; ++t) e[t] = p[min(t, count - 1)];
+    e[7] = 0;
+#pragma unroll
+    for (int t = 0; t < 8; t += 2) v[t / 2] = (t < count ? e[t] : 0) | (t + 1 < count ? e[t + 1] << 16 : 0);
+  }
+  return v;
+}
+__device__ __forceinline__ u32x4 load8(const uint16_t* p, int count) {
+  return count >= 8 ? reinterpret_cast<const block::Any16*>(p)->v : edge8(p, count);
+}
+
+struct __attribute__((packed, aligned(4))) Any16of4 { u32x4 v; };  // 16 bytes at any 4-byte address
+
+// C (4 or 8) consecutive columns of an expert's FP32 vector, or of a row of
+// 16-bit values, `count` of them inside it.
 template <int C>
 __device__ __forceinline__ void load_scales(const float* s, float (&v)[C], int count) {
+  if (count >= C) {
 #pragma unroll
-  for (int t = 0; t < C; ++t) v[t] = t < count ? s[t] : 0.f;
+    for (int t = 0; t < C; t += 4) {
+      const u32x4 x = reinterpret_cast<const Any16of4*>(s + t)->v;
+#pragma unroll
+      for (int f = 0; f < 4; ++f) v[t + f] = __uint_as_float(x[f]);
+    }
+  } else if (count > 0) {
+#pragma unroll
+    for (int t = 0; t < C; ++t) v[t] = s[min(t, count - 1)];
+  }
+}
+template <typename T, int C>
+__device__ __forceinline__ void load_values(const uint16_t* p, float (&v)[C], int count) {
+  if (count >= C) {
+    block::load_cols<T, C>(p, v, C);
+  } else if (count > 0) {
+    uint16_t e[C];
+#pragma unroll
+    for (int t = 0; t < C; ++t) e[t] = p[min(t, count - 1)];
+#pragma unroll
+    for (int t = 0; t < C; ++t) v[t] = T::load(e[t]);
+  }
 }
 
 // What the columns of an output need: scales and the bias.
 template <typename T, bool Gated, int C>
 struct Columns {
-  float scale[C], other[C];  // other: the up product's scale, or the bias
+  float scale[C] = {}, other[C] = {};  // other: the up product's scale, or the bias
   Columns() = default;
   __device__ __forceinline__ Columns(const ProductArgs& p, int expert, int col) {
     const int count = p.n - col;
@@ -53,11 +95,8 @@ struct Columns {
     load_scales<C>(p.scale[0] + at, scale, count);
     if constexpr (Gated) {
       load_scales<C>(p.scale[1] + at, other, count);
-    } else {
-#pragma unroll
-      for (int t = 0; t < C; ++t) other[t] = 0.f;
-      if (p.bias != nullptr && count > 0)
-        block::load_cols<T, C>(static_cast<const typename T::raw*>(p.bias) + at, other, count);
+    } else if (p.bias != nullptr) {
+      load_values<T, C>(static_cast<const uint16_t*>(p.bias) + at, other, count);
     }
   }
 };

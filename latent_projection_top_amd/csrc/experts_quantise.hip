@@ -86,14 +86,7 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int c = 16 * (t + Threads * i) + 8 * h;
-      v[i][h] = u32x4{0, 0, 0, 0};
-      if (c + 8 <= k) {
-        v[i][h] = reinterpret_cast<const block::Any16*>(in + c)->v;
-      } else if (c < k) {
-#pragma unroll
-        for (int e = 0; e < 7; ++e)
-          if (c + e < k) v[i][h][e >> 1] |= (uint32_t)in[c + e] << (16 * (e & 1));
-      }
+      v[i][h] = load8(in + c, k - c);
     }
   u16x2 m = {0, 0};
 #pragma unroll

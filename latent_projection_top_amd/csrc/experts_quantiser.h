@@ -1,12 +1,9 @@
 // Values as 8-bit integers with a common scale.
 #pragma once
 
-#include "block_device.h"
-#include "experts_launch.h"
+#include "experts_device.h"
 
 namespace experts {
-
-using block::u32x4;
 
 // The integers of values whose largest magnitude is `most`: q = rne(127 x / a),
 // s = a / 127. The quotient is decided without a division: with x and a of at

@@ -6,21 +6,14 @@
 // from there in order, eight at a time, so that eight rows' loads are in flight
 // together and a dropped choice costs nothing. Sums are FP32 in the order of
 // the choices.
-#include "block_device.h"
-#include "experts_launch.h"
+#include "experts_device.h"
 
 namespace experts {
 
-using block::BF16;
-using block::F16;
 using block::F32;
-using block::kWave;
-using block::u32x4;
 
 constexpr int kLaneCols = 8, kWaveCols = kLaneCols * kWave;
 constexpr int kGroup = 8;  // rows in flight
-
-struct __attribute__((packed, aligned(4))) Any16of4 { u32x4 v; };
 
 // Eight columns of a row as they are in memory.
 template <typename T>
@@ -39,11 +32,9 @@ struct Cols {
 #pragma unroll
         for (int t = 0; t < 4; ++t) w[t] = x[t];
       } else {
+        const u32x4 x = edge8(p, count);
 #pragma unroll
-        for (int t = 0; t < 4; ++t) w[t] = 0;
-#pragma unroll
-        for (int t = 0; t < 7; ++t)
-          if (t < count) w[t >> 1] |= (uint32_t)p[t] << (16 * (t & 1));
+        for (int t = 0; t < 4; ++t) w[t] = x[t];
       }
     } else if (count >= 8) {
       const u32x4 x = get(&reinterpret_cast<const Any16of4*>(p)->v);
@@ -55,7 +46,9 @@ struct Cols {
       }
     } else {
 #pragma unroll
-      for (int t = 0; t < 8; ++t) w[t] = t < count ? __float_as_uint(p[t]) : 0;
+      for (int t = 0; t < 8; ++t) w[t] = __float_as_uint(p[min(t, count - 1)]);
+#pragma unroll
+      for (int t = 0; t < 8; ++t) w[t] = t < count ? w[t] : 0;
     }
   }
   template <bool Once = false>

@@ -39,17 +39,8 @@ struct Shared {
 
 // 16 values of a row, `count` of them inside it.
 __device__ __forceinline__ void load16(const uint16_t* p, u32x4 (&v)[2], int count) {
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    v[h] = u32x4{0, 0, 0, 0};
-    if (count >= 8 * h + 8) {
-      v[h] = reinterpret_cast<const block::Any16*>(p + 8 * h)->v;
-    } else {
-#pragma unroll
-      for (int t = 0; t < 7; ++t)
-        if (8 * h + t < count) v[h][t >> 1] |= (uint32_t)p[8 * h + t] << (16 * (t & 1));
-    }
-  }
+  v[0] = load8(p, count);
+  v[1] = load8(p + 8, count - 8);
 }
 
 // One item's columns from tile0 on, C column tiles of them, its split-th of
@@ -59,7 +50,6 @@ __device__ __forceinline__ void load16(const uint16_t* p, u32x4 (&v)[2], int cou
 template <typename T, bool Gated, int C, int RT, bool Fused, bool Whole>
 __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it, int tile0, int unit, int split,
                                             int splits, Shared& shared) {
-  typedef typename T::raw raw;
   constexpr int kPitch = 16 * C + 4;
   typedef int32_t Part[16 * RT][kPitch];
   Part* part = reinterpret_cast<Part*>(shared.part);
@@ -279,7 +269,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     }
     float residual[4] = {};
     if (!Gated && p.residual != nullptr)
-      block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + r * p.ldr + col, residual, p.n - col);
+      load_values<T, 4>(static_cast<const uint16_t*>(p.residual) + r * p.ldr + col, residual, p.n - col);
     i32x4 v = {}, u = {};
     if (splits > 1) {
       const int32_t* from = units + 4 * (row * kQuads + quad);

@@ -185,15 +185,7 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
   const int wrow = 16 * MT * wm + lane / kLanes;
   u32x4 ahead[kGroup];
   auto fetch = [&](u32x4& d, int l) __attribute__((always_inline)) {
-    d = u32x4{0, 0, 0, 0};
-    const uint16_t* from_row = static_cast<const uint16_t*>(p.residual) + (row0 + l) * p.ldr + col;
-    if (l < rows && col + 8 <= p.n) {
-      d = reinterpret_cast<const block::Any16*>(from_row)->v;
-    } else if (l < rows) {
-#pragma unroll
-      for (int t = 0; t < 7; ++t)
-        if (col + t < p.n) d[t >> 1] |= (uint32_t)from_row[t] << (16 * (t & 1));
-    }
+    d = load8(static_cast<const uint16_t*>(p.residual) + (row0 + min(l, rows - 1)) * p.ldr + col, p.n - col);
   };
   if (add)
 #pragma unroll
@@ -308,8 +300,8 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
       step[i] = p.step[token_of(p, (int)row)];
 #pragma unroll
       for (int t = 0; t < 4; ++t) residual[i][t] = 0.f;
-      if (!Gated && p.residual != nullptr && col < p.n)
-        block::load_cols<T, 4>(static_cast<const raw*>(p.residual) + row * p.ldr + col, residual[i], p.n - col);
+      if (!Gated && p.residual != nullptr)
+        load_values<T, 4>(static_cast<const uint16_t*>(p.residual) + row * p.ldr + col, residual[i], p.n - col);
     }
     i32x4 acc[RT][C] = {};
     auto multiply = [&](const Step& d) __attribute__((always_inline)) {
