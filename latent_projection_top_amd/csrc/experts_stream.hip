@@ -298,8 +298,8 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
 
 // How many blocks share a unit of work: parts of at least four steps of a wave,
 // since a join costs 2 to 3 us, and a step some 0.4.
-__device__ __forceinline__ int splits_of(int64_t units, int blocks) {
-  return units == 0 || units >= kSplitUnits / 2 ? 1 : max(1, min(kSplitUnits / (int)units, blocks / (4 * kWaves)));
+__device__ __forceinline__ int splits_of(int units, int blocks) {
+  return units == 0 || units >= kSplitUnits / 2 ? 1 : max(1, min(kSplitUnits / units, blocks / (4 * kWaves)));
 }
 
 template <typename T, bool Gated, int C>
@@ -308,17 +308,16 @@ void stream_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(16))) Shared shared;
   const int groups = (packed_tiles<Gated>(p) + C - 1) / C;
   const bool listed = p.lists.counts != nullptr;
-  const int64_t total = (int64_t)(listed ? p.lists.counts[0] : 1) * groups;
-  const int splits = splits_of(total, p.blocks);
-  for (int64_t at = blockIdx.x; at < total * splits; at += gridDim.x) {
-    const int64_t u = at / splits;
-    const int split = (int)(at - u * splits);  // (more than one: u < kSplitUnits / 2)
-    const int i = (int)(u / groups), tile0 = (int)(u - (int64_t)i * groups) * C;
+  // (at most 2^12 experts by 2^13 groups)
+  const int total = (listed ? p.lists.counts[0] : 1) * groups, splits = splits_of(total, p.blocks);
+  for (int at = blockIdx.x; at < total * splits; at += gridDim.x) {
+    const int u = at / splits, split = at - u * splits;  // (more than one: u < kSplitUnits / 2)
+    const int i = u / groups, tile0 = (u - i * groups) * C;
     const Item it = listed ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
     if (it.rows <= 16)
-      stream_item<T, Gated, C, 1, false, true>(p, it, tile0, (int)u, split, splits, shared);
+      stream_item<T, Gated, C, 1, false, true>(p, it, tile0, u, split, splits, shared);
     else
-      stream_item<T, Gated, C, 2, false, true>(p, it, tile0, (int)u, split, splits, shared);
+      stream_item<T, Gated, C, 2, false, true>(p, it, tile0, u, split, splits, shared);
   }
 }
 
@@ -360,16 +359,14 @@ void fused_kernel(ProductArgs p) {
     items = min(items, kFusedRows);
   }
   const int tiles = packed_tiles<Gated>(p), wide = (tiles + C - 1) / C;
-  const int64_t total = (int64_t)items * wide;
-  const int splits = splits_of(total, p.blocks);
-  for (int64_t at = blockIdx.x; at < total * splits; at += gridDim.x) {
-    const int64_t u = at / splits;
-    const int i = (int)(u / wide), tile0 = (int)(u - (int64_t)i * wide) * C, split = (int)(at - u * splits);
+  const int total = items * wide, splits = splits_of(total, p.blocks);
+  for (int at = blockIdx.x; at < total * splits; at += gridDim.x) {
+    const int u = at / splits, split = at - u * splits, i = u / wide, tile0 = (u - i * wide) * C;
     Item it{0, 0, p.rows, 0};
     if (p.offsets != nullptr)
       it = Item{__builtin_amdgcn_readfirstlane(list[i].expert), __builtin_amdgcn_readfirstlane(list[i].row),
                 __builtin_amdgcn_readfirstlane(list[i].rows), 0};
-    stream_item<T, Gated, C, 1, true, Whole>(p, it, tile0, (int)u, split, splits, shared);
+    stream_item<T, Gated, C, 1, true, Whole>(p, it, tile0, u, split, splits, shared);
   }
 }
 

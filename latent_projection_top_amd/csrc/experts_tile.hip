@@ -239,7 +239,7 @@ __device__ __forceinline__ void tile(const ProductArgs& p, char* smem, int exper
 
 // A block's mid items of `end`: next_of(-1) is the first, at(j) the j-th.
 template <typename T, bool Gated, typename Next, typename At>
-__device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int64_t end, Next next_of, At at) {
+__device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int end, Next next_of, At at) {
   typedef typename T::raw raw;
   constexpr int C = kMidCols, RT = kMidRows / 16, kPitch = 16 * C + 4;
   typedef int32_t Slab[kWaves][16][kPitch];
@@ -264,8 +264,7 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
   const uint8_t* w[C];  // uniform; lanes are 16 bytes apart
   const int8_t* q[RT];
   Step d0, d1;
-  auto point = [&](int64_t j) __attribute__((always_inline)) {
-    it = at(j, tile0);
+  auto point = [&]() __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
       w[c] = packed_tile(p, it.expert, tiles, min(tile0 + c, tiles - 1)) + (int64_t)wave * kBlockBytes;
@@ -273,21 +272,24 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
     for (int r = 0; r < RT; ++r)
       q[r] = p.q + ((int64_t)token_of(p, it.row + min(16 * r + m, it.rows - 1)) * p.blocks + wave) * kBlockRed + 16 * g;
   };
-  auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
+  auto fetch = [&](Step& d, int i, int rows) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c)
       d.w[c] = *reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane));
 #pragma unroll
     for (int r = 0; r < RT; ++r)
-      if (16 * r < it.rows) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
+      if (16 * r < rows) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
   };
-  auto start = [&](int64_t j) __attribute__((always_inline)) {
-    point(j);
-    if (count > 0) fetch(d0, 0);
-    if (count > 1) fetch(d1, 1);
+  auto start = [&]() __attribute__((always_inline)) {
+    point();
+    if (count > 0) fetch(d0, 0, it.rows);
+    if (count > 1) fetch(d1, 1, it.rows);
   };
-  int64_t next = next_of(-1);
-  if (next < end) start(next);
+  int next = next_of(-1);
+  if (next < end) {
+    it = at(next, tile0);
+    start();
+  }
 #pragma unroll 1
   while (next < end) {
     const Item now = it;
@@ -303,6 +305,8 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
       if (!Gated && p.residual != nullptr)
         load_values<T, 4>(static_cast<const uint16_t*>(p.residual) + row * p.ldr + col, residual[i], p.n - col);
     }
+    next = next_of(next);
+    if (next < end) it = at(next, tile0);  // (early: the list is read from memory)
     i32x4 acc[RT][C] = {};
     auto multiply = [&](const Step& d) __attribute__((always_inline)) {
 #pragma unroll
@@ -315,15 +319,14 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int6
     for (int i = 0; i < count; i += 2) {
       multiply(d0);
       __builtin_amdgcn_sched_barrier(0);
-      if (i + 2 < count) fetch(d0, i + 2);
+      if (i + 2 < count) fetch(d0, i + 2, now.rows);
       if (i + 1 < count) {
         multiply(d1);
         __builtin_amdgcn_sched_barrier(0);
-        if (i + 3 < count) fetch(d1, i + 3);
+        if (i + 3 < count) fetch(d1, i + 3, now.rows);
       }
     }
-    next = next_of(next);
-    if (next < end) start(next);
+    if (next < end) start();
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int r = 0; r < RT; ++r)
@@ -363,16 +366,18 @@ void tile_kernel(ProductArgs p, int way) {
   const int slot = blockIdx.x >> 3;
   const int ntiles = (packed_tiles<Gated>(p) + kTileCols - 1) / kTileCols;
   const int mtiles = listed ? p.lists.counts[2] : way == kFew ? 0 : (p.rows + kTileRows - 1) / kTileRows;
-  const int64_t total = (int64_t)mtiles * ntiles;
+  // (products of items and columns stay below 2^31: 2^24 rows in items of 64 by
+  // 2^12 groups of columns at most)
+  const int total = mtiles * ntiles;
   // Blocks are dealt round-robin over the 8 XCDs: each XCD has a contiguous
   // range of tiles, which its blocks go through in turn.
-  const int64_t end = total * (xcd + 1) / 8;
-  for (int64_t at = total * xcd / 8 + (blockIdx.x >> 3); at < end; at += per) {
+  const int begin = (int)((int64_t)total * xcd / 8), end = (int)((int64_t)total * (xcd + 1) / 8);
+  for (int at = begin + slot; at < end; at += per) {
     // row tiles of an expert in groups of 8, column by column
     const Item it = listed ? p.lists.tiles[at / ntiles] : Item{0, 0, p.rows, 0};
     const int high = (it.rows + kTileRows - 1) / kTileRows;  // its row tiles
-    const int64_t local = at - (int64_t)it.first * ntiles;
-    const int group = (int)(local / (8 * ntiles)), in = (int)(local - (int64_t)group * 8 * ntiles);
+    const int local = at - it.first * ntiles;
+    const int group = local / (8 * ntiles), in = local - group * 8 * ntiles;
     const int gm = min(high - 8 * group, 8);
     const int height = min(((it.rows + high - 1) / high + 31) / 32 * 32, kTileRows);
     const int mt = 8 * group + in % gm, nt = in / gm;
@@ -396,20 +401,19 @@ void tile_kernel(ProductArgs p, int way) {
   // Blocks that had a tile less take the four mid items that it is worth first.
   const int groups = (packed_tiles<Gated>(p) + kMidCols - 1) / kMidCols;
   const int mids = listed ? p.lists.counts[1] : way == kFew ? (p.rows + kMidRows - 1) / kMidRows : 0;
-  const int64_t all = (int64_t)mids * groups, first = all * xcd / 8, count = all * (xcd + 1) / 8 - first;
-  const int more = (int)((end - total * xcd / 8) % per), less = per - more;
-  const int64_t extra = more != 0 ? 4 * less : 0;
-  auto next_of = [&](int64_t j) __attribute__((always_inline)) {
-    if (j < 0) return more != 0 && slot >= more ? (int64_t)(slot - more) : extra + slot;
+  const int all = mids * groups, first = (int)((int64_t)all * xcd / 8);
+  const int count = (int)((int64_t)all * (xcd + 1) / 8) - first;
+  const int more = (end - begin) % per, less = per - more, extra = more != 0 ? 4 * less : 0;
+  auto next_of = [&](int j) __attribute__((always_inline)) {
+    if (j < 0) return more != 0 && slot >= more ? slot - more : extra + slot;
     if (j >= extra) return j + per;
     return j + less < extra ? j + less : extra + slot;
   };
-  mid_items<T, Gated>(p, smem, count, next_of, [&](int64_t j, int& tile0) __attribute__((always_inline)) {
+  mid_items<T, Gated>(p, smem, count, next_of, [&](int j, int& tile0) __attribute__((always_inline)) {
     // row tiles of the same columns next to each other, where one expert has all
-    const int64_t at = first + j;
-    const int i = (int)(listed ? at / groups : at % mids);
-    tile0 = (int)(listed ? at % groups : at / mids) * kMidCols;
-    return listed ? p.lists.mid[i] : Item{0, i * kMidRows, min(p.rows - i * kMidRows, kMidRows), 0};
+    const int by = listed ? groups : mids, at = (first + j) / by, rest = first + j - at * by;
+    tile0 = (listed ? rest : at) * kMidCols;
+    return listed ? p.lists.mid[at] : Item{0, rest * kMidRows, min(p.rows - rest * kMidRows, kMidRows), 0};
   });
 }
 
