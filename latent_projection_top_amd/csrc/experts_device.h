@@ -11,6 +11,9 @@ using block::F16;
 using block::kWave;
 using block::u32x4;
 
+// Of a grid of two dimensions, which may have more blocks than there is work for.
+__device__ __forceinline__ int block_of_grid() { return (int)(blockIdx.y * gridDim.x + blockIdx.x); }
+
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 // Lane (g, m) = (l / 16, l % 16) of the result holds column m of `b` (a row of

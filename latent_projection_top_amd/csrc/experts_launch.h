@@ -13,6 +13,12 @@ namespace experts {
 
 using route::launch_kernel;
 
+// At least that many blocks, in two dimensions: one holds fewer than 2^32 threads.
+inline dim3 grid_of(int64_t blocks) {
+  const int64_t y = (blocks + (1 << 20) - 1) >> 20;
+  return dim3((unsigned)((blocks + y - 1) / y), (unsigned)y);
+}
+
 // ------------------------------------------------------------------- sort --
 
 struct SortArgs {

@@ -73,11 +73,12 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
   constexpr int kBlock = Threads < kThreads ? kThreads : Threads, kRowsPer = kBlock / Threads;
   __shared__ uint32_t part[kBlock / kWave];
   const int blocks = (p.tokens + kRowsPer - 1) / kRowsPer, k = p.k;
-  if ((int)blockIdx.x == blocks) {
-    make_lists(p);
+  const int block = block_of_grid();
+  if (block >= blocks) {
+    if (block == blocks && p.offsets != nullptr) make_lists(p);
     return;
   }
-  const int t = threadIdx.x % Threads, row = blockIdx.x * kRowsPer + threadIdx.x / Threads;
+  const int t = threadIdx.x % Threads, row = block * kRowsPer + threadIdx.x / Threads;
   const bool live = row < p.tokens;
   const uint16_t* in = p.x + (int64_t)(live ? row : p.tokens - 1) * p.ldx;
   u32x4 v[Groups][2];
@@ -117,8 +118,8 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
 template <typename T, int Threads, int Groups>
 static hipError_t launch_rows(const QuantiseArgs& p, hipStream_t stream) {
   constexpr int kBlock = Threads < kThreads ? kThreads : Threads, kRowsPer = kBlock / Threads;
-  const unsigned blocks = (unsigned)((p.tokens + kRowsPer - 1) / kRowsPer) + (p.offsets != nullptr ? 1 : 0);
-  return launch_kernel(quantise_kernel<T, Threads, Groups>, dim3(blocks), dim3(kBlock), stream, p);
+  const int64_t blocks = (p.tokens + kRowsPer - 1) / kRowsPer + (p.offsets != nullptr ? 1 : 0);
+  return launch_kernel(quantise_kernel<T, Threads, Groups>, grid_of(blocks), dim3(kBlock), stream, p);
 }
 
 // A wave to a row where there are enough of them to fill the CUs, else a block.

@@ -122,7 +122,7 @@ struct Choices {
 };
 
 __device__ __forceinline__ int wave_of_grid() {
-  return __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (blockDim.x / kWave) + threadIdx.x / kWave));
+  return __builtin_amdgcn_readfirstlane(block_of_grid() * (int)(blockDim.x / kWave) + (int)threadIdx.x / kWave);
 }
 
 // to_sorted = plain at every place.
@@ -269,7 +269,7 @@ __global__ __launch_bounds__(1024) void backward_kernel(RowsArgs p) {
 hipError_t launch_spread(int dtype, const RowsArgs& p, hipStream_t stream) {
   const int chunks = (p.width + kWaveCols - 1) / kWaveCols;
   if (p.weights == nullptr && p.dweights == nullptr) {
-    const dim3 grid((unsigned)(((int64_t)p.rows * chunks + 3) / 4));
+    const dim3 grid = grid_of(((int64_t)p.rows * chunks + 3) / 4);
     return launch_kernel(dtype == BLOCK_BF16 ? gather_kernel<BF16> : dtype == BLOCK_F16 ? gather_kernel<F16>
                                                                                         : gather_kernel<F32>,
                          grid, dim3(256), stream, p, chunks);
@@ -283,7 +283,7 @@ hipError_t launch_collect(int dtype, const RowsArgs& p, hipStream_t stream) {
   const int chunks = (p.width + kWaveCols - 1) / kWaveCols;
   // a row's waves in one block, whose CU then reads whole rows
   const int waves = (int64_t)p.rows * chunks < 4096 ? 1 : chunks < 16 ? chunks : 16;
-  const dim3 grid((unsigned)(((int64_t)p.rows * chunks + waves - 1) / waves));
+  const dim3 grid = grid_of(((int64_t)p.rows * chunks + waves - 1) / waves);
   return launch_kernel(dtype == BLOCK_BF16 ? collect_kernel<BF16> : dtype == BLOCK_F16 ? collect_kernel<F16>
                                                                                        : collect_kernel<F32>,
                        grid, dim3(kWave * waves), stream, p, chunks);

@@ -28,6 +28,7 @@ __device__ __forceinline__ void dma16_once(const char* addr, uint32_t lds) {
 __device__ __forceinline__ u32x4 lds_b128(uint32_t addr) {
   return *(const __attribute__((address_space(3))) u32x4*)(uintptr_t)addr;
 }
+
 // Wait until at most Vm of this wave's loads are in flight and at most Lgkm
 // LDS reads are outstanding, then meet the block.
 template <int Vm, int Lgkm>

@@ -283,8 +283,9 @@ def quantize(plan: _ProductPlan, w, stream=None) -> tuple[torch.Tensor, torch.Te
     scales [experts][outputs]); once per set of weights."""
     shape = (plan.experts, plan.inputs, plan.outputs)
     ptr = _dense(w, plan.dtype, plan, shape, "w")
-    w8 = torch.empty(shape, dtype=_I8, device=w.device)
-    scale = torch.empty(shape[0], shape[2], dtype=_F32, device=w.device)
+    with torch.cuda.stream(stream):  # memory is reused in the order of the stream that it is allocated on
+        w8 = torch.empty(shape, dtype=_I8, device=w.device)
+        scale = torch.empty(shape[0], shape[2], dtype=_F32, device=w.device)
     name = f"experts_{plan.OP}_quantize"
     _run(getattr(LIB, name), name, plan, ptr, w8.data_ptr(), scale.data_ptr(), _stream(plan, stream))
     return w8, scale
@@ -296,7 +297,8 @@ def pack(plan: _ProductPlan, *w, stream=None) -> torch.Tensor:
     if len(w) != (2 if plan.OP == "gated8" else 1):
         raise ValueError(f"pack: {plan.OP} has {2 if plan.OP == 'gated8' else 1} matrices, got {len(w)}")
     ptrs = [_dense(t, _I8, plan, (plan.experts, plan.inputs, plan.outputs), "w") for t in w]
-    packed = torch.empty(plan.packed_bytes, dtype=torch.uint8, device=w[0].device)
+    with torch.cuda.stream(stream):  # as in quantize
+        packed = torch.empty(plan.packed_bytes, dtype=torch.uint8, device=w[0].device)
     name = f"experts_{plan.OP}_pack"
     _run(getattr(LIB, name), name, plan, *ptrs, packed.data_ptr(), _stream(plan, stream))
     return packed
