@@ -118,7 +118,8 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.k = c.inputs;
   a.experts = c.experts;
   a.offsets = offsets;
-  if (experts::is_fused(rows, c.experts, offsets != nullptr))
+  const int column_tiles = planes * experts::column_tiles(c.outputs);
+  if (experts::is_fused(rows, c.experts, column_tiles, a.blocks, offsets != nullptr))
     return status_of(experts::launch_stream(c.dtype, a, true, s));
   experts::QuantiseArgs z{};
   z.x = a.x;
@@ -132,16 +133,15 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.stride = a.blocks * experts::kBlockRed;
   z.experts = c.experts;
   z.rows = rows;
-  z.column_tiles = planes * experts::column_tiles(c.outputs);
-  z.blocks = a.blocks;
-  z.way = experts::way_of(rows, c.experts, z.column_tiles, a.blocks, offsets != nullptr);
+  const experts::Way way = experts::way_of(rows, c.experts, column_tiles, a.blocks, offsets != nullptr);
+  z.way = way;
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);
   z.most_tiles = (int)experts::most_tiles(rows, c.experts);
   if (int st = status_of(experts::launch_quantise(c.dtype, z, s))) return st;
-  if (z.way == experts::kApart)
+  if (way == experts::kBrief || way == experts::kApart)
     if (int st = status_of(experts::launch_stream(c.dtype, a, false, s))) return st;
-  return rows > experts::kStreamRows ? status_of(experts::launch_tiles(c.dtype, a, z.way, s)) : ROUTE_OK;
+  return way != experts::kBrief ? status_of(experts::launch_tiles(c.dtype, a, way, s)) : ROUTE_OK;
 }
 
 int run_quantize(const Product8& c, const void* w, int8_t* w8, float* scale, void* stream) {

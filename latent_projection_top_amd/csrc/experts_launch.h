@@ -65,18 +65,20 @@ inline int column_tiles(int n) { return (n + 15) / 16; }
 
 // How a product's rows are dealt out. How many rows an expert has is known on
 // the device only, which makes lists of items:
-//   kApart     up to kStreamRows rows of an expert are a brief item, for a kernel
-//              that streams weights; of more, row tiles of up to kTileRows, for
-//              another
+//   kBrief     all are brief items of up to kStreamRows rows, for a kernel that
+//              streams weights
+//   kApart     experts of up to kStreamRows rows are brief items; of more, row
+//              tiles of up to kTileRows, for another kernel
 //   kTogether  short experts are row tiles of up to kMidRows (mid items), which
 //              the second kernel takes after its tiles: one launch less
 //   kFew       all are mid items
-enum Way { kApart = 0, kTogether = 1, kFew = 2 };
+enum Way { kBrief, kApart, kTogether, kFew };
 // (of a tile, `rows` is of all of its expert's, which are at `first` and after)
 struct Item {
   int32_t expert, row, rows, first;
 };
 constexpr int kStreamRows = 32, kMidRows = 64, kTileRows = 256;
+constexpr int kBriefRows = 512;  // the most rows of kBrief by expert
 constexpr int kMidCols = 4, kTileCols = 16;  // packed column tiles of 16 that each takes
 struct Lists {
   const int32_t* counts;  // brief, mid, tiles; NULL: one expert has every row
@@ -84,11 +86,11 @@ struct Lists {
   const Item* mid;
   const Item* tiles;
 };
-inline int64_t most_brief(int64_t rows, int experts) { return rows < experts ? rows : experts; }
-inline int64_t most_mid(int64_t rows, int experts) { return rows / kMidRows + most_brief(rows, experts); }
+inline int64_t most_live(int64_t rows, int experts) { return rows < experts ? rows : experts; }  // experts with rows
+inline int64_t most_brief(int64_t rows, int experts) { return rows / kStreamRows + most_live(rows, experts); }
+inline int64_t most_mid(int64_t rows, int experts) { return rows / kMidRows + most_live(rows, experts); }
 inline int64_t most_tiles(int64_t rows, int experts) {
-  const int64_t n = rows / (kStreamRows + 1);
-  return rows / kTileRows + (n < experts ? n : experts);
+  return rows / kTileRows + most_live(rows / (kStreamRows + 1), experts);
 }
 inline size_t list_bytes(int64_t rows, int experts) {
   return sizeof(Item) *
@@ -110,8 +112,8 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
 // experts of 3584 x 4096, 1.6 GB: 260 us, together 302; 33 of 253 x 320, 3 MB:
 // 26 and 22).
 inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
-  if (rows <= kStreamRows) return kApart;
-  const int64_t mids = (rows + kMidRows - 1) / kMidRows + (offsets ? most_brief(rows, experts) : 0);
+  if (rows <= kStreamRows || (offsets && rows <= kBriefRows && rows <= 8 * (int64_t)experts)) return kBrief;
+  const int64_t mids = (rows + kMidRows - 1) / kMidRows + (offsets ? most_live(rows, experts) : 0);
   const int64_t tiles = (rows + kTileRows - 1) / kTileRows;
   const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
   const int64_t t = tiles * ((column_tiles + kTileCols - 1) / kTileCols);
@@ -124,11 +126,13 @@ inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool 
   return offsets && bytes > 256e6 ? kApart : kTogether;
 }
 
-// The most rows of a product that makes the integers by itself: of an item, and
-// of all of them by expert, where most experts have to have few.
-constexpr int kFusedItem = 16, kFusedRows = 512;
-inline bool is_fused(int64_t rows, int experts, bool offsets) {
-  return rows <= kFusedItem || (offsets && rows <= kFusedRows && rows <= 8 * (int64_t)experts);
+// Few rows of few columns of a short reduction: the streaming kernel makes the
+// integers by itself, in items of up to kFusedItem rows, for every item again.
+constexpr int kFusedItem = 16, kFusedRows = 128, kFusedSteps = 4;
+inline bool is_fused(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
+  if (blocks > 8 * kFusedSteps) return false;
+  if (!offsets) return rows <= kFusedItem && column_tiles <= 2048;
+  return rows <= kFusedRows && rows <= 8 * (int64_t)experts && most_live(rows, experts) * column_tiles <= 8192;
 }
 
 // What the streaming kernel uses of the workspace: counters of its column
@@ -156,7 +160,7 @@ struct ProductArgs {
   int tokens, rows, experts, k, n, blocks, act, gated;
 };
 // Rows as integers; where there are offsets also the lists of a product of
-// `rows` rows and `column_tiles` packed column tiles (area: list_bytes).
+// `rows` rows (area: list_bytes).
 struct QuantiseArgs {
   const uint16_t* x;
   int8_t* q;
@@ -164,15 +168,15 @@ struct QuantiseArgs {
   const int32_t* offsets;
   Item* area;
   int64_t ldx;
-  int tokens, k, stride, experts, rows, column_tiles, blocks;
-  int way;
+  int tokens, k, stride, experts, rows;
+  Way way;
   int most_brief, most_mid, most_tiles;
 };
 hipError_t launch_quantise(int dtype, const QuantiseArgs& args, hipStream_t stream);
 // Brief items (without offsets every row, of kStreamRows at most).
 hipError_t launch_stream(int dtype, const ProductArgs& args, bool fused, hipStream_t stream);
 // Tiles and mid items (without offsets every row, as either).
-hipError_t launch_tiles(int dtype, const ProductArgs& args, int way, hipStream_t stream);
+hipError_t launch_tiles(int dtype, const ProductArgs& args, Way way, hipStream_t stream);
 
 hipError_t launch_pack(const int8_t* const* w, int planes, void* packed, int experts, int k, int n,
                        hipStream_t stream);

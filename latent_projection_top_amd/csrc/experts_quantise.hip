@@ -29,7 +29,7 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
       n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
     }
     // this thread's items: how many, of which list
-    const int kind = p.way == kFew ? 1 : n > kStreamRows ? 2 : p.way == kTogether ? 1 : 0;
+    const int kind = p.way == kBrief ? 0 : p.way == kFew ? 1 : n > kStreamRows ? 2 : p.way == kTogether ? 1 : 0;
     const int height = kind == 0 ? kStreamRows : kind == 1 ? kMidRows : kTileRows;
     const int m = (n + height - 1) / height;
     // sums over the block, and before this thread
@@ -55,10 +55,10 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
       const int l = __builtin_ctzll(todo);
       todo &= todo - 1;
       const int k = __shfl(kind, l), at = __shfl(start, l), count = __shfl(m, l);
-      const int of = __shfl(e, l), row = __shfl(first, l), rows = __shfl(n, l);
+      const int high = k == 0 ? kStreamRows : kMidRows, of = __shfl(e, l), row = __shfl(first, l), rows = __shfl(n, l);
       for (int i = lane; i < count && at + i < most[k]; i += kWave)
-        lists[k][at + i] = k == 1 ? Item{of, row + i * kMidRows, min(rows - i * kMidRows, kMidRows), at}
-                                  : Item{of, row, rows, at};
+        lists[k][at + i] = k == 2 ? Item{of, row, rows, at}
+                                  : Item{of, row + i * high, min(rows - i * high, high), at};
     }
     done = int4{done.x + all.x, done.y + all.y, done.z + all.z, 0};
   }
@@ -126,8 +126,8 @@ static hipError_t launch_rows(const QuantiseArgs& p, hipStream_t stream) {
 template <typename T>
 static hipError_t launch_typed(const QuantiseArgs& p, hipStream_t stream) {
   if (p.k > 8192) return launch_rows<T, 1024, 8>(p, stream);
-  if (p.k > 4096 || p.tokens < 1024) return launch_rows<T, 256, 2>(p, stream);
-  return launch_rows<T, 64, 4>(p, stream);
+  if (p.k > 2048 || p.tokens < 1024) return launch_rows<T, 256, 2>(p, stream);
+  return launch_rows<T, 64, 2>(p, stream);
 }
 
 hipError_t launch_quantise(int dtype, const QuantiseArgs& p, hipStream_t stream) {

@@ -145,7 +145,7 @@ __global__ __launch_bounds__(256) void gather_kernel(RowsArgs p, int chunks) {
 
 // to_plain = the weighted sum of sorted rows, and the residual.
 template <typename T>
-__global__ __launch_bounds__(1024) void collect_kernel(RowsArgs p, int chunks) {
+__global__ __launch_bounds__(kWave) void collect_kernel(RowsArgs p, int chunks) {
   typedef typename T::raw raw;
   const int id = wave_of_grid(), r = id / chunks;
   if (r >= p.rows) return;
@@ -281,12 +281,10 @@ hipError_t launch_spread(int dtype, const RowsArgs& p, hipStream_t stream) {
 
 hipError_t launch_collect(int dtype, const RowsArgs& p, hipStream_t stream) {
   const int chunks = (p.width + kWaveCols - 1) / kWaveCols;
-  // a row's waves in one block, whose CU then reads whole rows
-  const int waves = (int64_t)p.rows * chunks < 4096 ? 1 : chunks < 16 ? chunks : 16;
-  const dim3 grid = grid_of(((int64_t)p.rows * chunks + waves - 1) / waves);
+  const dim3 grid = grid_of((int64_t)p.rows * chunks);
   return launch_kernel(dtype == BLOCK_BF16 ? collect_kernel<BF16> : dtype == BLOCK_F16 ? collect_kernel<F16>
                                                                                        : collect_kernel<F32>,
-                       grid, dim3(kWave * waves), stream, p, chunks);
+                       grid, dim3(kWave), stream, p, chunks);
 }
 
 }  // namespace experts

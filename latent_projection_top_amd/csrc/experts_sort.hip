@@ -22,7 +22,7 @@ namespace experts {
 using block::kWave;
 
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
-constexpr int kOne = 4 * kThreads, kRead = 64 * kThreads;
+constexpr int kOne = kThreads, kRead = 64 * kThreads;
 constexpr int kBlocks = 64;
 enum Counts { kOwn, kAll, kListed };  // of a block's own choices, of all, by the launch before
 
@@ -245,14 +245,11 @@ static hipError_t launch_most(const SortArgs& p, hipStream_t stream) {
   int* hist = static_cast<int*>(p.workspace);
   const dim3 blocks(p.choices <= kOne ? 1 : blocks_for(p.choices)), threads(kThreads);
   if (p.choices <= kOne)
-    return launch_kernel(p.choices <= kThreads ? place_kernel<Most, 1, kOwn> : place_kernel<Most, 4, kOwn>, blocks,
-                         threads, stream, p, nullptr);
+    return launch_kernel(place_kernel<Most, 1, kOwn>, blocks, threads, stream, p, nullptr);
   if (p.choices <= kRead) return launch_kernel(place_kernel<Most, 1, kAll>, blocks, threads, stream, p, nullptr);
   const hipError_t e = launch_kernel(count_kernel<Most>, blocks, threads, stream, p, hist);
   if (e != hipSuccess) return e;
-  const bool many = p.choices > (int64_t)kBlocks * 2 * kThreads;
-  return launch_kernel(many ? place_kernel<Most, 4, kListed> : place_kernel<Most, 1, kListed>, blocks, threads, stream,
-                       p, hist);
+  return launch_kernel(place_kernel<Most, 4, kListed>, blocks, threads, stream, p, hist);
 }
 
 hipError_t launch_sort(const SortArgs& p, hipStream_t stream) {

@@ -45,10 +45,8 @@ __device__ __forceinline__ void load16(const uint16_t* p, u32x4 (&v)[2], int cou
 
 // One item's columns from tile0 on, C column tiles of them, its split-th of
 // `splits` parts of the reduction, with RT tiles of 16 rows.
-// Whole: the reduction is whole blocks (the loads of rows that end inside one
-// are many instructions, which no other product should have to fetch).
-template <typename T, bool Gated, int C, int RT, bool Fused, bool Whole>
-__device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it, int tile0, int unit, int split,
+template <typename T, bool Gated, int C, int RT, bool Fused, bool Split>
+__device__ __forceinline__ void stream_part(const ProductArgs& p, const Item& it, int tile0, int unit, int split,
                                             int splits, Shared& shared) {
   constexpr int kPitch = 16 * C + 4;
   typedef int32_t Part[16 * RT][kPitch];
@@ -61,8 +59,8 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int lane = tid & (kWave - 1), g = lane >> 4, m = lane & 15;
   const int tiles = packed_tiles<Gated>(p);
-  const int b0 = (int)((int64_t)p.blocks * split / splits) + wave;
-  const int b1 = (int)((int64_t)p.blocks * (split + 1) / splits);
+  const int b0 = (Split ? (int)((int64_t)p.blocks * split / splits) : 0) + wave;
+  const int b1 = Split ? (int)((int64_t)p.blocks * (split + 1) / splits) : p.blocks;
   const int count = b1 > b0 ? (b1 - b0 + kWaves - 1) / kWaves : 0;
 
   const uint8_t* w[C];  // uniform; lanes are 16 bytes apart
@@ -79,36 +77,17 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     else
       q[r] = reinterpret_cast<const char*>(p.q) + ((int64_t)token[r] * p.blocks + b0) * kBlockRed + 16 * g;
   }
-  constexpr int kX = Fused ? 2 : 1;
   struct Step {
-    u32x4 w[C], x[RT][kX];
+    u32x4 w[C], x[RT];
   };
-  auto fetch_w = [&](Step& d, int i) __attribute__((always_inline)) {
+  auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
 #pragma unroll
     for (int c = 0; c < C; ++c)  // past the caches: no other block reads them (16 x 3584 x 65536: 56 us, like this 51)
       d.w[c] = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane)));
-  };
-  auto fetch_x = [&](Step& d, int i) __attribute__((always_inline)) {
+    if constexpr (!Fused)
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      if constexpr (Fused) {
-        const uint16_t* from = reinterpret_cast<const uint16_t*>(q[r]) + (int64_t)i * kWaves * kBlockRed;
-        const int b = b0 + i * kWaves;
-        if (Whole || (b + 1) * kBlockRed <= p.k) {
-          d.x[r][0] = reinterpret_cast<const block::Any16*>(from)->v;
-          d.x[r][kX - 1] = reinterpret_cast<const block::Any16*>(from + 8)->v;
-        } else {
-          load16(from, reinterpret_cast<u32x4(&)[2]>(d.x[r]), p.k - b * kBlockRed - 16 * g);
-        }
-      } else {
-        d.x[r][0] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
-      }
-    }
-  };
-  auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
-    fetch_w(d, i);
-    fetch_x(d, i);
+      for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
   };
 
   // A thread ends four columns of one row. What it needs for that is on its way
@@ -130,102 +109,66 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
   constexpr bool kRoom = C == 2;  // registers for them meanwhile
   if (kRoom) fetch_ends();
 
-  Quantiser z[Fused ? RT : 1];
   i32x4 acc[C][RT] = {};
   auto multiply = [&](const Step& d) __attribute__((always_inline)) {
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      u32x4 x;
-      if constexpr (Fused)
-        x = z[r].template sixteen<T>(d.x[r][0], d.x[r][kX - 1]);
-      else
-        x = d.x[r][0];
+    for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c][r] = mfma(d.w[c], x, acc[c][r]);
-    }
+      for (int c = 0; c < C; ++c) acc[c][r] = mfma(d.w[c], d.x[r], acc[c][r]);
   };
   // Depth steps are on their way at once, as many as there are registers for.
   constexpr int kDepth = C == 2 ? 4 : RT == 1 ? 3 : 2;
   Step d[kDepth];
   if constexpr (Fused) {
-    // The rows' largest magnitudes: of this wave's blocks (of all of them, also
-    // where the reduction is split), then of all. The first blocks' loads go out
-    // before the weights', behind which they would have to wait.
-    constexpr int kFirst = 4;
-    static_assert(kDepth <= kFirst, "");
-    u32x4 v[kFirst][RT][2];
-    auto look = [&](u32x4(&d)[RT][2], int b) __attribute__((always_inline)) {
+    // The rows' loads go out before the weights', behind which they would have
+    // to wait.
+    u32x4 v[kFusedSteps][2];
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
-        load16(reinterpret_cast<const uint16_t*>(q[r]) + (int64_t)(b - b0) * kBlockRed, d[r],
-               Whole ? 16 : p.k - b * kBlockRed - 16 * g);
-    };
-#pragma unroll
-    for (int i = 0; i < kFirst; ++i) look(v[i], min(wave + i * kWaves, p.blocks - 1));
+    for (int i = 0; i < kFusedSteps; ++i)
+      load16(reinterpret_cast<const uint16_t*>(q[0]) + i * kWaves * kBlockRed, v[i],
+             p.k - (wave + i * kWaves) * kBlockRed - 16 * g);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int s = 0; s < kDepth; ++s)
-      if (s < count) fetch_w(d[s], s);
+      if (s < count) fetch(d[s], s);
     __builtin_amdgcn_sched_barrier(0);
-    u16x2 most[RT];
+    // the rows' largest magnitudes: of this wave's blocks, then of all
+    u16x2 most = {0, 0};
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      most[r] = u16x2{0, 0};
-#pragma unroll
-      for (int i = 0; i < kFirst; ++i) most[r] = larger(larger(most[r], v[i][r][0]), v[i][r][1]);
-    }
-    if (splits == 1)  // they are the first steps' as well
-#pragma unroll
-      for (int s = 0; s < kDepth; ++s)
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          d[s].x[r][0] = v[s][r][0];
-          d[s].x[r][kX - 1] = v[s][r][1];
-        }
-    constexpr int kMore = Whole ? kFirst : 1;  // (see Whole)
-#pragma unroll 1
-    for (int b = wave + kFirst * kWaves; b < p.blocks; b += kMore * kWaves) {
-#pragma unroll
-      for (int i = 0; i < kMore; ++i) look(v[i], min(b + i * kWaves, p.blocks - 1));
-#pragma unroll
-      for (int r = 0; r < RT; ++r)
-#pragma unroll
-        for (int i = 0; i < kMore; ++i) most[r] = larger(larger(most[r], v[i][r][0]), v[i][r][1]);
-    }
-#pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      uint32_t a = max((uint32_t)most[r][0], (uint32_t)most[r][1]);
-      a = max(a, (uint32_t)__shfl_xor((int)a, 16));
-      a = max(a, (uint32_t)__shfl_xor((int)a, 32));
-      if (g == 0) shared.most[wave][16 * r + m] = a;
-    }
+    for (int i = 0; i < kFusedSteps; ++i) most = larger(larger(most, v[i][0]), v[i][1]);
+    uint32_t a = max((uint32_t)most[0], (uint32_t)most[1]);
+    a = max(a, (uint32_t)__shfl_xor((int)a, 16));
+    a = max(a, (uint32_t)__shfl_xor((int)a, 32));
+    if (g == 0) shared.most[wave][m] = a;
     __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS only: the weights are still on their way
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+    a = 0;
 #pragma unroll
-    for (int r = 0; r < RT; ++r) {
-      uint32_t a = 0;
+    for (int k = 0; k < kWaves; ++k) a = max(a, shared.most[k][m]);
+    const Quantiser z(magnitude<T>(a));
 #pragma unroll
-      for (int k = 0; k < kWaves; ++k) a = max(a, shared.most[k][16 * r + m]);
-      z[r] = Quantiser(magnitude<T>(a));
-    }
-#pragma unroll
-    for (int s = 0; s < kDepth; ++s)
-      if (s < count && splits > 1) fetch_x(d[s], s);
+    for (int i = 0; i < kFusedSteps; ++i)
+      if (i < count) {
+        d[i % kDepth].x[0] = z.template sixteen<T>(v[i][0], v[i][1]);
+        multiply(d[i % kDepth]);
+        __builtin_amdgcn_sched_barrier(0);
+        if (i + kDepth < count) fetch(d[i % kDepth], i + kDepth);
+      }
   } else {
 #pragma unroll
     for (int s = 0; s < kDepth; ++s)
       if (s < count) fetch(d[s], s);
-  }
 #pragma unroll 1
-  for (int i = 0; i < count; i += kDepth)
+    for (int i = 0; i < count; i += kDepth)
 #pragma unroll
-    for (int s = 0; s < kDepth; ++s)
-      if (i + s < count) {
-        multiply(d[s]);
-        __builtin_amdgcn_sched_barrier(0);
-        if (i + s + kDepth < count) fetch(d[s], i + s + kDepth);
-      }
+      for (int s = 0; s < kDepth; ++s)
+        if (i + s < count) {
+          multiply(d[s]);
+          __builtin_amdgcn_sched_barrier(0);
+          if (i + s + kDepth < count) fetch(d[s], i + s + kDepth);
+        }
+  }
 
   if (!kRoom) fetch_ends();
   // lane (g, m) holds row 16 r + m, columns 16 c + 4 g .. + 3
@@ -242,7 +185,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
   };
   bool mine = row < it.rows && col < p.n;
   int32_t* units = p.partial + (int64_t)unit * splits * kUnitInts;
-  if (splits > 1) {
+  if constexpr (Split) {
     if (tid < it.rows * kQuads) {
       const i32x4 v = sums(tid / kQuads, tid % kQuads);
 #pragma unroll
@@ -271,7 +214,7 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
     if (!Gated && p.residual != nullptr)
       load_values<T, 4>(static_cast<const uint16_t*>(p.residual) + r * p.ldr + col, residual, p.n - col);
     i32x4 v = {}, u = {};
-    if (splits > 1) {
+    if constexpr (Split) {
       const int32_t* from = units + 4 * (row * kQuads + quad);
       for (int s = 0; s < splits; ++s)
 #pragma unroll
@@ -296,6 +239,15 @@ __device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it
   __syncthreads();  // before the next item's sums
 }
 
+template <typename T, bool Gated, int C, int RT>
+__device__ __forceinline__ void stream_item(const ProductArgs& p, const Item& it, int tile0, int unit, int split,
+                                            int splits, Shared& shared) {
+  if (splits > 1)
+    stream_part<T, Gated, C, RT, false, true>(p, it, tile0, unit, split, splits, shared);
+  else
+    stream_part<T, Gated, C, RT, false, false>(p, it, tile0, unit, 0, 1, shared);
+}
+
 // How many blocks share a unit of work: parts of at least four steps of a wave,
 // since a join costs 2 to 3 us, and a step some 0.4.
 __device__ __forceinline__ int splits_of(int units, int blocks) {
@@ -315,14 +267,14 @@ void stream_kernel(ProductArgs p) {
     const int i = u / groups, tile0 = (u - i * groups) * C;
     const Item it = listed ? p.lists.brief[i] : Item{0, 0, p.rows, 0};
     if (it.rows <= 16)
-      stream_item<T, Gated, C, 1, false, true>(p, it, tile0, u, split, splits, shared);
+      stream_item<T, Gated, C, 1>(p, it, tile0, u, split, splits, shared);
     else
-      stream_item<T, Gated, C, 2, false, true>(p, it, tile0, u, split, splits, shared);
+      stream_item<T, Gated, C, 2>(p, it, tile0, u, split, splits, shared);
   }
 }
 
 // The same from the rows as they are, in items of up to kFusedItem of them.
-template <typename T, bool Gated, int C, bool Whole>
+template <typename T, bool Gated, int C>
 __global__ __launch_bounds__(kThreads) __attribute__((amdgpu_waves_per_eu(4, 4)))
 void fused_kernel(ProductArgs p) {
   __shared__ __attribute__((aligned(16))) Shared shared;
@@ -358,15 +310,14 @@ void fused_kernel(ProductArgs p) {
     }
     items = min(items, kFusedRows);
   }
-  const int tiles = packed_tiles<Gated>(p), wide = (tiles + C - 1) / C;
-  const int total = items * wide, splits = splits_of(total, p.blocks);
-  for (int at = blockIdx.x; at < total * splits; at += gridDim.x) {
-    const int u = at / splits, split = at - u * splits, i = u / wide, tile0 = (u - i * wide) * C;
+  const int groups = (packed_tiles<Gated>(p) + C - 1) / C, total = items * groups;
+  for (int u = blockIdx.x; u < total; u += gridDim.x) {
+    const int i = u / groups, tile0 = (u - i * groups) * C;
     Item it{0, 0, p.rows, 0};
     if (p.offsets != nullptr)
       it = Item{__builtin_amdgcn_readfirstlane(list[i].expert), __builtin_amdgcn_readfirstlane(list[i].row),
                 __builtin_amdgcn_readfirstlane(list[i].rows), 0};
-    stream_item<T, Gated, C, 1, true, Whole>(p, it, tile0, u, split, splits, shared);
+    stream_part<T, Gated, C, 1, true, false>(p, it, tile0, u, 0, 1, shared);
   }
 }
 
@@ -374,15 +325,11 @@ void fused_kernel(ProductArgs p) {
 template <typename T, bool Gated>
 static hipError_t launch_typed(const ProductArgs& p, bool fused, hipStream_t stream) {
   const int64_t tiles = (Gated ? 2 : 1) * column_tiles(p.n);
-  const int64_t items = p.offsets != nullptr ? most_brief(p.rows, p.experts) : 1;
+  const int64_t items = p.offsets != nullptr ? most_live(p.rows, p.experts) : 1;
   const dim3 grid(512), block(kThreads);
-  const bool narrow = items * tiles <= 512 * 2;
-  if (fused && p.k % kBlockRed == 0)
-    return launch_kernel(narrow ? fused_kernel<T, Gated, 2, true> : fused_kernel<T, Gated, 4, true>, grid, block,
-                         stream, p);
+  const bool narrow = items * tiles <= 512;
   if (fused)
-    return launch_kernel(narrow ? fused_kernel<T, Gated, 2, false> : fused_kernel<T, Gated, 4, false>, grid, block,
-                         stream, p);
+    return launch_kernel(narrow ? fused_kernel<T, Gated, 2> : fused_kernel<T, Gated, 4>, grid, block, stream, p);
   return launch_kernel(narrow ? stream_kernel<T, Gated, 2> : stream_kernel<T, Gated, 4>, grid, block, stream, p);
 }
 

@@ -359,7 +359,7 @@ __device__ __forceinline__ void mid_items(const ProductArgs& p, char* smem, int 
 
 template <typename T, bool Gated>
 __global__ __launch_bounds__(kWave * kWaves) __attribute__((amdgpu_waves_per_eu(2, 2)))
-void tile_kernel(ProductArgs p, int way) {
+void tile_kernel(ProductArgs p, Way way) {
   __shared__ __attribute__((aligned(1024))) char smem[kLds];
   const bool listed = p.lists.counts != nullptr;
   const int xcd = blockIdx.x & 7, per = gridDim.x >> 3;
@@ -418,11 +418,11 @@ void tile_kernel(ProductArgs p, int way) {
 }
 
 template <typename T, bool Gated>
-static hipError_t launch_typed(const ProductArgs& p, int way, hipStream_t stream) {
+static hipError_t launch_typed(const ProductArgs& p, Way way, hipStream_t stream) {
   return launch_kernel(tile_kernel<T, Gated>, dim3(256), dim3(kWave * kWaves), stream, p, way);
 }
 
-hipError_t launch_tiles(int dtype, const ProductArgs& p, int way, hipStream_t stream) {
+hipError_t launch_tiles(int dtype, const ProductArgs& p, Way way, hipStream_t stream) {
   if (dtype == BLOCK_BF16)
     return p.gated ? launch_typed<BF16, true>(p, way, stream) : launch_typed<BF16, false>(p, way, stream);
   return p.gated ? launch_typed<F16, true>(p, way, stream) : launch_typed<F16, false>(p, way, stream);
