@@ -119,7 +119,8 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   a.experts = c.experts;
   a.offsets = offsets;
   const int column_tiles = planes * experts::column_tiles(c.outputs);
-  if (experts::is_fused(rows, c.experts, column_tiles, a.blocks, offsets != nullptr))
+  const experts::Way way = experts::way_of(rows, c.experts, column_tiles, a.blocks, offsets != nullptr);
+  if (experts::is_fused(way, rows, c.experts, a.blocks, offsets != nullptr))
     return status_of(experts::launch_stream(c.dtype, a, true, s));
   experts::QuantiseArgs z{};
   z.x = a.x;
@@ -133,7 +134,6 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.stride = a.blocks * experts::kBlockRed;
   z.experts = c.experts;
   z.rows = rows;
-  const experts::Way way = experts::way_of(rows, c.experts, column_tiles, a.blocks, offsets != nullptr);
   z.way = way;
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);

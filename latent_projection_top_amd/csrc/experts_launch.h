@@ -78,7 +78,6 @@ struct Item {
   int32_t expert, row, rows, first;
 };
 constexpr int kStreamRows = 32, kMidRows = 64, kTileRows = 256;
-constexpr int kBriefRows = 512;  // the most rows of kBrief by expert
 constexpr int kMidCols = 4, kTileCols = 16;  // packed column tiles of 16 that each takes
 struct Lists {
   const int32_t* counts;  // brief, mid, tiles; NULL: one expert has every row
@@ -102,17 +101,23 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
   return Lists{&items->expert, items + 1, mid, mid + most_mid(rows, experts)};
 }
 
-// The way of a product of `rows` rows. kFew where its modelled time in us is less
-// than the tiles': a mid item's is mostly latency; many wait for each other, 256
-// at a time, or for their operands, 8 KB for each block of the reduction, which
-// the L2s deliver at 8 TB/s; tiles come in rounds of 256, and by expert with
-// another launch before them. (By expert mid items as many, and tiles as few, as
-// there can be.) Where the weights are more than the last-level cache holds,
-// streaming the short experts' in a kernel of its own is worth a launch (112
-// experts of 3584 x 4096, 1.6 GB: 260 us, together 302; 33 of 253 x 320, 3 MB:
-// 26 and 22).
+// The way of a product of `rows` rows.
+//   kBrief where experts have few rows on average: weights that a few items read
+// again come from the caches (gated, in us, this and the next best: 1024 x 16 of
+// 896 experts of 512 x 256, 18 rows to each, 75 and 103; 96 x 16 of 64, 24 to
+// each, 2048 x 2048, 102 and 115; 30 to each 127 and 113).
+//   kFew where its modelled time in us is less than the tiles' (256 x 3584 x 7168:
+// 27 and 52; 40 x 2048 x 2048: 11 and 17; 333 x 6 of 40 experts of 1019 x 777: 25
+// and 33): a mid item's is mostly latency; many wait for each other, 256 at a
+// time, or for their operands, 8 KB for each block of the reduction, which the L2s
+// deliver at 8 TB/s; tiles come in rounds of 256, and by expert with another
+// launch before them. (By expert mid items as many, and tiles as few, as there can
+// be.)
+//   kApart where the weights are more than the last-level cache holds: streaming
+// the short experts' in a kernel of its own is worth a launch (112 experts of 3584
+// x 4096, 1.6 GB: 260 us, together 302; 33 of 253 x 320, 3 MB: 26 and 22).
 inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
-  if (rows <= kStreamRows || (offsets && rows <= kBriefRows && rows <= 8 * (int64_t)experts)) return kBrief;
+  if (rows <= kStreamRows || (offsets && rows <= 24 * (int64_t)experts)) return kBrief;
   const int64_t mids = (rows + kMidRows - 1) / kMidRows + (offsets ? most_live(rows, experts) : 0);
   const int64_t tiles = (rows + kTileRows - 1) / kTileRows;
   const int64_t m = mids * ((column_tiles + kMidCols - 1) / kMidCols);
@@ -126,13 +131,17 @@ inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool 
   return offsets && bytes > 256e6 ? kApart : kTogether;
 }
 
-// Few rows of few columns of a short reduction: the streaming kernel makes the
-// integers by itself, in items of up to kFusedItem rows, for every item again.
-constexpr int kFusedItem = 16, kFusedRows = 128, kFusedSteps = 4;
-inline bool is_fused(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
-  if (blocks > 8 * kFusedSteps) return false;
-  if (!offsets) return rows <= kFusedItem && column_tiles <= 2048;
-  return rows <= kFusedRows && rows <= 8 * (int64_t)experts && most_live(rows, experts) * column_tiles <= 8192;
+// Few rows of a short reduction: the streaming kernel makes the integers by
+// itself, in items of up to kFusedItem rows, for every item again, which saves a
+// launch (8 x 512 x 7168: 5.0 us and 6.7; 8 x 2048 x 7168: 7.4 and 8.0; gated 32
+// x 16 of 64 experts, 2048 x 512: 26.2 and 27.2), but costs more than that in
+// longer rows (8 x 3584 x 7168: 10.8 and 10.0; 8 x 7168 x 7168: 18.2 and 14.8) and
+// where experts have more rows than an item (30 x 16 of 20, 2048 x 1024: 30 and 22).
+constexpr int kFusedItem = 16, kFusedRows = 512, kFusedSteps = 4;
+inline bool is_fused(Way way, int64_t rows, int experts, int blocks, bool offsets) {
+  if (way != kBrief || blocks > 8 * kFusedSteps) return false;
+  return rows <= kFusedItem ||
+         (offsets && (rows <= kStreamRows || (rows <= kFusedRows && rows <= kFusedItem * (int64_t)experts)));
 }
 
 // What the streaming kernel uses of the workspace: counters of its column

@@ -126,7 +126,7 @@ static hipError_t launch_rows(const QuantiseArgs& p, hipStream_t stream) {
 template <typename T>
 static hipError_t launch_typed(const QuantiseArgs& p, hipStream_t stream) {
   if (p.k > 8192) return launch_rows<T, 1024, 8>(p, stream);
-  if (p.k > 2048 || p.tokens < 1024) return launch_rows<T, 256, 2>(p, stream);
+  if (p.k > 2048) return launch_rows<T, 256, 2>(p, stream);
   return launch_rows<T, 64, 2>(p, stream);
 }
 

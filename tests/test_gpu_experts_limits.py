@@ -25,6 +25,26 @@ def test_weights_past_the_last_cache(planes, act, tokens, dtype):
                     residual=planes == 1, seed=1, spare=5).check(experts, "large")
 
 
+@pytest.mark.parametrize("planes,act,tokens", [(1, "silu", 0), (2, "gelu", 900)])
+def test_many_rows_of_weights_past_the_last_cache(planes, act, tokens):
+    """The same with more than 24 rows to an expert on average."""
+    log(f"large weights, many rows {planes}")
+    counts = [1, 0, 2, 31, 32, 33, 700, 17, 16, 1200, 0, 128, 129, 9, 600]
+    counts += [0] * ((66 if planes == 1 else 34) - len(counts) - 1) + [60]
+    kit.ProductCase(planes, 2048, 2040, act, BF, counts=counts, tokens=tokens, bias=planes == 1,
+                    residual=planes == 1, seed=3, spare=5).check(experts, "large")
+
+
+@pytest.mark.parametrize("counts", [[24], [5, 19, 0, 40], [16] * 32, [17] * 30, [0, 50] * 10, [24] * 20,
+                                    [100] + [1] * 40, [513] + [0] * 30, [33, 65, 97, 129] + [0] * 20])
+@pytest.mark.parametrize("k", [520, 2048, 2056])
+def test_experts_of_few_rows_on_average(counts, k):
+    """Some of them with more than an item's: they become several."""
+    log(f"brief {counts} {k}")
+    for planes, act in ((1, "none"), (2, "silu")):
+        kit.ProductCase(planes, k, 72, act, BF, counts=counts, tokens=99, seed=k).check(experts, f"{counts}")
+
+
 @pytest.mark.parametrize("planes,act", [(1, "relu"), (2, "gelu_tanh")])
 def test_many_rows_of_small_experts(planes, act):
     """Enough rows for tiles: short experts follow them in the same launch."""
