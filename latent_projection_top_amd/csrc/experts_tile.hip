@@ -9,15 +9,21 @@
 // one is read into registers while the one before is multiplied, the others are
 // on their way from memory. Rows lie in LDS as 64-byte lines with a swizzle,
 // weights as the packed form has them, so that neither read meets a bank
-// conflict. There is a body for 64, 128, 192 and 256 rows. The weights of an
-// expert with one row tile pass by the caches (64 rows of 3584 x 65536: 53 us,
-// like this 46; 256 rows: 74 and 70; where row tiles share them it costs 4 %).
+// conflict. There is a body for 64, 128, 192 and 256 rows (160 rows of 3584 x
+// 65536: 60 us, in the next larger one 63; 64 rows 53, in the largest 56). The
+// weights of an expert with one row tile pass by the caches (64 rows of 3584 x
+// 65536: 45 us, else 53; where row tiles share them it costs 4 %).
+//   2048 x 3584 x 7168: 58 us, 1.8 POP/s, 224 tiles of 256 CUs, whose matrix cores
+// are busy half of the time: a stage of 256 rows takes 0.67 us, of which the
+// MFMAs are 0.43, and 13 us go into start and ending, which nothing overlaps. 8192 x
+// 8192 x 8192: 464 us, 2.37 POP/s.
 //
 // mid items, where there are few tiles, or after them: up to 64 rows by 64
 // columns, the reduction dealt to the eight waves, whose operands come straight
 // from memory and whose sums meet in LDS: half of the matrix cores' rate at
 // best, but an eighth of the steps one after another, which is what the time is
-// made of there. The next item's first operands are on their way while one ends.
+// made of there (256 x 3584 x 7168: 26 us, as 28 tiles 52). The next item's first
+// operands are on their way while one ends.
 #include "experts_device.h"
 #include "lds_device.h"
 
@@ -373,7 +379,8 @@ void tile_kernel(ProductArgs p, Way way) {
   // range of tiles, which its blocks go through in turn.
   const int begin = (int)((int64_t)total * xcd / 8), end = (int)((int64_t)total * (xcd + 1) / 8);
   for (int at = begin + slot; at < end; at += per) {
-    // row tiles of an expert in groups of 8, column by column
+    // row tiles of an expert in groups of 8, column by column (8192 x 8192 x 8192:
+    // 464 us, without groups 510; 2048 x 3584 x 7168: 58.7 and 60.1)
     const Item it = listed ? p.lists.tiles[at / ntiles] : Item{0, 0, p.rows, 0};
     const int high = (it.rows + kTileRows - 1) / kTileRows;  // its row tiles
     const int local = at - it.first * ntiles;
