@@ -15,7 +15,8 @@
 // all for itself, in the same launch (32752 choices of 112 of 896 experts: 6.6 us,
 // with a launch for the counts 8.1; 65536 of 896: 10.2 and 12.0; 131072: 17.0 and
 // 14.8). Of more, a first launch counts each block's, and in the second every block
-// adds up what the others have (262144: 17.3 us; 2^20: 42).
+// adds up what the others have (262144: 17.3 us, with twice the blocks 21.5; 2^20:
+// 42 and 33, so it has them there).
 #include "block_device.h"
 #include "experts_launch.h"
 
@@ -25,8 +26,8 @@ using block::kWave;
 
 constexpr int kThreads = 1024, kWaves = kThreads / kWave;
 constexpr int kOne = kThreads, kRead = 64 * kThreads;
-constexpr int kBlocks = 64;
-enum Counts { kOwn, kAll, kListed };  // of a block's own choices, of all, by the launch before
+constexpr int kBlocks = 128, kSome = 64, kMany = 512 * kThreads;  // kSome blocks up to kMany choices
+enum Counts { kOwn, kAll, kListed, kLonger };  // of its own choices, of all, listed for kSome or kBlocks blocks
 
 // An id counted from `first`, in unsigned arithmetic: below `experts` if it is one
 // of them. (Negative ids are all one: -1 - first is never small.)
@@ -134,23 +135,24 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
       mine[i] = e < p.experts ? before[i] + after[e] : 0;
     }
     scan();
-  } else if constexpr (From == kListed) {
+  } else if constexpr (From == kListed || From == kLonger) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int e = min(kMine * t + i, p.experts - 1);
-      int n[kBlocks];
+#pragma unroll 1
+      for (int g = 0; g < (From == kListed ? kSome : (int)gridDim.x); g += kSome) {
+        int n[kSome];
 #pragma unroll
-      for (int b = 0; b < kBlocks; ++b) n[b] = hist[min(b, (int)gridDim.x - 1) * p.experts + e];
-      // (which blocks there are, and come before, is the same for all lanes)
-      if (kMine * t + i < p.experts) {
+        for (int b = 0; b < kSome; ++b) n[b] = hist[min(g + b, (int)gridDim.x - 1) * p.experts + e];
+        // (which blocks there are, and come before, is the same for all lanes)
 #pragma unroll
-        for (int b = 0; b < kBlocks; ++b)
-          if (b < (int)blockIdx.x)
+        for (int b = 0; b < kSome; ++b)
+          if (g + b < (int)blockIdx.x)
             before[i] += n[b];
-          else if (b < (int)gridDim.x)
+          else if (g + b < (int)gridDim.x)
             mine[i] += n[b];
-        mine[i] += before[i];
       }
+      mine[i] = kMine * t + i < p.experts ? mine[i] + before[i] : 0;
     }
     scan();
   }
@@ -235,7 +237,8 @@ __global__ __launch_bounds__(kThreads) void place_kernel(SortArgs p, const int* 
 }
 
 static int blocks_for(int64_t choices) {
-  return (int)((choices + kThreads - 1) / kThreads < kBlocks ? (choices + kThreads - 1) / kThreads : kBlocks);
+  const int64_t most = choices <= kMany ? kSome : kBlocks, rounds = (choices + kThreads - 1) / kThreads;
+  return (int)(rounds < most ? rounds : most);
 }
 
 size_t sort_workspace_bytes(int64_t choices, int experts) {
@@ -251,7 +254,8 @@ static hipError_t launch_most(const SortArgs& p, hipStream_t stream) {
   if (p.choices <= kRead) return launch_kernel(place_kernel<Most, 1, kAll>, blocks, threads, stream, p, nullptr);
   const hipError_t e = launch_kernel(count_kernel<Most>, blocks, threads, stream, p, hist);
   if (e != hipSuccess) return e;
-  return launch_kernel(place_kernel<Most, 4, kListed>, blocks, threads, stream, p, hist);
+  return launch_kernel(blocks.x <= kSome ? place_kernel<Most, 4, kListed> : place_kernel<Most, 4, kLonger>, blocks,
+                       threads, stream, p, hist);
 }
 
 hipError_t launch_sort(const SortArgs& p, hipStream_t stream) {

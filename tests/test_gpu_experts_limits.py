@@ -234,3 +234,51 @@ def test_weights_made_on_another_stream():
     at = w8_s.data_ptr()
     del w8_s
     assert torch.empty_like(w8).data_ptr() != at
+
+
+@pytest.mark.parametrize("rows,topk,experts_,first", [(32768, 16, 900, 0), (32769, 16, 900, 3), (40000, 16, 3000, 500),
+                                                      (1 << 20, 16, 4096, 0)])
+def test_sort_of_many_choices(rows, topk, experts_, first):
+    """On both sides of where it takes more blocks, and the most choices."""
+    log(f"sort {rows}x{topk} {experts_}")
+    ids = torch.randint(0, 4096, (rows, topk), generator=torch.Generator().manual_seed(rows), dtype=torch.int32).cuda()
+    plan = experts.SortPlan(rows, topk, experts_, first=first)
+    capacity = rows * topk - 5
+    out = [torch.empty(s, dtype=torch.int32, device="cuda") for s in ((experts_ + 1,), (rows, topk), (capacity,))]
+    ws = plan.new_workspace()
+    for _ in range(2):
+        experts.sort(plan, ids, *out, ws)
+    torch.cuda.synchronize()
+    offsets, place, token = kit.sort_reference(ids, experts_, first, capacity)
+    assert (out[0].cpu().numpy() == offsets).all() and (out[1].cpu().numpy() == place).all()
+    assert (out[2].cpu().numpy()[:token.size] == token).all()
+
+
+def test_graphs_that_share_a_workspace():
+    """Calls of 8, 40 and 300 rows of one plan, captured into a graph each with
+    the same workspace and replayed in turn, eager calls in between."""
+    log("graphs, one workspace")
+    c = kit.ProductCase(1, 8192, 136, "gelu", BF, rows=300, bias=True, residual=True, seed=11)
+    plan = c.plan(experts)
+    packed, ws = experts.pack(plan, *c.w), plan.new_workspace()
+    ref, bound = c.reference()
+    graphs = []
+    for rows in (8, 40, 300):
+        y = torch.zeros(300, 136, dtype=BF, device="cuda")
+        c.run(experts, plan, packed, y, ws, rows=rows)
+        torch.cuda.synchronize()
+        bk.check(y[:rows], ref[:rows], bound[:rows], None, BF, f"{rows} rows")
+        got = torch.zeros_like(y)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            c.run(experts, plan, packed, got, ws, rows=rows)
+        graphs.append((graph, got, y))
+    eager = torch.empty_like(y)
+    for i in (0, 1, 2, 0, 0, 2, 1):
+        graph, got, want = graphs[i]
+        got.zero_()
+        graph.replay()
+        c.run(experts, plan, packed, eager, ws, rows=20)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want), i
+    assert not ws[:experts.WORKSPACE_ZEROED].any()
