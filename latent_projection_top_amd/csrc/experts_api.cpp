@@ -134,6 +134,7 @@ int run_product(const Product8& c, const void* x, int64_t x_stride, const void* 
   z.stride = a.blocks * experts::kBlockRed;
   z.experts = c.experts;
   z.rows = rows;
+  z.sorted = offsets != nullptr && token == nullptr;
   z.way = way;
   z.most_brief = (int)experts::most_brief(rows, c.experts);
   z.most_mid = (int)experts::most_mid(rows, c.experts);

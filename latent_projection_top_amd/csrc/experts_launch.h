@@ -178,6 +178,7 @@ struct QuantiseArgs {
   Item* area;
   int64_t ldx;
   int tokens, k, stride, experts, rows;
+  bool sorted;  // x has a row for each row of y
   Way way;
   int most_brief, most_mid, most_tiles;
 };

@@ -79,9 +79,13 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
     if (block == blocks && p.offsets != nullptr) make_lists(p);
     return;
   }
+  // rows behind the last expert's are nobody's (65536 rows of 2048 of which an
+  // eighth is kept, and their products of 512 columns: 103 us with them, 43)
+  const int tokens = p.sorted ? min(p.offsets[p.experts], p.tokens) : p.tokens;
+  if (block * kRowsPer >= tokens) return;
   const int t = threadIdx.x % Threads, row = block * kRowsPer + threadIdx.x / Threads;
-  const bool live = row < p.tokens;
-  const uint16_t* in = p.x + (int64_t)(live ? row : p.tokens - 1) * p.ldx;
+  const bool live = row < tokens;
+  const uint16_t* in = p.x + (int64_t)(live ? row : tokens - 1) * p.ldx;
   u32x4 v[Groups][2];
 #pragma unroll
   for (int i = 0; i < Groups; ++i)

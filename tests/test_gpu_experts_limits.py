@@ -282,3 +282,23 @@ def test_graphs_that_share_a_workspace():
         torch.cuda.synchronize()
         assert torch.equal(got, want), i
     assert not ws[:experts.WORKSPACE_ZEROED].any()
+
+
+@pytest.mark.parametrize("counts,spare", [([3, 0, 9, 1], 20), ([30, 2, 0, 7] * 8, 1), ([30, 2, 0, 7] * 8, 3000),
+                                          ([200, 0, 33, 300], 5000), ([0, 0, 0], 4000)])
+def test_rows_behind_the_last_experts(counts, spare):
+    """A rank's share of the choices: most rows are nobody's, whatever they and
+    the workspace hold."""
+    log(f"spare {counts} {spare}")
+    for k, n in ((330, 90), (2100, 264)):
+        c = kit.ProductCase(1, k, n, "silu", BF, counts=counts, bias=True, residual=True, seed=12, spare=spare)
+        c.x[c.kept:] = float("nan")
+        plan = c.plan(experts)
+        packed, ws = experts.pack(plan, *c.w), plan.new_workspace()
+        ws[experts.WORKSPACE_ZEROED:] = 255
+        y = torch.full((c.rows, n), 7.0, dtype=BF, device="cuda")
+        c.run(experts, plan, packed, y, ws)
+        torch.cuda.synchronize()
+        ref, bound = c.reference()
+        bk.check(y[:c.kept], ref, bound, None, BF, "kept rows")
+        assert (y[c.kept:] == 7).all()
