@@ -52,8 +52,10 @@
  *
  * Any size and element-aligned pointer is accepted; row strides are as in
  * block.h. `place`, `token` and `offsets` are read on the device and not
- * trusted: entries out of range are dropped (place), clamped (token) or cut to
- * 0..rows (offsets), so that no access leaves the buffers.
+ * trusted: entries out of range are dropped (place), clamped (token) or cut
+ * (offsets: the last to 0..rows, the others to 0 and the last), so that no
+ * access leaves the buffers. Rows that the ranges of several experts hold get no
+ * defined values.
  *
  * Ownership, threading, capture: as in block.h. Run calls only enqueue kernels
  * on `stream` and can be captured into a HIP graph. The first

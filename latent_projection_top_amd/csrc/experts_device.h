@@ -37,6 +37,20 @@ __device__ __forceinline__ int token_of(const ProductArgs& p, int row) {
   return p.token != nullptr ? min(max(p.token[row], 0), p.tokens - 1) : row;
 }
 
+// The rows that expert e has: its range of `offsets`, cut to `end`, the rows that
+// there are before offsets[experts], behind which they are nobody's (their
+// integers are not made).
+struct Range {
+  int first, rows;
+};
+__device__ __forceinline__ int end_of_rows(const int32_t* offsets, int experts, int rows) {
+  return min(max(offsets[experts], 0), rows);
+}
+__device__ __forceinline__ Range range_of(const int32_t* offsets, int e, int end) {
+  const int first = min(max(offsets[e], 0), end);
+  return Range{first, max(min(max(offsets[e + 1], 0), end) - first, 0)};
+}
+
 // `count` (less than eight) consecutive 16-bit values, zeros after them. Every
 // load is of a value that is there, so that they go out together: one by one
 // where the row's end says so, each would be waited for (7 us a row's end).

@@ -20,14 +20,11 @@ __device__ __forceinline__ void make_lists(const QuantiseArgs& p) {
   const int t = threadIdx.x, lane = t & (kWave - 1), wave = t / kWave;
   Item* lists[3] = {p.area + 1, p.area + 1 + p.most_brief, p.area + 1 + p.most_brief + p.most_mid};
   const int most[3] = {p.most_brief, p.most_mid, p.most_tiles};
+  const int end = end_of_rows(p.offsets, p.experts, p.rows);
   int4 done = {0, 0, 0, 0};
   for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
     const int e = e0 + t;
-    int first = 0, n = 0;
-    if (t < kThreads && e < p.experts) {
-      first = min(max(p.offsets[e], 0), p.rows);
-      n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
-    }
+    const auto [first, n] = t < kThreads && e < p.experts ? range_of(p.offsets, e, end) : Range{0, 0};
     // this thread's items: how many, of which list
     const int kind = p.way == kBrief ? 0 : p.way == kFew ? 1 : n > kStreamRows ? 2 : p.way == kTogether ? 1 : 0;
     const int height = kind == 0 ? kStreamRows : kind == 1 ? kMidRows : kTileRows;
@@ -81,7 +78,7 @@ __global__ __launch_bounds__(Threads < kThreads ? kThreads : Threads) void quant
   }
   // rows behind the last expert's are nobody's (65536 rows of 2048 of which an
   // eighth is kept, and their products of 512 columns: 103 us with them, 43)
-  const int tokens = p.sorted ? min(p.offsets[p.experts], p.tokens) : p.tokens;
+  const int tokens = p.sorted ? end_of_rows(p.offsets, p.experts, p.rows) : p.tokens;
   if (block * kRowsPer >= tokens) return;
   const int t = threadIdx.x % Threads, row = block * kRowsPer + threadIdx.x / Threads;
   const bool live = row < tokens;

@@ -290,13 +290,10 @@ void fused_kernel(ProductArgs p) {
   int items = 1;
   if (p.offsets != nullptr) {
     items = 0;
+    const int end = end_of_rows(p.offsets, p.experts, p.rows);
     for (int e0 = 0; e0 < p.experts; e0 += kThreads) {
       const int e = e0 + t;
-      int first = 0, n = 0;
-      if (e < p.experts) {
-        first = min(max(p.offsets[e], 0), p.rows);
-        n = max(min(max(p.offsets[e + 1], 0), p.rows) - first, 0);
-      }
+      const auto [first, n] = e < p.experts ? range_of(p.offsets, e, end) : Range{0, 0};
       const int m = (n + kFusedItem - 1) / kFusedItem;
       int run = m;
       for (int d = 1; d < kWave; d *= 2) {
