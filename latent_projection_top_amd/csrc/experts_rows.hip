@@ -157,25 +157,28 @@ __global__ __launch_bounds__(kWave) void collect_kernel(RowsArgs p, int chunks) 
   const int id = wave_of_grid(), r = id / chunks;
   if (r >= p.rows) return;
   const int c = (id - r * chunks) * kWaveCols + kLaneCols * (threadIdx.x & (kWave - 1)), count = p.width - c;
+  const bool inside = count > 0;  // lanes past the row's end stay: places and weights are read out of them
   Choices k(p, r, p.weights);
-  if (count <= 0) return;
   Cols<T> res;
-  if (p.residual != nullptr) res.load(static_cast<const raw*>(p.residual) + r * p.ld_residual + c, count);
+  if (inside && p.residual != nullptr) res.load(static_cast<const raw*>(p.residual) + r * p.ld_residual + c, count);
   float sum[8] = {};
   while (k.live != 0) {
     int at[kGroup], which[kGroup];
     float w[kGroup];
     Cols<T> v[kGroup];
     const int n = k.next(at, w, which);
+    if (inside) {
 #pragma unroll
-    for (int q = 0; q < kGroup; ++q)
-      v[q].template load<true>(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
+      for (int q = 0; q < kGroup; ++q)
+        v[q].template load<true>(static_cast<const raw*>(p.sorted) + at[q] * p.ld_sorted + c, count);
 #pragma unroll
-    for (int q = 0; q < kGroup; ++q)
-      if (q < n)
+      for (int q = 0; q < kGroup; ++q)
+        if (q < n)
 #pragma unroll
-        for (int t = 0; t < 8; ++t) sum[t] = fmaf(w[q], v[q].get(t), sum[t]);
+          for (int t = 0; t < 8; ++t) sum[t] = fmaf(w[q], v[q].get(t), sum[t]);
+    }
   }
+  if (!inside) return;
   if (p.residual != nullptr)
 #pragma unroll
     for (int t = 0; t < 8; ++t) sum[t] += res.get(t);

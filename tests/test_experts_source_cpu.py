@@ -1,0 +1,33 @@
+"""What the routed half's kernels rest on, read in their sources: the built
+kernels may have it right by chance."""
+import os
+import re
+
+CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "latent_projection_top_amd", "csrc")
+
+
+def kernels(name):
+    """{kernel: body without comments} of a source."""
+    src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+    out = {}
+    for m in re.finditer(r"\bvoid (\w+_kernel)\([^{;]*\)\s*\{", src):
+        depth, end = 1, m.end()
+        while depth:
+            depth += {"{": 1, "}": -1}.get(src[end], 0)
+            end += 1
+        out[m.group(1)] = src[m.end():end]
+    return out
+
+
+def test_lanes_that_hold_choices_stay_until_they_are_read():
+    """Places and weights are read out of the lanes that hold them, one choice
+    to a lane whatever the row's width: no lane may leave between the two."""
+    bodies = kernels("experts_rows.hip")
+    assert {"gather_kernel", "collect_kernel", "backward_kernel"} <= set(bodies)
+    for name, body in bodies.items():
+        if "Choices k(" not in body:
+            continue
+        held = body[body.index("Choices k("):]
+        reads = [m.end() for m in re.finditer(r"k\.next\(|readlane\(", held)]
+        assert reads, name
+        assert not re.search(r"\breturn\b", held[:reads[-1]]), name
