@@ -114,7 +114,8 @@ struct Choices {
   }
   // the next kGroup live ones, the last of them repeated; returns how many
   __device__ __forceinline__ int next(int (&at)[kGroup], float (&w)[kGroup], int (&which)[kGroup]) {
-    const int n = min(__popcll(live), kGroup);
+    // (a scalar of its own: compared in 64 bits, 8 x 16 x 7168 takes 4.1 us instead of 4.0)
+    const int n = __builtin_amdgcn_readfirstlane(min((int)__popcll(live), kGroup));
     int j = 0;
 #pragma unroll
     for (int q = 0; q < kGroup; ++q) {

@@ -2,6 +2,12 @@
 kernels may have it right by chance."""
 import os
 import re
+import shutil
+import subprocess
+
+import pytest
+
+from latent_projection_top_amd import build
 
 CSRC = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "latent_projection_top_amd", "csrc")
 
@@ -31,3 +37,16 @@ def test_lanes_that_hold_choices_stay_until_they_are_read():
         reads = [m.end() for m in re.finditer(r"k\.next\(|readlane\(", held)]
         assert reads, name
         assert not re.search(r"\breturn\b", held[:reads[-1]]), name
+
+
+@pytest.mark.skipif(shutil.which(build.HIPCC) is None, reason="no hipcc")
+@pytest.mark.parametrize("name", ["experts_rows.hip", "experts_sort.hip", "experts_quantise.hip"])
+def test_no_arithmetic_in_doubles(name, tmp_path):
+    """Counts are integers and sums FP32: an FP64 instruction is a call that
+    resolved to another overload than was meant."""
+    out = str(tmp_path / "kernels.s")
+    r = subprocess.run([build.HIPCC, *build.COMMON_FLAGS, *build.EXTRA_FLAGS.get(name, []), "--cuda-device-only", "-S",
+                        os.path.join(CSRC, name), "-o", out], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    doubles = set(re.findall(r"\bv_\w+_f64\w*", open(out).read()))
+    assert not doubles, doubles
