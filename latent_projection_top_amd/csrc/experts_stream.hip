@@ -144,7 +144,7 @@ __device__ __forceinline__ void stream_part(const ProductArgs& p, const Item& it
     a = max(a, (uint32_t)__shfl_xor((int)a, 16));
     a = max(a, (uint32_t)__shfl_xor((int)a, 32));
     if (g == 0) shared.most[wave][m] = a;
-    __builtin_amdgcn_s_waitcnt(0xc07f);  // LDS only: the weights are still on their way
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");  // LDS only
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     a = 0;

@@ -50,3 +50,20 @@ def test_no_arithmetic_in_doubles(name, tmp_path):
     assert r.returncode == 0, r.stderr
     doubles = set(re.findall(r"\bv_\w+_f64\w*", open(out).read()))
     assert not doubles, doubles
+
+
+def test_bare_barriers_stand_between_fences():
+    """A barrier that orders no memory by itself: what was stored before it is
+    released, what is read after it acquired, in the source and not only in the
+    order that the compiler chose."""
+    found = 0
+    for name in sorted(os.listdir(CSRC)):
+        if not name.startswith("experts"):
+            continue
+        src = re.sub(r"//[^\n]*", "", open(os.path.join(CSRC, name)).read())
+        for m in re.finditer(r"__builtin_amdgcn_s_barrier\(\);", src):
+            found += 1
+            before, after = src[:m.start()].rstrip(), src[m.end():].lstrip()
+            assert re.search(r"__builtin_amdgcn_fence\(__ATOMIC_RELEASE, \"workgroup\"[^;]*\);$", before), name
+            assert re.match(r"__builtin_amdgcn_fence\(__ATOMIC_ACQUIRE, \"workgroup\"", after), name
+    assert found
