@@ -37,8 +37,9 @@
  *   linear8   z = (sum_k q[k] W[e][k, n]) * s * scale[e][n] + bias[e][n],
  *             y = act(z) + residual
  *   gated8    g and u are two such products without bias, h = act(g) * u
- * The integer sums are exact; what follows is FP32, rounded once. A row of
- * zeros has s = 0. A row that holds an infinity or NaN gives NaN throughout.
+ * The integer sums are exact; what follows is FP32, the sum times the channel's
+ * scale first, and rounded once. A row of zeros has s = 0. A row that holds an
+ * infinity or NaN gives NaN throughout.
  * Row p of y is of the expert whose range of `offsets` holds p, and of row
  * t = token[p] of x (token NULL: t = p). With `offsets` NULL, in a plan of one
  * expert, every row is that expert's. Rows at offsets[experts] and beyond are

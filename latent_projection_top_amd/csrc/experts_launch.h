@@ -105,7 +105,11 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
 //   kBrief where experts have few rows on average: weights that a few items read
 // again come from the caches (gated, in us, this and the next best: 1024 x 16 of
 // 896 experts of 512 x 256, 18 rows to each, 75 and 103; 96 x 16 of 64, 24 to
-// each, 2048 x 2048, 102 and 115; 30 to each 127 and 113).
+// each, 2048 x 2048, 102 and 115; 30 to each 127 and 113). An expert
+// of many rows among them becomes as many items, each of which reads its weights
+// (2048 rows of 112 experts of 3584 x 4096, dealt evenly, then with a quarter, half
+// and nine tenths of them one expert's: 310, 345, 369 and 417; by the rules below
+// 312, 340, 331 and 323).
 //   kFew where its modelled time in us is less than the tiles' (256 x 3584 x 7168:
 // 27 and 52; 40 x 2048 x 2048: 11 and 17; 333 x 6 of 40 experts of 1019 x 777: 25
 // and 33): a mid item's is mostly latency; many wait for each other, 256 at a
@@ -116,6 +120,9 @@ inline Lists lists_at(void* area, int64_t rows, int experts) {
 //   kApart where the weights are more than the last-level cache holds: streaming
 // the short experts' in a kernel of its own is worth a launch (112 experts of 3584
 // x 4096, 1.6 GB: 260 us, together 302; 33 of 253 x 320, 3 MB: 26 and 22).
+//   What counts is the rows that there is room for, of which the experts may keep
+// few (a rank's share; gated, 112 experts of 3584 x 4096 that keep 2048 of 16384 rows:
+// 334 us, by the way of 2048 rows 321; 1024 of 8192: 299 and 308).
 inline Way way_of(int64_t rows, int experts, int column_tiles, int blocks, bool offsets) {
   if (rows <= kStreamRows || (offsets && rows <= 24 * (int64_t)experts)) return kBrief;
   const int64_t mids = (rows + kMidRows - 1) / kMidRows + (offsets ? most_live(rows, experts) : 0);

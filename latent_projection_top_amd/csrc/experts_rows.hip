@@ -4,13 +4,15 @@
 //
 // A wave reads its token's places once, one to a lane, and takes the live ones
 // from there in order, eight at a time, so that eight rows' loads are in flight
-// together and a dropped choice costs nothing. Sums are FP32 in the order of
-// the choices. Sorted rows pass by the caches (a training step of 4096 x 16 x 3584
-// BF16: 460 us, else 530).
+// together and a dropped choice costs nothing. (Not in the wave that holds a row's
+// end inside a vector: it waits for each row's last values in turn.) Sums are
+// FP32 in the order of the choices. 16-bit sorted rows pass by the caches (a
+// training step of 4096 x 16 x 3584 BF16 in a graph: 460 us, else 530).
 //
-// That step: gather 103 us (4.9 TB/s; a copy reaches 5.2), combine 88 (5.7), its
-// backward pass 201 (4.8), gather's like combine. 8 x 16 x 7168: combine 4.3 us,
-// two dependent loads and a launch. A wave is a block of its own where rows are
+// That step's calls, traced one by one: gather 103 us (4.9 TB/s; a copy reaches
+// 5.2), combine 88 (5.7), its backward pass 204 (4.8), gather's like combine. 8 x 16 x
+// 7168: combine 4.4 us, a launch and three trips one after the other: places and
+// weights, the residual, rows. A wave is a block of its own where rows are
 // only read together (8 x 16 x 7168 with a row to a block 6.1 us, larger ones the
 // same); where a row's products are summed over its columns, a row is a block's.
 #include "experts_device.h"

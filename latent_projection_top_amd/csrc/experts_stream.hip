@@ -12,8 +12,8 @@
 // the last of them to arrive: integers, so in any order the same.
 //
 // Gated, 8 x 16 of 112 experts of 3584 x 4096: 33 us, 206 to 220 MB at 6.4 TB/s, more
-// than a copy reaches. 8 x 2048 x 7168: 7.2 us for 15 MB, a launch and two trips to
-// memory one after the other.
+// than a copy reaches. 8 x 2048 x 7168: 7.2 us for 15 MB, a launch and three trips to
+// memory one after the other: scales and bias, rows and weights, the residual.
 //
 // For few rows of short reductions (Fused) the kernel reads the rows as they are
 // and makes the integers itself: each wave those of its own blocks of the
@@ -85,8 +85,10 @@ __device__ __forceinline__ void stream_part(const ProductArgs& p, const Item& it
     u32x4 w[C], x[RT];
   };
   auto fetch = [&](Step& d, int i) __attribute__((always_inline)) {
+    // past the caches: no other block reads them (16 x 3584 x 65536: 56 us, like
+    // this 51) but those of the other items that an expert of many rows becomes
 #pragma unroll
-    for (int c = 0; c < C; ++c)  // past the caches: no other block reads them (16 x 3584 x 65536: 56 us, like this 51)
+    for (int c = 0; c < C; ++c)
       d.w[c] = __builtin_nontemporal_load(
           reinterpret_cast<const u32x4*>(w[c] + (int64_t)i * kWaves * kBlockBytes + (uint32_t)(16 * lane)));
     if constexpr (!Fused)
@@ -94,8 +96,10 @@ __device__ __forceinline__ void stream_part(const ProductArgs& p, const Item& it
       for (int r = 0; r < RT; ++r) d.x[r] = *reinterpret_cast<const u32x4*>(q[r] + (int64_t)i * kWaves * kBlockRed);
   };
 
-  // A thread ends four columns of one row. What it needs for that is on its way
-  // with the first operands, or after the last, where registers are short.
+  // A thread ends four columns of one row. What it needs for that is loaded before
+  // the first operands (and there before them: these loads are conditional, and the
+  // compiler waits where their branches meet), or after the last, where registers
+  // are short.
   constexpr int kQuads = 4 * C, kOut = Gated ? 2 * C : 4 * C;  // groups of 4 packed and output columns
   static_assert(16 * RT * kQuads <= kThreads, "");
   int row, col, quad;
@@ -125,7 +129,8 @@ __device__ __forceinline__ void stream_part(const ProductArgs& p, const Item& it
   Step d[kDepth];
   if constexpr (Fused) {
     // The rows' loads go out before the weights', behind which they would have
-    // to wait.
+    // to wait. (They are in one trip: the weights' are conditional as well, and have
+    // arrived where the magnitudes begin.)
     u32x4 v[kFusedSteps][2];
 #pragma unroll
     for (int i = 0; i < kFusedSteps; ++i)
